@@ -265,6 +265,108 @@ int lazy_mixed_attn(const lazy_attn_cfg *cfg, const lazy_prefill_batch *prefill,
                     const uint32_t *blk_meta, const uint16_t *k_pool, const uint16_t *v_pool, int num_blocks,
                     int *d_status, void *stream);
 
+/* ---- the pool in 8 bits: e4m3 codes with one scale per (block, KV head) ---- */
+
+/* A pool of half the size.  Element d of slot s of KV head h in block b stands for
+ *   K: k_scale[b][h] * e4m3(k_codes[b][h][s][d])      V: v_scale[b][h] * e4m3(v_codes[b][h][s][d])
+ * with e4m3 the 8-bit float of 4 exponent and 3 fraction bits (largest value 448, no
+ * infinities, codes 0x7F / 0xFF are NaN).  Keys carry RoPE at their local position and
+ * blk_meta, tables, positions and masks are those of the bf16 pool.  All pointers are device
+ * pointers to the caller's buffers; k_codes and v_codes are 16-byte aligned (LAZY_EINVAL).
+ * lazy_kv_write_q8 makes every scale a power of two; the attention entry points
+ * take any positive finite scale of at least 2^-126. */
+typedef struct lazy_q8_pool {
+    uint8_t *k_codes, *v_codes;   /* [num_blocks][Hkv][16][128] */
+    float *k_scale, *v_scale;     /* [num_blocks][Hkv] */
+    uint32_t *blk_meta;           /* [num_blocks], as for the bf16 pool */
+    int num_blocks;
+} lazy_q8_pool;
+
+/* Workspace for lazy_kv_write_q8: 0 up to 1024 tokens, else one row of 16 token indices and a
+ * metadata word per block of the pool.  The workspaces of this section are 16-byte aligned
+ * (LAZY_EINVAL), and calls that may overlap on the GPU need one each. */
+size_t lazy_kv_write_q8_workspace_bytes(const lazy_attn_cfg *cfg, int n_tok, int num_blocks);
+
+/* lazy_kv_write into an 8-bit pool.  With x = RoPE(k_raw[t][h][:], local_j[t]) for keys and
+ * x = v_raw[t][h][:] for values, every block that the call writes to gets, per head,
+ *   scale = max(old scale if blk_meta says that the block holds tokens,
+ *               the least power of two s >= 2^-126 with |x| <= 448 s over the call's tokens),
+ *   code  = e4m3(x / scale), rounded to nearest even,
+ * and where the scale grew, the earlier tokens' codes (slots below n_valid that the call does
+ * not write) become e4m3(value / scale): exact, but for values that fall below the new scale's
+ * normal range.  Other slots keep their codes.  Infinite elements are stored as +-448 scale and
+ * NaN as NaN; neither counts for the scale.  Tokens may come in any order; of two tokens with
+ * the same slot the later one in the call is stored.  Bad slots and misaligned indices are
+ * reported and skipped as by lazy_kv_write, and blk_meta is maintained the same way.  The result
+ * depends on the inputs alone (no order of execution enters it).  k_raw, v_raw: 8-byte
+ * aligned (LAZY_EINVAL).  A call must not overlap on the GPU with another that reads or writes
+ * the same blocks. */
+int lazy_kv_write_q8(const lazy_attn_cfg *cfg, const uint16_t *k_raw, const uint16_t *v_raw, int n_tok,
+                     const int32_t *slot, const int32_t *local_j, const lazy_q8_pool *pool, void *workspace,
+                     size_t ws_bytes, int *d_status, void *stream);
+
+/* Workspace for lazy_decode_attn_q8 on the current device; with_mass != 0 if it is called with
+ * a block_mass. */
+size_t lazy_decode_q8_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, int max_words, int with_mass);
+
+/* lazy_decode_attn over an 8-bit pool.  block_mass: NULL, or float32 with one accumulator per
+ * table word, indexed like `table`: accumulator w of request r gets
+ *   block_mass[w] += sum over query heads and over the word's visible keys of the softmax weight
+ * (so a request's accumulators grow by Hq in all per call, or by nothing if its query sees no
+ * key).  Sums are taken in a fixed order: the same inputs give the same bits.  Words past
+ * max_words of a request (LAZY_DSTATUS_BAD_TABLE) are ignored.  NaN or garbage in slots that
+ * the query does not see has no influence. */
+int lazy_decode_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_pos, int num_req,
+                        const uint32_t *table, const int32_t *table_indptr, int max_words,
+                        const lazy_q8_pool *pool, uint16_t *out, float *block_mass, void *workspace,
+                        size_t ws_bytes, int *d_status, void *stream);
+
+/* Workspace for lazy_prefill_attn_q8 on the current device; total_words: at least the table
+ * words of all requests together. */
+size_t lazy_prefill_q8_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, int total_q, int max_q,
+                                       int max_words, int total_words);
+
+/* lazy_prefill_attn over an 8-bit pool; the workspace is required (LAZY_EWORKSPACE).  Slots that
+ * no query of the request can see (unwritten ones, and keys behind its last query's position) have
+ * no influence, whatever they hold.  total_words <= 131072, num_req <= 65535 (LAZY_ERANGE). */
+int lazy_prefill_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *cu_q,
+                         const int32_t *q_pos0, int num_req, int total_q, int max_q, const uint32_t *table,
+                         const int32_t *table_indptr, int max_words, int total_words, const lazy_q8_pool *pool,
+                         uint16_t *out, void *workspace, size_t ws_bytes, int *d_status, void *stream);
+
+/* ---- eviction by accumulated attention weight ---- */
+
+/* Workspace for lazy_decode_attn_mass on the current device. */
+size_t lazy_decode_mass_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, int max_words);
+
+/* lazy_decode_attn (bf16 pool) that also adds each table word's attention weight to
+ * block_mass, as lazy_decode_attn_q8 does; block_mass must not be NULL. */
+int lazy_decode_attn_mass(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_pos, int num_req,
+                          const uint32_t *table, const int32_t *table_indptr, int max_words,
+                          const uint32_t *blk_meta, const uint16_t *k_pool, const uint16_t *v_pool,
+                          int num_blocks, uint16_t *out, float *block_mass, void *workspace, size_t ws_bytes,
+                          int *d_status, void *stream);
+
+/* Shortens every request's table to the words of largest accumulated weight.  Request r with n
+ * words keeps k = min(n, max(keep[r], 0)) of them, chosen in this order: the words among its
+ * first n_first and last n_last before all others, then by block_mass (largest first; NaN
+ * counts as +infinity and -0 as 0), then the lowest index.  The kept words stay in table order
+ * (their keys keep their positions: a gap in the table is legal).  keep: device int32 [num_req].
+ * Writes, for all requests one after the other:
+ *   table_out, mass_out: the kept words and their accumulators,
+ *   indptr_out [num_req + 1]: the new row pointers, from 0,
+ *   evicted: the dropped words, those of request r from table_indptr[r] - table_indptr[0] -
+ *            indptr_out[r] on (NULL: not written).
+ * Entries behind the last one written are left as they were.  The three outputs need room for
+ * the input's words; none may be an input (LAZY_EINVAL for equal pointers).  A request with
+ * more than max_words words sets LAZY_DSTATUS_BAD_TABLE; it is shortened all the same, with
+ * its words past max_words dropped (evicted).  A dropped word only leaves this request's table:
+ * the block itself is the caller's, and other requests may go on using it. */
+int lazy_evict_blocks(const uint32_t *table, const int32_t *table_indptr, int num_req, int max_words,
+                      const float *block_mass, const int32_t *keep, int n_first, int n_last,
+                      uint32_t *table_out, int32_t *indptr_out, float *mass_out, uint32_t *evicted,
+                      int *d_status, void *stream);
+
 /* ---- comparison paths (the position-aware alternative the pages argue against) ---- */
 
 /* Materialises position-adjusted keys ([ABS]: copying keys re-encoded for

@@ -108,6 +108,10 @@ float scale_log2(const lazy_attn_cfg *cfg) {
     return static_cast<float>(s * 1.4426950408889634);   // log2(e)
 }
 
+// Stand-ins for the pointers of a pool without blocks, never read.
+const uint32_t kNoMeta[1] = {0};
+const uint16_t kNoPool[8] = {0};
+
 int launch_rc(cudaError_t e) { return e == cudaSuccess ? LAZY_OK : LAZY_ECUDA; }
 
 size_t decode_ws(const lazy_attn_cfg *cfg, int num_req, int max_words) {
@@ -181,6 +185,65 @@ int decode_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *
         !make_blocks_map(&tv8, v_pool, num_blocks, p.hkv, 8))
         return LAZY_ECUDA;
     return launch_rc(launch_decode(tk, tv, tk8, tv8, p, plain, static_cast<cudaStream_t>(stream)));
+}
+
+bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// An 8-bit pool's fields (its pointers may be null when it has no blocks).
+int check_q8_pool(const lazy_q8_pool *pool) {
+    if (!pool || pool->num_blocks < 0) return LAZY_EINVAL;
+    if (static_cast<uint32_t>(pool->num_blocks) > LAZY_MAX_BLOCKS) return LAZY_ERANGE;
+    if (pool->num_blocks > 0 &&
+        (!pool->k_codes || !pool->v_codes || !pool->k_scale || !pool->v_scale || !pool->blk_meta))
+        return LAZY_EINVAL;
+    if (!aligned(pool->k_codes, 16) || !aligned(pool->v_codes, 16)) return LAZY_EINVAL;
+    return LAZY_OK;
+}
+
+// Workspace of the streaming decode: partial outputs, their (max, sum, reference), and with block
+// mass one log2 weight sum per (request, word, query head).
+size_t lane_ws(const lazy_attn_cfg *cfg, int num_req, int max_words, bool q8, bool mass, LanePlan &pl) {
+    const int G = cfg->num_q_heads / cfg->num_kv_heads;
+    pl = lane_plan(num_req, cfg->num_kv_heads, max_words, G, q8, mass, sm_count());
+    size_t n = static_cast<size_t>(pl.slots) * G * (128 * sizeof(float) + sizeof(float4));
+    if (mass) n += static_cast<size_t>(num_req) * max_words * cfg->num_q_heads * sizeof(float);
+    return n;
+}
+
+int lane_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_pos, int num_req,
+              const uint32_t *table, const int32_t *table_indptr, int max_words, const uint32_t *blk_meta,
+              const void *k, const void *v, const float *k_scale, const float *v_scale, int num_blocks,
+              uint16_t *out, float *mass, void *workspace, size_t ws_bytes, int *d_status, void *stream, bool q8) {
+    LaneParams p;
+    int rc = attn_common(cfg, p.a, num_req, table, table_indptr, max_words, num_blocks > 0 ? blk_meta : kNoMeta,
+                         num_blocks > 0 ? static_cast<const uint16_t *>(v) : kNoPool, num_blocks, out, d_status);
+    if (rc) return rc;
+    if (num_req == 0) return LAZY_OK;
+    if (!q_raw || !q_pos || (num_blocks > 0 && !k)) return LAZY_EINVAL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q_raw, 4)) return LAZY_EINVAL;
+    if (max_words == 0 || num_blocks == 0)
+        // nothing can be visible: every output row is zero
+        return launch_rc(cudaMemsetAsync(out, 0, static_cast<size_t>(num_req) * p.a.hq * 128 * 2,
+                                         static_cast<cudaStream_t>(stream)));
+    // one CTA per output row, and with block mass one per 32 words of a request
+    if (static_cast<int64_t>(num_req) * (p.a.hq + (mass ? max_words / 32 + 1 : 0)) > INT32_MAX) return LAZY_ERANGE;
+    LanePlan pl;
+    const size_t need = lane_ws(cfg, num_req, max_words, q8, mass != nullptr, pl);
+    if (!workspace || ws_bytes < need) return LAZY_EWORKSPACE;
+    if (!aligned(workspace, 16)) return LAZY_EINVAL;
+    p.a.q_raw = q_raw;
+    p.a.q_pos = q_pos;
+    const size_t rows = static_cast<size_t>(pl.slots) * p.a.group;
+    p.a.ws_acc = static_cast<float *>(workspace);
+    p.ws_ml = reinterpret_cast<float4 *>(p.a.ws_acc + rows * 128);
+    p.ws_lse = reinterpret_cast<float *>(p.ws_ml + rows);
+    p.mass = mass;
+    p.k = static_cast<const uint8_t *>(k);
+    p.v = static_cast<const uint8_t *>(v);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.warps_per_head = pl.warps_per_head;
+    return launch_rc(launch_decode_lane(p, q8, static_cast<cudaStream_t>(stream)));
 }
 
 int prefill_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *cu_q, const int32_t *q_pos0,
@@ -363,6 +426,171 @@ int lazy_mixed_attn(const lazy_attn_cfg *cfg, const lazy_prefill_batch *pf, cons
                            blk_meta, k_pool, rows, v_pool, num_blocks, dc->out, dc->workspace, dc->ws_bytes,
                            d_status, stream, false);
     return LAZY_OK;
+}
+
+size_t lazy_kv_write_q8_workspace_bytes(const lazy_attn_cfg *cfg, int n_tok, int num_blocks) {
+    if (check_cfg(cfg) != LAZY_OK || n_tok <= kQ8ScanTokens || num_blocks <= 0) return 0;
+    return q8_write_ws_bytes(num_blocks);
+}
+
+int lazy_kv_write_q8(const lazy_attn_cfg *cfg, const uint16_t *k_raw, const uint16_t *v_raw, int n_tok,
+                     const int32_t *slot, const int32_t *local_j, const lazy_q8_pool *pool, void *workspace,
+                     size_t ws_bytes, int *d_status, void *stream) {
+    int rc = check_cfg(cfg);
+    if (rc) return rc;
+    if (n_tok < 0) return LAZY_EINVAL;
+    rc = check_q8_pool(pool);
+    if (rc) return rc;
+    if (n_tok == 0) return LAZY_OK;
+    if (!k_raw || !v_raw || !slot || !local_j || !aligned(k_raw, 8) || !aligned(v_raw, 8)) return LAZY_EINVAL;
+    const size_t need = lazy_kv_write_q8_workspace_bytes(cfg, n_tok, pool->num_blocks);
+    if (need > 0 && (!workspace || ws_bytes < need)) return LAZY_EWORKSPACE;
+    if (need > 0 && !aligned(workspace, 16)) return LAZY_EINVAL;
+    Q8WriteParams p;
+    p.k_raw = k_raw;
+    p.v_raw = v_raw;
+    p.slot = slot;
+    p.local_j = local_j;
+    p.k_codes = pool->k_codes;
+    p.v_codes = pool->v_codes;
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
+    p.blk_meta = pool->blk_meta;
+    p.rows = need > 0 ? static_cast<uint32_t *>(workspace) : nullptr;
+    p.n_tok = n_tok;
+    p.hkv = cfg->num_kv_heads;
+    p.num_blocks = pool->num_blocks;
+    p.d_status = d_status;
+    fill_rope(p.rope, cfg);
+    return launch_rc(launch_kv_write_q8(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t lazy_decode_q8_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, int max_words, int with_mass) {
+    if (check_cfg(cfg) != LAZY_OK || num_req <= 0 || max_words <= 0) return 0;
+    LanePlan pl;
+    return lane_ws(cfg, num_req, max_words, true, with_mass != 0, pl);
+}
+
+int lazy_decode_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_pos, int num_req,
+                        const uint32_t *table, const int32_t *table_indptr, int max_words,
+                        const lazy_q8_pool *pool, uint16_t *out, float *block_mass, void *workspace,
+                        size_t ws_bytes, int *d_status, void *stream) {
+    int rc = check_cfg(cfg);
+    if (rc) return rc;
+    rc = check_q8_pool(pool);
+    if (rc) return rc;
+    return lane_impl(cfg, q_raw, q_pos, num_req, table, table_indptr, max_words, pool->blk_meta, pool->k_codes,
+                     pool->v_codes, pool->k_scale, pool->v_scale, pool->num_blocks, out, block_mass, workspace,
+                     ws_bytes, d_status, stream, true);
+}
+
+size_t lazy_decode_mass_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, int max_words) {
+    if (check_cfg(cfg) != LAZY_OK || num_req <= 0 || max_words <= 0) return 0;
+    LanePlan pl;
+    return lane_ws(cfg, num_req, max_words, false, true, pl);
+}
+
+int lazy_decode_attn_mass(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_pos, int num_req,
+                          const uint32_t *table, const int32_t *table_indptr, int max_words,
+                          const uint32_t *blk_meta, const uint16_t *k_pool, const uint16_t *v_pool,
+                          int num_blocks, uint16_t *out, float *block_mass, void *workspace, size_t ws_bytes,
+                          int *d_status, void *stream) {
+    int rc = check_cfg(cfg);
+    if (rc) return rc;
+    if (num_req > 0 && !block_mass) return LAZY_EINVAL;
+    return lane_impl(cfg, q_raw, q_pos, num_req, table, table_indptr, max_words, blk_meta, k_pool, v_pool, nullptr,
+                     nullptr, num_blocks, out, block_mass, workspace, ws_bytes, d_status, stream, false);
+}
+
+size_t lazy_prefill_q8_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, int total_q, int max_q, int max_words,
+                                       int total_words) {
+    if (check_cfg(cfg) != LAZY_OK || num_req <= 0 || max_q <= 0 || total_words < 0) return 0;
+    return q8_stage_bytes(total_words, cfg->num_kv_heads, num_req) +
+           lazy_prefill_workspace_bytes(cfg, num_req, total_q, max_q, max_words);
+}
+
+int lazy_prefill_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *cu_q,
+                         const int32_t *q_pos0, int num_req, int total_q, int max_q, const uint32_t *table,
+                         const int32_t *table_indptr, int max_words, int total_words, const lazy_q8_pool *pool,
+                         uint16_t *out, void *workspace, size_t ws_bytes, int *d_status, void *stream) {
+    int rc = check_cfg(cfg);
+    if (rc) return rc;
+    rc = check_q8_pool(pool);
+    if (rc) return rc;
+    if (num_req < 0 || total_q < 0 || max_q < 0 || max_words < 0 || total_words < 0) return LAZY_EINVAL;
+    if (num_req == 0 || total_q == 0 || max_q == 0) return LAZY_OK;
+    if (!q_raw || !cu_q || !q_pos0 || !table_indptr || !out || (max_words > 0 && !table)) return LAZY_EINVAL;
+    if (total_words > static_cast<int>(LAZY_MAX_BLOCKS) || num_req > 65535) return LAZY_ERANGE;
+    if (max_words == 0 || total_words == 0 || pool->num_blocks == 0)
+        return launch_rc(cudaMemsetAsync(out, 0, static_cast<size_t>(total_q) * cfg->num_q_heads * 128 * 2,
+                                         static_cast<cudaStream_t>(stream)));
+    const size_t stage = q8_stage_bytes(total_words, cfg->num_kv_heads, num_req);
+    if (!workspace || ws_bytes < lazy_prefill_q8_workspace_bytes(cfg, num_req, total_q, max_q, max_words, total_words))
+        return LAZY_EWORKSPACE;
+    if (!aligned(workspace, 16)) return LAZY_EINVAL;
+    Q8StageParams p;
+    p.k_codes = pool->k_codes;
+    p.v_codes = pool->v_codes;
+    p.k_scale = pool->k_scale;
+    p.v_scale = pool->v_scale;
+    p.blk_meta = pool->blk_meta;
+    p.table = table;
+    p.table_indptr = table_indptr;
+    p.cu_q = cu_q;
+    p.q_pos0 = q_pos0;
+    const int64_t rows = static_cast<int64_t>(total_words) * cfg->num_kv_heads * 16;
+    p.k_out = static_cast<uint16_t *>(workspace);
+    p.v_out = p.k_out + rows * 128;
+    p.table_out = reinterpret_cast<uint32_t *>(p.v_out + rows * 128);
+    p.meta_out = p.table_out + total_words;
+    p.indptr_out = reinterpret_cast<int32_t *>(p.meta_out + total_words);
+    p.num_req = num_req;
+    p.hkv = cfg->num_kv_heads;
+    p.num_blocks = pool->num_blocks;
+    p.max_words = max_words;
+    p.cap_words = total_words;
+    p.d_status = d_status;
+    fill_rope(p.rope, cfg);
+    rc = prefill_impl(cfg, q_raw, cu_q, q_pos0, num_req, total_q, max_q, p.table_out, p.indptr_out, max_words,
+                      p.meta_out, p.k_out, rows, p.v_out, total_words, out, static_cast<char *>(workspace) + stage,
+                      ws_bytes - stage, d_status, stream, !cfg->alibi_slopes, true);
+    if (rc) return rc;
+    rc = launch_rc(launch_q8_stage(p, static_cast<cudaStream_t>(stream)));
+    if (rc) return rc;
+    return prefill_impl(cfg, q_raw, cu_q, q_pos0, num_req, total_q, max_q, p.table_out, p.indptr_out, max_words,
+                        p.meta_out, p.k_out, rows, p.v_out, total_words, out, static_cast<char *>(workspace) + stage,
+                        ws_bytes - stage, d_status, stream, !cfg->alibi_slopes);
+}
+
+int lazy_evict_blocks(const uint32_t *table, const int32_t *table_indptr, int num_req, int max_words,
+                      const float *block_mass, const int32_t *keep, int n_first, int n_last,
+                      uint32_t *table_out, int32_t *indptr_out, float *mass_out, uint32_t *evicted,
+                      int *d_status, void *stream) {
+    if (num_req < 0 || max_words < 0 || n_first < 0 || n_last < 0) return LAZY_EINVAL;
+    if (!indptr_out || (num_req > 0 && (!table_indptr || !keep))) return LAZY_EINVAL;
+    if (num_req == 0) return launch_rc(cudaMemsetAsync(indptr_out, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)));
+    if (max_words > 0 && (!block_mass || !table_out || !mass_out)) return LAZY_EINVAL;
+    if ((max_words > 0 || evicted) && !table) return LAZY_EINVAL;
+    const void *in[4] = {table, table_indptr, block_mass, keep};
+    const void *outs[4] = {table_out, indptr_out, mass_out, evicted};
+    for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j)
+            if (outs[i] && (outs[i] == in[j] || (i != j && outs[i] == outs[j]))) return LAZY_EINVAL;
+    EvictParams p;
+    p.table = table;
+    p.table_indptr = table_indptr;
+    p.mass = block_mass;
+    p.keep = keep;
+    p.table_out = table_out;
+    p.evicted = evicted;
+    p.indptr_out = indptr_out;
+    p.mass_out = mass_out;
+    p.num_req = num_req;
+    p.max_words = max_words;
+    p.n_first = n_first;
+    p.n_last = n_last;
+    p.d_status = d_status;
+    return launch_rc(launch_evict(p, static_cast<cudaStream_t>(stream)));
 }
 
 int lazy_materialize_k(const lazy_attn_cfg *cfg, const uint32_t *table, int total_words, const uint32_t *blk_meta,

@@ -1,0 +1,176 @@
+// evict.cu -- each request's table cut to its words of largest accumulated attention weight.
+//
+// Order of request r's n words: protected ones (the first n_first and last n_last) before all
+// others, then by weight, then by index; the first k = min(n, max(keep, 0)) stay, in table order.
+// Weights become 32-bit keys of the same order; the k-th key is found by radix selection (8 bits a
+// pass, stopping as soon as the bin that holds it is taken whole), ties at that key go to the lowest
+// indices, and one ordered compaction writes survivors and evicted words.  A CTA takes one request:
+// keys are read once and stay in shared memory.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace lazy {
+
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kSmemKeys = 49152;   // words of a request whose keys stay in shared memory
+
+__device__ __forceinline__ uint32_t key_of(float m) {
+    if (m != m) m = INFINITY;
+    m += 0.f;   // -0 as 0
+    const uint32_t u = __float_as_uint(m);
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, int smem_keys) {
+    extern __shared__ uint32_t keys[];
+    __shared__ int hist[256];
+    __shared__ int red[kWarps], cnt_gt[kWarps], cnt_eq[kWarps];
+    __shared__ int sel_bin, sel_above, sel_count;
+    const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int base = p.table_indptr[0];
+    const int beg = p.table_indptr[r], n_all = p.table_indptr[r + 1] - beg;
+    const int n = max(0, min(n_all, p.max_words));
+    if (tid == 0 && n_all > p.max_words) set_status(p.d_status, LAZY_DSTATUS_BAD_TABLE);
+    auto kept_of = [&](int q) {
+        const int m = p.table_indptr[q + 1] - p.table_indptr[q];
+        return max(0, min(min(m, p.max_words), p.keep[q]));
+    };
+    const int k = kept_of(r);
+    // ---- where this request's survivors go
+    int before = 0;
+    for (int q = tid; q < r; q += kThreads) before += kept_of(q);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) before += __shfl_xor_sync(0xffffffffu, before, x);
+    if (lane == 0) red[warp] = before;
+    // ---- keys
+    const float *mass = p.mass + beg;
+    for (int i = tid; i < min(n, smem_keys); i += kThreads) keys[i] = key_of(mass[i]);
+    __syncthreads();
+    int out = red[lane];
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) out += __shfl_xor_sync(0xffffffffu, out, x);
+    if (tid == 0) {
+        if (r == 0) p.indptr_out[0] = 0;
+        p.indptr_out[r + 1] = out + k;
+    }
+    auto key = [&](int i) { return i < smem_keys ? keys[i] : key_of(mass[i]); };
+    // ---- the class that the cut goes through: the protected words if they alone are too many, else the others
+    const int nf = min(p.n_first, n), nl = min(p.n_last, n - nf), n_prot = nf + nl;
+    auto is_prot = [&](int i) { return i < nf || i >= n - nl; };
+    const bool cut_prot = k < n_prot;
+    int need = cut_prot ? k : k - n_prot;
+    const int n_class = cut_prot ? n_prot : n - n_prot;
+    const bool none = need == 0, all = need == n_class;
+    uint32_t prefix = 0u, mask = 0u;
+    bool whole = false;   // every key of the class with (key & mask) == prefix stays
+    if (!none && !all) {
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            if (tid < 256) hist[tid] = 0;
+            __syncthreads();
+            for (int i = tid; i < n; i += kThreads) {
+                const uint32_t u = key(i);
+                if (is_prot(i) == cut_prot && (u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1);
+            }
+            __syncthreads();
+            if (warp == 0) {
+                // lane l: bins 255 - 8 l downwards
+                int c[8], s = 0;
+#pragma unroll
+                for (int x = 0; x < 8; ++x) s += c[x] = hist[255 - 8 * lane - x];
+                int inc = s;
+#pragma unroll
+                for (int x = 1; x < 32; x <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, inc, x);
+                    if (lane >= x) inc += y;
+                }
+                int above = inc - s;
+                if (above < need && need <= inc) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        if (above < need && need <= above + c[x]) {
+                            sel_bin = 255 - 8 * lane - x;
+                            sel_above = above;
+                            sel_count = c[x];
+                        }
+                        above += c[x];
+                    }
+                }
+            }
+            __syncthreads();
+            prefix |= static_cast<uint32_t>(sel_bin) << shift;
+            mask |= 255u << shift;
+            need -= sel_above;
+            if (need == sel_count) {
+                whole = true;
+                break;
+            }
+            __syncthreads();
+        }
+    }
+    // 2: stays, 1: stays if among the first `need` of its kind, 0: goes
+    auto verdict = [&](int i) {
+        if (is_prot(i) != cut_prot) return cut_prot ? 0 : 2;
+        if (none || all) return all ? 2 : 0;
+        const uint32_t u = key(i) & mask;
+        return u > prefix ? 2 : u < prefix ? 0 : whole ? 2 : 1;
+    };
+    // ---- ordered compaction: a warp takes a run of words
+    const int seg = ((n + kThreads - 1) / kThreads) * 32;
+    const int w0 = min(n, warp * seg), w1 = min(n, w0 + seg);
+    int gt = 0, eq = 0;
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int v = i0 + lane < w1 ? verdict(i0 + lane) : 0;
+        gt += __popc(__ballot_sync(0xffffffffu, v == 2));
+        eq += __popc(__ballot_sync(0xffffffffu, v == 1));
+    }
+    if (lane == 0) {
+        cnt_gt[warp] = gt;
+        cnt_eq[warp] = eq;
+    }
+    __syncthreads();
+    int gt_before = lane < warp ? cnt_gt[lane] : 0, eq_before = lane < warp ? cnt_eq[lane] : 0;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) {
+        gt_before += __shfl_xor_sync(0xffffffffu, gt_before, x);
+        eq_before += __shfl_xor_sync(0xffffffffu, eq_before, x);
+    }
+    int stay = gt_before + min(eq_before, need);   // survivors before this position
+    const uint32_t lower = (1u << lane) - 1u;
+    const int gone0 = beg - base - out;
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int i = i0 + lane;
+        const bool in = i < w1;
+        const int v = in ? verdict(i) : 0;
+        const uint32_t em = __ballot_sync(0xffffffffu, v == 1);
+        const bool st = v == 2 || (v == 1 && eq_before + __popc(em & lower) < need);
+        const uint32_t sm = __ballot_sync(0xffffffffu, st);
+        if (in) {
+            const uint32_t w = p.table[beg + i];
+            const int pos = stay + __popc(sm & lower);
+            if (st) {
+                p.table_out[out + pos] = w;
+                p.mass_out[out + pos] = mass[i];
+            } else if (p.evicted) {
+                p.evicted[gone0 + i - pos] = w;
+            }
+        }
+        stay += __popc(sm);
+        eq_before += __popc(em);
+    }
+    if (p.evicted)
+        for (int i = n + tid; i < n_all; i += kThreads) p.evicted[gone0 + i - k] = p.table[beg + i];
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t s) {
+    const int smem_keys = p.max_words < kSmemKeys ? p.max_words : kSmemKeys;
+    cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKeys * 4);
+    if (e != cudaSuccess) return e;
+    evict_kernel<<<p.num_req, kThreads, smem_keys * 4, s>>>(p, smem_keys);
+    return cudaGetLastError();
+}
+
+}  // namespace lazy

@@ -119,4 +119,74 @@ inline size_t prefill_qprep_bytes(long long units) {
     return static_cast<size_t>(units) * kPrefillRows * 128 * sizeof(uint16_t);
 }
 
+// ---- the 8-bit pool, block mass and eviction ----
+
+struct Q8WriteParams {
+    const uint16_t *k_raw, *v_raw;
+    const int32_t *slot, *local_j;
+    uint8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    uint32_t *blk_meta;
+    uint32_t *rows;              // large calls: [num_blocks][16] token index + 1 per slot, [num_blocks] metadata; or null
+    int n_tok, hkv, num_blocks;
+    int *d_status;
+    RopeTableHost rope;
+};
+constexpr int kQ8ScanTokens = 1024;   // up to this many tokens a write finds each block's tokens by scanning the call
+inline size_t q8_write_ws_bytes(int num_blocks) { return static_cast<size_t>(num_blocks) * (16 + 1) * 4; }
+cudaError_t launch_kv_write_q8(const Q8WriteParams &p, cudaStream_t s);
+
+// Streaming decode (decode_lane.cu) over the 8-bit pool, or over the bf16 pool with block mass.
+// a.ws_acc: partial outputs [slot][G][128]; ws_ml: per partial (running max, sum, output
+// reference, 0) [slot][G]; ws_lse: log2 of each word's weight sum [num_req][max_words][Hq].
+struct LaneParams {
+    AttnParams a;
+    const uint8_t *k, *v;            // codes, or bf16 pools
+    const float *k_scale, *v_scale;  // null for bf16 pools
+    float4 *ws_ml;
+    float *ws_lse;
+    float *mass;                     // null: no accumulators
+    int warps_per_head;              // warps that share one KV head's words
+};
+struct LanePlan {
+    int warps_per_head;
+    int64_t slots;                   // partials in the workspace
+};
+LanePlan lane_plan(int num_req, int hkv, int max_words, int group, bool q8, bool mass, int sms);
+cudaError_t launch_decode_lane(const LaneParams &p, bool q8, cudaStream_t s);
+
+// Prefill over the 8-bit pool: the words of `num_req` requests as bf16 keys (rotated to their
+// absolute positions) and values, one row of the staging buffers per word, with a table and
+// metadata that name those rows.
+struct Q8StageParams {
+    const uint8_t *k_codes, *v_codes;
+    const float *k_scale, *v_scale;
+    const uint32_t *blk_meta, *table;
+    const int32_t *table_indptr, *cu_q, *q_pos0;
+    uint16_t *k_out, *v_out;         // [cap_words][Hkv][16][128]
+    uint32_t *table_out, *meta_out;  // [cap_words]
+    int32_t *indptr_out;             // [num_req + 1]
+    int num_req, hkv, num_blocks, max_words, cap_words;
+    int *d_status;
+    RopeTableHost rope;
+};
+inline size_t q8_stage_bytes(int total_words, int hkv, int num_req) {
+    const size_t n = static_cast<size_t>(total_words) * (static_cast<size_t>(hkv) * 8192 + 8) + (static_cast<size_t>(num_req) + 1) * 4;
+    return (n + 1023) / 1024 * 1024;
+}
+cudaError_t launch_q8_stage(const Q8StageParams &p, cudaStream_t s);
+
+struct EvictParams {
+    const uint32_t *table;
+    const int32_t *table_indptr;
+    const float *mass;
+    const int32_t *keep;
+    uint32_t *table_out, *evicted;
+    int32_t *indptr_out;
+    float *mass_out;
+    int num_req, max_words, n_first, n_last;
+    int *d_status;
+};
+cudaError_t launch_evict(const EvictParams &p, cudaStream_t s);
+
 }  // namespace lazy

@@ -29,6 +29,9 @@ EXPORTED = [
     "lazy_cache_create", "lazy_cache_destroy", "lazy_cache_access", "lazy_cache_contains", "lazy_cache_stats",
     "lazy_mixed_attn", "lazy_rope_theta", "lazy_rope_theta_llama31", "lazy_alibi_slopes",
     "lazy_debug_bounded_wait",
+    "lazy_kv_write_q8_workspace_bytes", "lazy_kv_write_q8", "lazy_decode_q8_workspace_bytes", "lazy_decode_attn_q8",
+    "lazy_prefill_q8_workspace_bytes", "lazy_prefill_attn_q8", "lazy_decode_mass_workspace_bytes",
+    "lazy_decode_attn_mass", "lazy_evict_blocks",
 ]
 
 
@@ -93,6 +96,15 @@ class DecodeBatch(ctypes.Structure):
                 ("max_words", _i), ("out", _vp), ("workspace", _vp), ("ws_bytes", _sz)]
 
 
+class LazyQ8Pool(ctypes.Structure):
+    """lazy_q8_pool: device pointers of an 8-bit pool."""
+    _fields_ = [("k_codes", _vp), ("v_codes", _vp), ("k_scale", _vp), ("v_scale", _vp), ("blk_meta", _vp),
+                ("num_blocks", _i)]
+
+
+_q8p = ctypes.POINTER(LazyQ8Pool)
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with `python -m position_agnostic_paged_b200.build` "
@@ -123,6 +135,17 @@ def _load():
                                          ctypes.c_double, _vp]),
         "lazy_alibi_slopes": (_i, [_i, _vp]),
         "lazy_debug_bounded_wait": (_i, [ctypes.c_uint32, _i, _vp, _vp, _vp]),
+        "lazy_kv_write_q8_workspace_bytes": (_sz, [_cfgp, _i, _i]),
+        "lazy_kv_write_q8": (_i, [_cfgp, _vp, _vp, _i, _vp, _vp, _q8p, _vp, _sz, _vp, _vp]),
+        "lazy_decode_q8_workspace_bytes": (_sz, [_cfgp, _i, _i, _i]),
+        "lazy_decode_attn_q8": (_i, [_cfgp, _vp, _vp, _i, _vp, _vp, _i, _q8p, _vp, _vp, _vp, _sz, _vp, _vp]),
+        "lazy_prefill_q8_workspace_bytes": (_sz, [_cfgp, _i, _i, _i, _i, _i]),
+        "lazy_prefill_attn_q8": (_i, [_cfgp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _q8p, _vp, _vp, _sz, _vp,
+                                      _vp]),
+        "lazy_decode_mass_workspace_bytes": (_sz, [_cfgp, _i, _i]),
+        "lazy_decode_attn_mass": (_i, [_cfgp, _vp, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp,
+                                       _vp]),
+        "lazy_evict_blocks": (_i, [_vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
         "lazy_cache_create": (_vp, [_i64]),
         "lazy_cache_destroy": (None, [_vp]),
         "lazy_cache_access": (_i, [_vp, ctypes.c_uint64, ctypes.c_int32, _vp]),
@@ -327,6 +350,206 @@ def decode_attn_noalloc(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: 
         ctypes.byref(c), _ptr(q_raw), _ptr(q_pos), int(q_pos.numel()), _ptr(table), _ptr(table_indptr),
         int(max_words), _ptr(blk_meta), _ptr(k_pool), _ptr(v_pool), int(k_pool.shape[0]), _ptr(out),
         _ptr(d_status), _stream(stream)))
+
+
+# ---- the 8-bit pool, block mass and eviction.  These calls check what the C side cannot see: types
+# (two-byte and four-byte elements would be read as something else), contiguity, shapes and the device.
+
+def _take(name: str, t, kinds: tuple, shape: tuple | None = None):
+    if str(t.dtype)[6:] not in kinds:
+        raise ValueError(f"{name} must be {' or '.join(kinds)}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+
+
+_WORD = ("int32", "uint32")
+
+
+def _on(ts, stream):
+    """(device guard, stream handle) for a launch on the tensors' device, which need not be the current one."""
+    import contextlib
+
+    import torch
+    dev = {t.device for t in ts if t is not None}
+    if len(dev) != 1:
+        raise ValueError("all tensors must be on one device")
+    dev = dev.pop()
+    if dev.type != "cuda":
+        raise ValueError("all tensors must be CUDA tensors")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    guard = contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return guard, _stream(stream)
+
+
+class Q8Pool:
+    """A pool of e4m3 codes with one float32 scale per (block, KV head) (lazy_q8_pool).
+
+    k_codes, v_codes: one-byte elements [num_blocks, Hkv, 16, 128]; k_scale, v_scale: float32
+    [num_blocks, Hkv]; blk_meta: int32 [num_blocks].  The tensors stay the caller's."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale, blk_meta):
+        nb, hkv = int(k_codes.shape[0]), int(k_codes.shape[1])
+        for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+            _take(name, t, ("uint8", "float8_e4m3fn"), (nb, hkv, 16, 128))
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _take(name, t, ("float32",), (nb, hkv))
+        _take("blk_meta", blk_meta, _WORD, (nb,))
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale, self.blk_meta = k_codes, v_codes, k_scale, v_scale, blk_meta
+        self.num_blocks, self.num_kv_heads = nb, hkv
+
+    @classmethod
+    def empty(cls, num_blocks: int, num_kv_heads: int, device="cuda") -> "Q8Pool":
+        """A pool whose blocks hold no tokens."""
+        import torch
+        codes = lambda: torch.zeros(num_blocks, num_kv_heads, 16, 128, dtype=torch.uint8, device=device)   # noqa: E731
+        scale = lambda: torch.ones(num_blocks, num_kv_heads, dtype=torch.float32, device=device)           # noqa: E731
+        return cls(codes(), codes(), scale(), scale(), torch.zeros(num_blocks, dtype=torch.int32, device=device))
+
+    def c(self) -> LazyQ8Pool:
+        return LazyQ8Pool(_ptr(self.k_codes), _ptr(self.v_codes), _ptr(self.k_scale), _ptr(self.v_scale),
+                          _ptr(self.blk_meta), self.num_blocks)
+
+
+def _heads(cfg: Cfg, pool: Q8Pool) -> None:
+    if pool.num_kv_heads != cfg.num_kv_heads:
+        raise ValueError(f"the pool has {pool.num_kv_heads} KV heads, the configuration {cfg.num_kv_heads}")
+
+
+def kv_write_q8_workspace_bytes(cfg: Cfg, n_tok: int, num_blocks: int) -> int:
+    c = cfg.c()
+    return int(_lib.lazy_kv_write_q8_workspace_bytes(ctypes.byref(c), int(n_tok), int(num_blocks)))
+
+
+def kv_write_q8(cfg: Cfg, k_raw, v_raw, slot, local_j, pool: Q8Pool, workspace=None, d_status=None, stream=None):
+    """New tokens into an 8-bit pool (lazy_kv_write_q8): scales, codes and metadata of the blocks they fall in."""
+    c, q, n = cfg.c(), pool.c(), int(slot.numel())
+    _heads(cfg, pool)
+    for name, t in (("k_raw", k_raw), ("v_raw", v_raw)):
+        _take(name, t, ("bfloat16",), (n, cfg.num_kv_heads, 128))
+    for name, t in (("slot", slot), ("local_j", local_j)):
+        _take(name, t, ("int32",))
+    if local_j.numel() != n:
+        raise ValueError("slot and local_j must have one element per token")
+    guard, st = _on((k_raw, v_raw, slot, local_j, pool.k_codes, workspace, d_status), stream)
+    with guard:
+        _check("lazy_kv_write_q8", _lib.lazy_kv_write_q8(
+            ctypes.byref(c), _ptr(k_raw), _ptr(v_raw), n, _ptr(slot), _ptr(local_j), ctypes.byref(q),
+            _ptr(workspace), _nbytes(workspace), _ptr(d_status), st))
+
+
+def _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass):
+    n = int(q_pos.numel())
+    _take("q_raw", q_raw, ("bfloat16",), (n, cfg.num_q_heads, 128))
+    _take("out", out, ("bfloat16",), (n, cfg.num_q_heads, 128))
+    _take("q_pos", q_pos, ("int32",))
+    _take("table", table, _WORD)
+    _take("table_indptr", table_indptr, ("int32",))
+    if table_indptr.numel() != n + 1:
+        raise ValueError("table_indptr must have one element more than q_pos")
+    if block_mass is not None:
+        _take("block_mass", block_mass, ("float32",))
+        if block_mass.numel() != table.numel():
+            raise ValueError("block_mass must have one element per table word")
+    return n
+
+
+def decode_q8_workspace_bytes(cfg: Cfg, num_req: int, max_words: int, with_mass: bool = False) -> int:
+    c = cfg.c()
+    return int(_lib.lazy_decode_q8_workspace_bytes(ctypes.byref(c), int(num_req), int(max_words), 1 if with_mass else 0))
+
+
+def decode_attn_q8(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: int, pool: Q8Pool, out, workspace,
+                   block_mass=None, d_status=None, stream=None):
+    """One decode step over an 8-bit pool (lazy_decode_attn_q8).  block_mass: optional float32
+    accumulators, one per table word, that grow by the words' attention weights."""
+    c, q = cfg.c(), pool.c()
+    _heads(cfg, pool)
+    n = _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass)
+    guard, st = _on((q_raw, q_pos, table, table_indptr, pool.k_codes, out, workspace, block_mass, d_status), stream)
+    with guard:
+        _check("lazy_decode_attn_q8", _lib.lazy_decode_attn_q8(
+            ctypes.byref(c), _ptr(q_raw), _ptr(q_pos), n, _ptr(table), _ptr(table_indptr), int(max_words),
+            ctypes.byref(q), _ptr(out), _ptr(block_mass), _ptr(workspace), _nbytes(workspace), _ptr(d_status), st))
+
+
+def decode_mass_workspace_bytes(cfg: Cfg, num_req: int, max_words: int) -> int:
+    c = cfg.c()
+    return int(_lib.lazy_decode_mass_workspace_bytes(ctypes.byref(c), int(num_req), int(max_words)))
+
+
+def decode_attn_mass(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: int, blk_meta, k_pool, v_pool, out,
+                     block_mass, workspace, d_status=None, stream=None):
+    """decode_attn over the bf16 pool that also adds each table word's attention weight to block_mass
+    (lazy_decode_attn_mass)."""
+    c = cfg.c()
+    n = _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass)
+    nb = int(k_pool.shape[0])
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        _take(name, t, ("bfloat16",), (nb, cfg.num_kv_heads, 16, 128))
+    _take("blk_meta", blk_meta, _WORD, (nb,))
+    guard, st = _on((q_raw, q_pos, table, table_indptr, blk_meta, k_pool, v_pool, out, block_mass, workspace, d_status),
+                    stream)
+    with guard:
+        _check("lazy_decode_attn_mass", _lib.lazy_decode_attn_mass(
+            ctypes.byref(c), _ptr(q_raw), _ptr(q_pos), n, _ptr(table), _ptr(table_indptr), int(max_words),
+            _ptr(blk_meta), _ptr(k_pool), _ptr(v_pool), nb, _ptr(out), _ptr(block_mass), _ptr(workspace),
+            _nbytes(workspace), _ptr(d_status), st))
+
+
+def prefill_q8_workspace_bytes(cfg: Cfg, num_req: int, total_q: int, max_q: int, max_words: int,
+                               total_words: int) -> int:
+    c = cfg.c()
+    return int(_lib.lazy_prefill_q8_workspace_bytes(ctypes.byref(c), int(num_req), int(total_q), int(max_q),
+                                                    int(max_words), int(total_words)))
+
+
+def prefill_attn_q8(cfg: Cfg, q_raw, cu_q, q_pos0, max_q: int, table, table_indptr, max_words: int, pool: Q8Pool,
+                    out, workspace, d_status=None, stream=None):
+    """Causal prefill over an 8-bit pool (lazy_prefill_attn_q8)."""
+    c, q = cfg.c(), pool.c()
+    _heads(cfg, pool)
+    n, total_q = int(q_pos0.numel()), int(q_raw.shape[0])
+    _take("q_raw", q_raw, ("bfloat16",), (total_q, cfg.num_q_heads, 128))
+    _take("out", out, ("bfloat16",), (total_q, cfg.num_q_heads, 128))
+    for name, t in (("cu_q", cu_q), ("q_pos0", q_pos0), ("table_indptr", table_indptr)):
+        _take(name, t, ("int32",))
+    _take("table", table, _WORD)
+    if cu_q.numel() != n + 1 or table_indptr.numel() != n + 1:
+        raise ValueError("cu_q and table_indptr must have one element more than q_pos0")
+    guard, st = _on((q_raw, cu_q, q_pos0, table, table_indptr, pool.k_codes, out, workspace, d_status), stream)
+    with guard:
+        _check("lazy_prefill_attn_q8", _lib.lazy_prefill_attn_q8(
+            ctypes.byref(c), _ptr(q_raw), _ptr(cu_q), _ptr(q_pos0), n, total_q, int(max_q), _ptr(table),
+            _ptr(table_indptr), int(max_words), int(table.numel()), ctypes.byref(q), _ptr(out), _ptr(workspace),
+            _nbytes(workspace), _ptr(d_status), st))
+
+
+def evict_blocks(table, table_indptr, max_words: int, block_mass, keep, n_first: int, n_last: int, table_out,
+                 indptr_out, mass_out, evicted=None, d_status=None, stream=None):
+    """Shortens every request's table to the keep[r] words of largest accumulated weight
+    (lazy_evict_blocks); the first n_first and last n_last words of a request go last."""
+    n, words = int(keep.numel()), int(table.numel())
+    for name, t in (("table", table), ("table_out", table_out), ("evicted", evicted)):
+        if t is not None:
+            _take(name, t, _WORD)
+    for name, t in (("block_mass", block_mass), ("mass_out", mass_out)):
+        _take(name, t, ("float32",))
+    for name, t in (("table_indptr", table_indptr), ("indptr_out", indptr_out), ("keep", keep)):
+        _take(name, t, ("int32",))
+    if table_indptr.numel() != n + 1 or indptr_out.numel() < n + 1:
+        raise ValueError("table_indptr and indptr_out must have one element more than keep")
+    if block_mass.numel() != words:
+        raise ValueError("block_mass must have one element per table word")
+    if min([words] + [t.numel() for t in (table_out, mass_out, evicted) if t is not None]) < words:
+        raise ValueError("table_out, mass_out and evicted need room for every table word")
+    guard, st = _on((table, table_indptr, block_mass, keep, table_out, indptr_out, mass_out, evicted, d_status), stream)
+    with guard:
+        _check("lazy_evict_blocks", _lib.lazy_evict_blocks(
+            _ptr(table), _ptr(table_indptr), n, int(max_words), _ptr(block_mass), _ptr(keep), int(n_first),
+            int(n_last), _ptr(table_out), _ptr(indptr_out), _ptr(mass_out), _ptr(evicted), _ptr(d_status), st))
 
 
 class BlockCache:
