@@ -321,18 +321,21 @@ int lazy_decode_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const i
                         const lazy_q8_pool *pool, uint16_t *out, float *block_mass, void *workspace,
                         size_t ws_bytes, int *d_status, void *stream);
 
-/* Workspace for lazy_prefill_attn_q8 on the current device; total_words: at least the table
- * words of all requests together. */
+/* Workspace for lazy_prefill_attn_q8 on the current device: the query tiles, and partial results of
+ * units that are split over their words (see lazy_prefill_workspace_bytes; total_q and total_words,
+ * the table words of all requests, do not enter it at present). */
 size_t lazy_prefill_q8_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, int total_q, int max_q,
                                        int max_words, int total_words);
 
-/* lazy_prefill_attn over an 8-bit pool; the workspace is required (LAZY_EWORKSPACE).  Slots that
- * no query of the request can see (unwritten ones, and keys behind its last query's position) have
- * no influence, whatever they hold.  total_words <= 131072, num_req <= 65535 (LAZY_ERANGE). */
+/* lazy_prefill_attn over an 8-bit pool.  The workspace is required (LAZY_EWORKSPACE).  Slots that
+ * no query of the request sees (unwritten ones, and keys behind its last query's position) have
+ * no influence, whatever they hold.  Words past max_words of a request (LAZY_DSTATUS_BAD_TABLE) are
+ * ignored.  q_raw: 8-byte, out: 16-byte aligned (LAZY_EINVAL); num_req <= 65535 and at most 2^22
+ * units of 256 query rows (LAZY_ERANGE). */
 int lazy_prefill_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *cu_q,
                          const int32_t *q_pos0, int num_req, int total_q, int max_q, const uint32_t *table,
-                         const int32_t *table_indptr, int max_words, int total_words, const lazy_q8_pool *pool,
-                         uint16_t *out, void *workspace, size_t ws_bytes, int *d_status, void *stream);
+                         const int32_t *table_indptr, int max_words, const lazy_q8_pool *pool, uint16_t *out,
+                         void *workspace, size_t ws_bytes, int *d_status, void *stream);
 
 /* ---- eviction by accumulated attention weight ---- */
 

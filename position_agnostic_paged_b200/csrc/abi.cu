@@ -200,6 +200,12 @@ int check_q8_pool(const lazy_q8_pool *pool) {
     return LAZY_OK;
 }
 
+// Work units of a prefill: 256 query rows of one KV head of one request.
+int64_t prefill_units(const lazy_attn_cfg *cfg, int num_req, int max_q) {
+    const int64_t rows = static_cast<int64_t>(max_q) * (cfg->num_q_heads / cfg->num_kv_heads);
+    return (rows + kPrefillRows - 1) / kPrefillRows * cfg->num_kv_heads * num_req;
+}
+
 // Workspace of the streaming decode: partial outputs, their (max, sum, reference), and with block
 // mass one log2 weight sum per (request, word, query head).
 size_t lane_ws(const lazy_attn_cfg *cfg, int num_req, int max_words, bool q8, bool mass, LanePlan &pl) {
@@ -504,62 +510,50 @@ int lazy_decode_attn_mass(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const
 
 size_t lazy_prefill_q8_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, int total_q, int max_q, int max_words,
                                        int total_words) {
-    if (check_cfg(cfg) != LAZY_OK || num_req <= 0 || max_q <= 0 || total_words < 0) return 0;
-    return q8_stage_bytes(total_words, cfg->num_kv_heads, num_req) +
-           lazy_prefill_workspace_bytes(cfg, num_req, total_q, max_q, max_words);
+    (void)total_q;
+    (void)total_words;
+    if (check_cfg(cfg) != LAZY_OK || num_req <= 0 || max_q <= 0 || max_words < 0) return 0;
+    return q8_prefill_ws_bytes(prefill_units(cfg, num_req, max_q), max_words, sm_count());
 }
 
 int lazy_prefill_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *cu_q,
                          const int32_t *q_pos0, int num_req, int total_q, int max_q, const uint32_t *table,
-                         const int32_t *table_indptr, int max_words, int total_words, const lazy_q8_pool *pool,
-                         uint16_t *out, void *workspace, size_t ws_bytes, int *d_status, void *stream) {
+                         const int32_t *table_indptr, int max_words, const lazy_q8_pool *pool, uint16_t *out,
+                         void *workspace, size_t ws_bytes, int *d_status, void *stream) {
     int rc = check_cfg(cfg);
     if (rc) return rc;
     rc = check_q8_pool(pool);
     if (rc) return rc;
-    if (num_req < 0 || total_q < 0 || max_q < 0 || max_words < 0 || total_words < 0) return LAZY_EINVAL;
+    if (num_req < 0 || total_q < 0 || max_q < 0 || max_words < 0) return LAZY_EINVAL;
     if (num_req == 0 || total_q == 0 || max_q == 0) return LAZY_OK;
-    if (!q_raw || !cu_q || !q_pos0 || !table_indptr || !out || (max_words > 0 && !table)) return LAZY_EINVAL;
-    if (total_words > static_cast<int>(LAZY_MAX_BLOCKS) || num_req > 65535) return LAZY_ERANGE;
-    if (max_words == 0 || total_words == 0 || pool->num_blocks == 0)
-        return launch_rc(cudaMemsetAsync(out, 0, static_cast<size_t>(total_q) * cfg->num_q_heads * 128 * 2,
+    Q8PrefillParams p;
+    const bool blocks = pool->num_blocks > 0;
+    rc = attn_common(cfg, p.a, num_req, table, table_indptr, max_words, blocks ? pool->blk_meta : kNoMeta,
+                     blocks ? reinterpret_cast<const uint16_t *>(pool->v_codes) : kNoPool, pool->num_blocks, out,
+                     d_status);
+    if (rc) return rc;
+    if (!q_raw || !cu_q || !q_pos0 || !aligned(q_raw, 8) || !aligned(out, 16)) return LAZY_EINVAL;
+    if (max_words == 0 || !blocks)
+        // nothing can be visible: every output row is zero
+        return launch_rc(cudaMemsetAsync(out, 0, static_cast<size_t>(total_q) * p.a.hq * 128 * 2,
                                          static_cast<cudaStream_t>(stream)));
-    const size_t stage = q8_stage_bytes(total_words, cfg->num_kv_heads, num_req);
-    if (!workspace || ws_bytes < lazy_prefill_q8_workspace_bytes(cfg, num_req, total_q, max_q, max_words, total_words))
-        return LAZY_EWORKSPACE;
+    const int64_t units = prefill_units(cfg, num_req, max_q);
+    // rows of all units, and the query kernel's grid
+    if (static_cast<int64_t>(max_q) * p.a.group > (int64_t(1) << 30) || units > (int64_t(1) << 22) || num_req > 65535)
+        return LAZY_ERANGE;
+    const int sms = sm_count();
+    if (!workspace || ws_bytes < q8_prefill_ws_bytes(units, max_words, sms)) return LAZY_EWORKSPACE;
     if (!aligned(workspace, 16)) return LAZY_EINVAL;
-    Q8StageParams p;
+    p.a.q_raw = q_raw;
+    p.a.cu_q = cu_q;
+    p.a.q_pos0 = q_pos0;
+    p.a.max_q = max_q;
+    p.a.pf_mtiles = static_cast<int>((static_cast<int64_t>(max_q) * p.a.group + kPrefillRows - 1) / kPrefillRows);
     p.k_codes = pool->k_codes;
     p.v_codes = pool->v_codes;
     p.k_scale = pool->k_scale;
     p.v_scale = pool->v_scale;
-    p.blk_meta = pool->blk_meta;
-    p.table = table;
-    p.table_indptr = table_indptr;
-    p.cu_q = cu_q;
-    p.q_pos0 = q_pos0;
-    const int64_t rows = static_cast<int64_t>(total_words) * cfg->num_kv_heads * 16;
-    p.k_out = static_cast<uint16_t *>(workspace);
-    p.v_out = p.k_out + rows * 128;
-    p.table_out = reinterpret_cast<uint32_t *>(p.v_out + rows * 128);
-    p.meta_out = p.table_out + total_words;
-    p.indptr_out = reinterpret_cast<int32_t *>(p.meta_out + total_words);
-    p.num_req = num_req;
-    p.hkv = cfg->num_kv_heads;
-    p.num_blocks = pool->num_blocks;
-    p.max_words = max_words;
-    p.cap_words = total_words;
-    p.d_status = d_status;
-    fill_rope(p.rope, cfg);
-    rc = prefill_impl(cfg, q_raw, cu_q, q_pos0, num_req, total_q, max_q, p.table_out, p.indptr_out, max_words,
-                      p.meta_out, p.k_out, rows, p.v_out, total_words, out, static_cast<char *>(workspace) + stage,
-                      ws_bytes - stage, d_status, stream, !cfg->alibi_slopes, true);
-    if (rc) return rc;
-    rc = launch_rc(launch_q8_stage(p, static_cast<cudaStream_t>(stream)));
-    if (rc) return rc;
-    return prefill_impl(cfg, q_raw, cu_q, q_pos0, num_req, total_q, max_q, p.table_out, p.indptr_out, max_words,
-                        p.meta_out, p.k_out, rows, p.v_out, total_words, out, static_cast<char *>(workspace) + stage,
-                        ws_bytes - stage, d_status, stream, !cfg->alibi_slopes);
+    return launch_rc(launch_prefill_q8(p, workspace, units, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int lazy_evict_blocks(const uint32_t *table, const int32_t *table_indptr, int num_req, int max_words,

@@ -155,26 +155,20 @@ struct LanePlan {
 LanePlan lane_plan(int num_req, int hkv, int max_words, int group, bool q8, bool mass, int sms);
 cudaError_t launch_decode_lane(const LaneParams &p, bool q8, cudaStream_t s);
 
-// Prefill over the 8-bit pool: the words of `num_req` requests as bf16 keys (rotated to their
-// absolute positions) and values, one row of the staging buffers per word, with a table and
-// metadata that name those rows.
-struct Q8StageParams {
+// Prefill over the 8-bit pool (prefill_q8.cu).  a.q_prep: prepared query tiles; row_scale: their row
+// factors [units][256]; units from a.pf_base run as `parts` CTAs each.
+struct Q8PrefillParams {
+    AttnParams a;
     const uint8_t *k_codes, *v_codes;
     const float *k_scale, *v_scale;
-    const uint32_t *blk_meta, *table;
-    const int32_t *table_indptr, *cu_q, *q_pos0;
-    uint16_t *k_out, *v_out;         // [cap_words][Hkv][16][128]
-    uint32_t *table_out, *meta_out;  // [cap_words]
-    int32_t *indptr_out;             // [num_req + 1]
-    int num_req, hkv, num_blocks, max_words, cap_words;
-    int *d_status;
-    RopeTableHost rope;
+    float *row_scale;
+    int parts;
 };
-inline size_t q8_stage_bytes(int total_words, int hkv, int num_req) {
-    const size_t n = static_cast<size_t>(total_words) * (static_cast<size_t>(hkv) * 8192 + 8) + (static_cast<size_t>(num_req) + 1) * 4;
-    return (n + 1023) / 1024 * 1024;
-}
-cudaError_t launch_q8_stage(const Q8StageParams &p, cudaStream_t s);
+struct Q8PrefillPlan {
+    int nsplit, parts;
+};
+size_t q8_prefill_ws_bytes(int64_t units, int max_words, int sms);
+cudaError_t launch_prefill_q8(Q8PrefillParams &p, void *workspace, int64_t units, int sms, cudaStream_t s);
 
 struct EvictParams {
     const uint32_t *table;

@@ -140,8 +140,7 @@ def _load():
         "lazy_decode_q8_workspace_bytes": (_sz, [_cfgp, _i, _i, _i]),
         "lazy_decode_attn_q8": (_i, [_cfgp, _vp, _vp, _i, _vp, _vp, _i, _q8p, _vp, _vp, _vp, _sz, _vp, _vp]),
         "lazy_prefill_q8_workspace_bytes": (_sz, [_cfgp, _i, _i, _i, _i, _i]),
-        "lazy_prefill_attn_q8": (_i, [_cfgp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _i, _q8p, _vp, _vp, _sz, _vp,
-                                      _vp]),
+        "lazy_prefill_attn_q8": (_i, [_cfgp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _i, _q8p, _vp, _vp, _sz, _vp, _vp]),
         "lazy_decode_mass_workspace_bytes": (_sz, [_cfgp, _i, _i]),
         "lazy_decode_attn_mass": (_i, [_cfgp, _vp, _vp, _i, _vp, _vp, _i, _vp, _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp,
                                        _vp]),
@@ -523,8 +522,8 @@ def prefill_attn_q8(cfg: Cfg, q_raw, cu_q, q_pos0, max_q: int, table, table_indp
     with guard:
         _check("lazy_prefill_attn_q8", _lib.lazy_prefill_attn_q8(
             ctypes.byref(c), _ptr(q_raw), _ptr(cu_q), _ptr(q_pos0), n, total_q, int(max_q), _ptr(table),
-            _ptr(table_indptr), int(max_words), int(table.numel()), ctypes.byref(q), _ptr(out), _ptr(workspace),
-            _nbytes(workspace), _ptr(d_status), st))
+            _ptr(table_indptr), int(max_words), ctypes.byref(q), _ptr(out), _ptr(workspace), _nbytes(workspace),
+            _ptr(d_status), st))
 
 
 def evict_blocks(table, table_indptr, max_words: int, block_mass, keep, n_first: int, n_last: int, table_out,

@@ -47,12 +47,12 @@ def _mass(cfg=OK, **kw):
 
 
 def _prefill(cfg=OK, pool=None, no_pool=False, **kw):
-    a = dict(q=P, cu=P, p0=P, n=2, tq=6, mq=3, table=P, indptr=P, mw=4, tw=8, out=P, ws=P, wsb=1 << 30)
+    a = dict(q=P, cu=P, p0=P, n=2, tq=6, mq=3, table=P, indptr=P, mw=4, out=P, ws=P, wsb=1 << 30)
     a.update(kw)
     c = cfg.c() if cfg else None
     pl = None if no_pool else (pool or _pool())
     return la._lib.lazy_prefill_attn_q8(_ref(c), a["q"], a["cu"], a["p0"], a["n"], a["tq"], a["mq"], a["table"],
-                                        a["indptr"], a["mw"], a["tw"], _ref(pl), a["out"], a["ws"], a["wsb"], None, None)
+                                        a["indptr"], a["mw"], _ref(pl), a["out"], a["ws"], a["wsb"], None, None)
 
 
 def _evict(**kw):
@@ -116,10 +116,12 @@ def test_decode_refusals():
 def test_prefill_refusals():
     for f in ("q", "cu", "p0", "table", "indptr", "out"):
         assert _prefill(**{f: None}) == la.LAZY_EINVAL
-    for f in ("tq", "mq", "mw", "tw"):
+    for f in ("tq", "mq", "mw"):
         assert _prefill(**{f: -1}) == la.LAZY_EINVAL
     assert _prefill(ws=None) == la.LAZY_EWORKSPACE
     assert _prefill(ws=P + 8) == la.LAZY_EINVAL
+    assert _prefill(q=P + 4) == la.LAZY_EINVAL and _prefill(out=P + 8) == la.LAZY_EINVAL
+    assert _prefill(n=65536) == la.LAZY_ERANGE and _prefill(mq=1 << 30) == la.LAZY_ERANGE
     assert _prefill(wsb=la.prefill_q8_workspace_bytes(OK, 2, 6, 3, 4, 8) - 1) == la.LAZY_EWORKSPACE
     assert _prefill(tq=0) == la.LAZY_OK and _prefill(mq=0) == la.LAZY_OK
 
