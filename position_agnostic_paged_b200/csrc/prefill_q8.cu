@@ -16,17 +16,18 @@
 //   P'  w 2^(log2 s_v - r) with a running reference r >= max(s + log2 s_v) - 8, so that neither
 //       a large nor a small V scale over- or underflows f16;
 //   V'  the codes themselves (exact).
-// f16 keeps every operand to 2^-11 of its largest element, where bf16 would keep 2^-8.  Sums, maxima
-// and outputs are fp32.
+// f16 keeps an operand to 2^-11 of its largest element where bf16 would keep 2^-8; K' is rotated in f16
+// (cos and sin, one product and the sum rounded: 3 x 2^-11), which halves its cost and moves the
+// output's error by less than its bf16 rounding.  Sums, maxima and outputs are fp32.
 //
-// 16 warps, registers split by role:
+// 16 warps by role:
 //   warp 0      table walk: per tile the words' metadata and scales into a ring of records, and the
 //               blocks' codes (2 KiB per block, contiguous) into shared memory by bulk copies
-//   warp 2      MMA issuer (and owner of tensor memory); warp 3 loads the query tiles
+//   warp 2      MMA issuer (and owner of tensor memory)
 //   warps 4-7, 8-11   softmax of row tile 0 and 1, one row per thread
-//   warps 12-15 codes to f16, K rotated, V with the slots that no row sees as zeros, into the
-//               128-byte-swizzled operand tiles (two stages each); codes have one stage each: a
-//               tile's codes are converted in a third of its time, the rest covers the next copy
+//   warps 12-15 K codes to rotated f16; warps 1 and 3 (after loading the query tiles) the angles of the
+//               next tile, and V codes to f16, slots that no row sees as zeros.  Operand tiles are
+//               128-byte swizzled, two stages each; codes have one stage each
 // Tensor memory (512 columns): S0, S1 (P over their first halves), O0, O1, 128 columns each.
 #include <cuda_fp16.h>
 
@@ -45,7 +46,7 @@ namespace {
 constexpr int kTileRows = 128, kRows = 2 * kTileRows, kTileBlocks = 8;
 constexpr int kTileBytes = kTileRows * kHeadDim * 2, kHalfPlane = kTileBytes / 2;
 constexpr int kCodeBlock = kBlockTokens * kHeadDim, kCodeBytes = kTileBlocks * kCodeBlock;
-constexpr int kStages = 2, kInfoStages = 8, kThreads = 512;
+constexpr int kStages = 2, kInfoStages = 4, kThreads = 512;
 static_assert(kRows == kPrefillRows, "rows per CTA");
 
 // One tile of the walk; n = 0 ends it.
@@ -66,22 +67,15 @@ constexpr int kOffBar = kOffInfo + kInfoStages * static_cast<int>(sizeof(TileInf
 constexpr int B_KCFULL = 0, B_KCEMPTY = 1, B_VCFULL = 2, B_VCEMPTY = 3, B_KFULL = 4, B_KEMPTY = B_KFULL + kStages,
               B_VFULL = B_KEMPTY + kStages, B_VEMPTY = B_VFULL + kStages, B_IFULL = B_VEMPTY + kStages,
               B_IEMPTY = B_IFULL + kInfoStages, B_SFULL = B_IEMPTY + kInfoStages, B_PFULL = B_SFULL + 2,
-              B_ODONE = B_PFULL + 2, B_QFULL = B_ODONE + 2, B_DRAIN = B_QFULL + 1, kNumBars = B_DRAIN + 1;
-constexpr int kOffTheta = kOffBar + kNumBars * 8;
-constexpr int kOffMisc = kOffTheta + kHalfDim * 8;
+              B_ODONE = B_PFULL + 2, B_QFULL = B_ODONE + 2, B_DRAIN = B_QFULL + 1, B_AFULL = B_DRAIN + 1,
+              kNumBars = B_AFULL + 2;
+constexpr int kOffAngle = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // two tables of f16 cos [64], sin [64]
+constexpr int kOffMisc = kOffAngle + 2 * 256;
 constexpr int kOffSlope = kOffMisc + 16;
 constexpr size_t kSmem = kOffSlope + 32 * 4 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
-constexpr int kInfoConsumers = 13;          // 8 softmax warps, the MMA warp, 4 conversion warps
+constexpr int kInfoConsumers = 15;          // 8 softmax warps, the MMA warp, 4 + 2 conversion warps
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P' stays below 2^8 between rescales of O
-
-// Register split (launch: 512 threads x 128): 72 + 2 x 184 + 72 = 512.
-constexpr int kProducerRegs = 72, kSoftmaxRegs = 184, kConvRegs = 72;
-static_assert(kProducerRegs + 2 * kSoftmaxRegs + kConvRegs <= 512, "register split");
-template <int N>
-__device__ __forceinline__ void setmaxnreg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void setmaxnreg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
 
 // kind::f16 with f16 A/B and fp32 accumulation, 128 x 128.
 constexpr uint32_t idesc_f16(bool b_mn_major) {
@@ -94,12 +88,28 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t s
                  "l"(src), "r"(size), "r"(smem_u32(bar))
                  : "memory");
 }
+// Out of line: the roles' loops together have to fit the instruction cache.
+__device__ __noinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *d_status) {
+    return wait_or_abort(bar, parity, abort_flag, d_status);
+}
+// Same decision for every lane of the warp.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *d_status) {
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, d_status));
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_long(bar, parity, abort_flag, d_status));
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t h2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
 }
 __device__ __forceinline__ float log2_of(float x) {
     float y;
@@ -129,7 +139,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kOffBar);
     float *slope_s = reinterpret_cast<float *>(sm + kOffSlope);
     TileInfo *info = reinterpret_cast<TileInfo *>(sm + kOffInfo);
-    double *theta_s = reinterpret_cast<double *>(sm + kOffTheta);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kOffMisc + 4);
 
@@ -163,11 +172,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
         mbar_init(&bars[B_KCFULL], 1);
         mbar_init(&bars[B_KCEMPTY], 4);
         mbar_init(&bars[B_VCFULL], 1);
-        mbar_init(&bars[B_VCEMPTY], 4);
+        mbar_init(&bars[B_VCEMPTY], 2);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars[B_KFULL + i], 4);
             mbar_init(&bars[B_KEMPTY + i], 1);
-            mbar_init(&bars[B_VFULL + i], 4);
+            mbar_init(&bars[B_VFULL + i], 2);
+            mbar_init(&bars[B_AFULL + i], 2);
             mbar_init(&bars[B_VEMPTY + i], 1);
         }
         for (int i = 0; i < kInfoStages; ++i) {
@@ -185,7 +195,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
         if (mt == 0 && kvh == 0 && n_all > p.max_words) set_status(p.d_status, LAZY_DSTATUS_BAD_TABLE);
         fence_barrier_init();
     }
-    if (threadIdx.x < kHalfDim) theta_s[threadIdx.x] = p.rope.theta[threadIdx.x];
     if (ALIBI && threadIdx.x < G) slope_s[threadIdx.x] = p.alibi_log2[kvh * G + threadIdx.x];
     if (warp == 2) {
         tc::tmem_alloc(tmem_slot, 512);
@@ -197,53 +206,77 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
     const uint32_t tbase = *tmem_slot;
 
     if (warp < 4) {
-        setmaxnreg_dec<kProducerRegs>();
         const bool leader = tc::elect_one();
         if (warp == 0) {
             // ======================================================== table walk and code copies
             int j = 0, n_kc = 0, n_vc = 0;   // tiles, K and V copies issued
             bool ok = true;
+            int n_v = 0;        // tile n_vc: its blocks, and this lane's block
+            size_t bh_v = 0;
+            auto load_v = [&]() {
+                if (!warp_wait(&bars[B_VCEMPTY], (n_vc & 1) ^ 1, abort_flag, p.d_status)) return false;
+                if (leader) mbar_arrive_expect_tx(&bars[B_VCFULL], n_v * kCodeBlock);
+                __syncwarp();
+                if (lane < n_v) bulk_load(sm + kOffVC + lane * kCodeBlock, P.v_codes + bh_v * kCodeBlock, kCodeBlock, &bars[B_VCFULL]);
+                ++n_vc;
+                return true;
+            };
+            // 32 words at a time, one per lane, with their blocks' metadata and scales: three dependent loads
+            // serve up to four tiles
+            uint32_t wl = 0u, mt_l = 0u, seen = 0u;
+            float ks_l = 0.f, lv_l = 0.f;
+            int w0 = INT_MIN / 2;
             for (int w = wbeg; w < wend;) {
-                // lane l: word w + l
-                uint32_t wl = 0u, mt_l = 0u;
-                bool vis = false;
-                const bool in = w + lane < wend;
-                if (in) {
-                    wl = p.table[wbase + w + lane];
-                    const uint32_t b = word_block(wl);
-                    if (b < static_cast<uint32_t>(p.num_blocks)) {
-                        mt_l = p.blk_meta[b];
-                        vis = meta_valid(mt_l) > 0 && word_offset(wl) + meta_j0(mt_l) <= Plast;
-                    } else {
-                        set_status(p.d_status, LAZY_DSTATUS_BAD_BLOCK);
+                if (w - w0 + kTileBlocks > 32 && w0 + 32 < wend) {
+                    w0 = w;
+                    wl = mt_l = 0u;
+                    bool vis = false;
+                    if (w + lane < wend) {
+                        wl = p.table[wbase + w + lane];
+                        const uint32_t b = word_block(wl);
+                        if (b < static_cast<uint32_t>(p.num_blocks)) {
+                            const size_t bh = static_cast<size_t>(b) * p.hkv + kvh;
+                            mt_l = p.blk_meta[b];
+                            ks_l = P.k_scale[bh];
+                            lv_l = log2_of(P.v_scale[bh]);
+                            vis = meta_valid(mt_l) > 0 && word_offset(wl) + meta_j0(mt_l) <= Plast;
+                        } else {
+                            set_status(p.d_status, LAZY_DSTATUS_BAD_BLOCK);
+                        }
                     }
+                    seen = __ballot_sync(0xffffffffu, vis);
                 }
-                const uint32_t seen = __ballot_sync(0xffffffffu, vis);
-                const int skip = seen ? __ffs(seen) - 1 : 32;
+                const int i = w - w0;
+                const uint32_t rest = seen >> i;
+                if (rest == 0u) {
+                    w = w0 + 32;
+                    continue;
+                }
+                const int skip = __ffs(rest) - 1;
                 if (skip > 0) {
                     w += skip;
                     continue;
                 }
-                const int off = word_offset(__shfl_sync(0xffffffffu, wl, 0));
-                const bool same = lane < kTileBlocks && vis && word_offset(wl) == off;
+                // the tile: up to 8 visible words that share an offset; lane k < 8 holds word w + k
+                const int src = (i + lane) & 31;
+                const uint32_t wk = __shfl_sync(0xffffffffu, wl, src);
+                const uint32_t mt = __shfl_sync(0xffffffffu, mt_l, src);
+                const float ks = __shfl_sync(0xffffffffu, ks_l, src), lv = __shfl_sync(0xffffffffu, lv_l, src);
+                const int off = word_offset(__shfl_sync(0xffffffffu, wl, i));
+                const bool same = lane < kTileBlocks && i + lane < 32 && ((seen >> src) & 1u) && word_offset(wk) == off;
                 const int n = __ffs(~__ballot_sync(0xffffffffu, same)) - 1;
-                const size_t bh = static_cast<size_t>(word_block(wl)) * p.hkv + kvh;
-                float ks = 0.f, lv = 0.f;
-                if (lane < n) {
-                    ks = P.k_scale[bh];
-                    lv = log2_of(P.v_scale[bh]);
-                }
+                const size_t bh = static_cast<size_t>(word_block(wk)) * p.hkv + kvh;
                 const bool full =
-                    n == kTileBlocks && __all_sync(0xffffffffu, lane >= n || (meta_valid(mt_l) == kBlockTokens &&
-                                                                              off + meta_j0(mt_l) + kBlockTokens - 1 <= Pbase));
+                    n == kTileBlocks && __all_sync(0xffffffffu, lane >= n || (meta_valid(mt) == kBlockTokens &&
+                                                                              off + meta_j0(mt) + kBlockTokens - 1 <= Pbase));
                 const int is = j % kInfoStages;
                 ok = warp_wait(&bars[B_IEMPTY + is], ((j / kInfoStages) & 1) ^ 1, abort_flag, p.d_status);
                 if (!ok) break;
                 TileInfo &ti = info[is];
                 if (lane < kTileBlocks) {
-                    ti.meta[lane] = lane < n ? mt_l : 0u;
-                    ti.ks[lane] = ks;
-                    ti.lv[lane] = lv;
+                    ti.meta[lane] = lane < n ? mt : 0u;
+                    ti.ks[lane] = lane < n ? ks : 0.f;
+                    ti.lv[lane] = lane < n ? lv : 0.f;
                 }
                 if (leader) {
                     ti.n = n;
@@ -258,15 +291,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
                 __syncwarp();
                 if (lane < n) bulk_load(sm + kOffKC + lane * kCodeBlock, P.k_codes + bh * kCodeBlock, kCodeBlock, &bars[B_KCFULL]);
                 ++n_kc;
-                ok = warp_wait(&bars[B_VCEMPTY], (j & 1) ^ 1, abort_flag, p.d_status);
-                if (!ok) break;
-                if (leader) mbar_arrive_expect_tx(&bars[B_VCFULL], n * kCodeBlock);
-                __syncwarp();
-                if (lane < n) bulk_load(sm + kOffVC + lane * kCodeBlock, P.v_codes + bh * kCodeBlock, kCodeBlock, &bars[B_VCFULL]);
-                ++n_vc;
+                // V one tile behind, so that the record of tile j never waits for the V of tile j - 2
+                if (j > 0 && !(ok = load_v())) break;
+                n_v = n;
+                bh_v = bh;
                 ++j;
                 w += n;
             }
+            if (ok && j > 0) ok = load_v();
             if (ok) {
                 const int is = j % kInfoStages;
                 if (warp_wait(&bars[B_IEMPTY + is], ((j / kInfoStages) & 1) ^ 1, abort_flag, p.d_status)) {
@@ -345,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
             if (leader) tc::commit(&bars[B_DRAIN]);
             __syncwarp();
             mbar_wait(&bars[B_DRAIN], 0);
-        } else if (warp == 3) {
-            // ======================================================== query tiles (prepared layout)
-            if (leader) {
+        } else {
+            // ======================================================== query tiles, angles, V codes (warps 1 and 3)
+            if (warp == 3 && leader) {
                 mbar_arrive_expect_tx(&bars[B_QFULL], 2 * kTileBytes);
                 const uint16_t *q = p.q_prep + unit_rows(p, mt, kvh, r) * kHeadDim;
 #pragma unroll
@@ -355,11 +387,82 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
                     bulk_load(sm + kOffQ + t * kHalfPlane, q + t * (kHalfPlane / 2), kHalfPlane, &bars[B_QFULL]);
             }
             __syncwarp();
-            mbar_wait(&bars[B_QFULL], 0);   // landed before the kernel can end
+            const int pair = (warp == 3 ? 32 : 0) + lane;
+            const double th = p.rope.theta[pair];
+            int cur = INT_MIN;
+            float c = 1.f, s = 0.f;
+            // angles of tile j (this warp's 32 pairs) into table j & 1, free since the K of tile j - 2 is done;
+            // returns the tile's blocks, -1 if a wait gave up
+            auto angles = [&](int j) -> int {
+                const int is = j % kInfoStages, st = j % kStages;
+                if (!warp_wait(&bars[B_IFULL + is], (j / kInfoStages) & 1, abort_flag, p.d_status)) return -1;
+                const int n = info[is].n, off = info[is].off;
+                if (n == 0) return 0;
+                if (off != cur) {
+                    cur = off;
+                    rope_cos_sin(off - Pbase, th, c, s);
+                }
+                if (!warp_wait(&bars[B_KFULL + st], ((j / kStages) & 1) ^ 1, abort_flag, p.d_status)) return -1;
+                __half *tab = reinterpret_cast<__half *>(sm + kOffAngle + st * 256);
+                tab[pair] = __float2half_rn(c);
+                tab[kHalfDim + pair] = __float2half_rn(s);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_AFULL + st]);
+                return n;
+            };
+            // V: thread (ch, rb) takes dims 16 ch .. + 15 of slots rb and rb + 8 of every block
+            const int ch = lane & 7, rb = (lane >> 3) + (warp == 3 ? 4 : 0);
+            const uint8_t *vc = sm + kOffVC + rb * kHeadDim + 16 * ch;
+            const uint32_t vrow = (ch >> 2) * kHalfPlane + rb * 128;
+            const uint32_t v0 = vrow + (((2 * (ch & 3)) ^ rb) << 4), v1 = vrow + (((2 * (ch & 3) + 1) ^ rb) << 4);
+            int n = angles(0);
+            for (int j = 0; n > 0; ++j) {
+                const int is = j % kInfoStages, st = j % kStages;
+                const int n_next = angles(j + 1);
+                const TileInfo &ti = info[is];
+                uint32_t keep = 0u;   // bit k, bit 8 + k: some row may see slot rb, rb + 8 of block k
+#pragma unroll
+                for (int k = 0; k < kTileBlocks; ++k) {
+                    const int lim = min(meta_valid(ti.meta[k]), Plast - ti.off - meta_j0(ti.meta[k]) + 1);
+                    keep |= (rb < lim ? 1u << k : 0u) | (rb + 8 < lim ? 256u << k : 0u);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_IEMPTY + is]);
+                if (!warp_wait(&bars[B_VCFULL], j & 1, abort_flag, p.d_status)) break;
+                if (!warp_wait(&bars[B_VEMPTY + st], ((j / kStages) & 1) ^ 1, abort_flag, p.d_status)) break;
+                uint8_t *vt = sm + kOffV + st * kTileBytes;
+                // blocks behind the tile's last hold old codes that no MMA reads
+#pragma unroll
+                for (int k0 = 0; k0 < kTileBlocks; k0 += 2) {
+                    uint4 w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = *reinterpret_cast<const uint4 *>(vc + (k0 + (k >> 1)) * kCodeBlock + (k & 1) * 8 * kHeadDim);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (!((keep >> (k0 + (k >> 1) + 8 * (k & 1))) & 1u)) w[k] = make_uint4(0, 0, 0, 0);   // 0 * NaN
+                        uint4 x, y;
+                        codes_to_f16(w[k].x, x.x, x.y);
+                        codes_to_f16(w[k].y, x.z, x.w);
+                        codes_to_f16(w[k].z, y.x, y.y);
+                        codes_to_f16(w[k].w, y.z, y.w);
+                        uint8_t *vd = vt + (k0 + (k >> 1)) * kBoxBytes + (k & 1) * 1024;
+                        *reinterpret_cast<uint4 *>(vd + v0) = x;
+                        *reinterpret_cast<uint4 *>(vd + v1) = y;
+                    }
+                }
+                fence_proxy_async_smem();   // generic writes become visible to the tensor core
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bars[B_VCEMPTY]);
+                    mbar_arrive(&bars[B_VFULL + st]);
+                }
+                n = n_next;
+            }
+            if (warp == 3) mbar_wait(&bars[B_QFULL], 0);   // landed before the kernel can end
         }
     } else if (warp < 12) {
         // ============================================================ softmax (one row per thread)
-        setmaxnreg_inc<kSoftmaxRegs>();
         const int t = (warp - 4) >> 2;
         const int row = threadIdx.x - 128 - 128 * t;
         const int R = R0 + kTileRows * t + row;
@@ -393,46 +496,54 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
             ok = warp_wait(&bars[B_SFULL + t], j & 1, abort_flag, p.d_status);
             if (!ok) break;
             tc::fence_after_sync();
-            uint32_t sv[128];
-            tc::ld32(tS + lane_off + 0, *reinterpret_cast<uint32_t(*)[32]>(sv + 0));
-            tc::ld32(tS + lane_off + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
-            tc::ld32(tS + lane_off + 64, *reinterpret_cast<uint32_t(*)[32]>(sv + 64));
-            tc::ld32(tS + lane_off + 96, *reinterpret_cast<uint32_t(*)[32]>(sv + 96));
-            tc::wait_ld();
+            // The row in two halves of 64 columns, first for its maxima and again for the weights: tensor
+            // memory is read twice, but the loop is a quarter of the code of one over all 128 columns in
+            // registers, whose instructions did not fit the cache beside the other roles'.
+            uint32_t sv[64];
             auto f = [&](int c) { return __uint_as_float(sv[c]); };
-            if (ALIBI) {
-                // scores with the in-block part of the bias; the block part joins the maxima and offsets
+            auto load = [&](int h) {
+                tc::ld32(tS + lane_off + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(sv));
+                tc::ld32(tS + lane_off + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+                tc::wait_ld();
+                if (ALIBI) {
+                    // scores with the in-block part of the bias; the block part joins the maxima and offsets
 #pragma unroll
-                for (int k = 0; k < kTileBlocks; ++k) {
-                    const float fk = ti.ks[k] * hm;
+                    for (int k = 0; k < 4; ++k) {
+                        const float fk = ti.ks[4 * h + k] * hm;
 #pragma unroll
-                    for (int c = 16 * k; c < 16 * k + 16; ++c)
-                        sv[c] = __float_as_uint(fmaf(f(c), fk, slope * static_cast<float>(c & 15)));
+                        for (int c = 16 * k; c < 16 * k + 16; ++c)
+                            sv[c] = __float_as_uint(fmaf(f(c), fk, slope * static_cast<float>(c & 15)));
+                    }
                 }
-            }
-            if (!ti.full) {
+                if (!ti.full) {
+                    const uint32_t l4 = static_cast<uint32_t>(limp >> (20 * h));
 #pragma unroll
-                for (int k = 0; k < kTileBlocks; ++k) {
-                    const int lim = static_cast<int>((limp >> (5 * k)) & 31u);
+                    for (int k = 0; k < 4; ++k) {
+                        const int lim = static_cast<int>((l4 >> (5 * k)) & 31u);
 #pragma unroll
-                    for (int c = 16 * k; c < 16 * k + 16; ++c) sv[c] = (c & 15) < lim ? sv[c] : 0xFF800000u;
+                        for (int c = 16 * k; c < 16 * k + 16; ++c) sv[c] = (c & 15) < lim ? sv[c] : 0xFF800000u;
+                    }
                 }
-            }
+            };
             // factor of a block's scores; at least the smallest normal number, so that -inf stays -inf
             auto factor = [&](int k) { return ALIBI ? 1.f : fmaxf(ti.ks[k] * hm, 0x1p-126f); };
             auto bias = [&](int k) { return ALIBI ? slope * static_cast<float>(ti.off + meta_j0(ti.meta[k]) - prow) : 0.f; };
             float m_new = m_run, mo_new = -INFINITY;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                load(h);
 #pragma unroll
-            for (int k = 0; k < kTileBlocks; ++k) {
-                float a = max3(f(16 * k), f(16 * k + 1), f(16 * k + 2)), b = f(16 * k + 15);
+                for (int k = 0; k < 4; ++k) {
+                    float a = max3(f(16 * k), f(16 * k + 1), f(16 * k + 2)), b = f(16 * k + 15);
 #pragma unroll
-                for (int c = 3; c < 15; c += 4) {
-                    a = max3(a, f(16 * k + c), f(16 * k + c + 1));
-                    b = max3(b, f(16 * k + c + 2), f(16 * k + c + 3));
+                    for (int c = 3; c < 15; c += 4) {
+                        a = max3(a, f(16 * k + c), f(16 * k + c + 1));
+                        b = max3(b, f(16 * k + c + 2), f(16 * k + c + 3));
+                    }
+                    const float s = fmaf(fmaxf(a, b), factor(4 * h + k), bias(4 * h + k));
+                    m_new = fmaxf(m_new, s);
+                    mo_new = fmaxf(mo_new, s + ti.lv[4 * h + k]);
                 }
-                const float s = fmaf(fmaxf(a, b), factor(k), bias(k));
-                m_new = fmaxf(m_new, s);
-                mo_new = fmaxf(mo_new, s + ti.lv[k]);
             }
             const float mu = m_new == -INFINITY ? 0.f : m_new;
             if (m_new != m_run) {
@@ -447,27 +558,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
             }
             const float mou = mo == -INFINITY ? 0.f : mo;
             float ls0 = 0.f, ls1 = 0.f;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                load(h);
 #pragma unroll
-            for (int k = 0; k < kTileBlocks; ++k) {
-                const float fk = factor(k), nm = bias(k) - mu;
-                const float F = fast_exp2(fminf(mu + ti.lv[k] - mou, 126.f));
+                for (int k = 0; k < 4; ++k) {
+                    const float fk = factor(4 * h + k), nm = bias(4 * h + k) - mu;
+                    const float F = fast_exp2(fminf(mu + ti.lv[4 * h + k] - mou, 126.f));
 #pragma unroll
-                for (int e = 8 * k; e < 8 * k + 8; ++e) {
-                    float x0, x1;
-                    fma2v(x0, x1, f(2 * e), f(2 * e + 1), fk, fk, nm, nm);
-                    float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                    add2(ls0, ls1, p0, p1);
-                    mul2(p0, p1, p0, p1, F, F);
-                    sv[e] = pack_h2(p0, p1);
+                    for (int e = 8 * k; e < 8 * k + 8; ++e) {
+                        float x0, x1;
+                        fma2v(x0, x1, f(2 * e), f(2 * e + 1), fk, fk, nm, nm);
+                        float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                        add2(ls0, ls1, p0, p1);
+                        mul2(p0, p1, p0, p1, F, F);
+                        sv[e] = pack_h2(p0, p1);
+                    }
                 }
+                // P over columns of S that have been read
+                tc::st32(tS + lane_off + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(sv));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_IEMPTY + is]);
-            tc::st32(tS + lane_off + 0, *reinterpret_cast<uint32_t(*)[32]>(sv + 0));
-            tc::st32(tS + lane_off + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
             l_run += ls0 + ls1;
             if (j > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[32];
                     tc::ld32(tO + lane_off + 32 * c, o);
@@ -500,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
         } else if (row_ok) {
             o = reinterpret_cast<uint4 *>(p.out + (static_cast<size_t>(q0 + tok) * p.hq + kvh * G + g) * kHeadDim);
         }
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             uint32_t ob[32];
             if (have) {
@@ -526,98 +641,58 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
             }
         }
     } else {
-        // ============================================================ codes to operand tiles
-        setmaxnreg_dec<kConvRegs>();
-        // thread (ch, rb): slot rb of every block; K pairs 8 ch .. + 7, V dims 16 ch .. + 15
+        // ============================================================ K codes to rotated f16 tiles
+        // thread (ch, rb): pairs 8 ch .. + 7 of slot rb of every block.  (a, b) -> (a c - b s, b c + a s) in f16
         const int tid = threadIdx.x - 384;
         const int ch = tid & 7, rb = tid >> 3;
         const uint8_t *kc = sm + kOffKC + rb * kHeadDim + 8 * ch;
-        const uint8_t *vc = sm + kOffVC + rb * kHeadDim + 16 * ch;
         const uint32_t ksw = rb * 128 + ((ch ^ (rb & 7)) << 4);
-        // V dims 16 ch .. + 15: two 16-byte chunks of one half plane
-        const uint32_t vrow = (ch >> 2) * kHalfPlane + rb * 128;
-        const uint32_t v0 = vrow + (((2 * (ch & 3)) ^ (rb & 7)) << 4), v1 = vrow + (((2 * (ch & 3) + 1) ^ (rb & 7)) << 4);
-        int cur = INT_MIN;
-        float c[8], s[8];
         for (int j = 0;; ++j) {
             const int is = j % kInfoStages, st = j % kStages;
             if (!warp_wait(&bars[B_IFULL + is], (j / kInfoStages) & 1, abort_flag, p.d_status)) break;
-            const TileInfo &ti = info[is];
-            const int n = ti.n;
+            const int n = info[is].n;
             if (n == 0) break;
-            const int off = ti.off;
-            uint32_t keep = 0u;   // bit k: some row may see slot rb of block k
-#pragma unroll
-            for (int k = 0; k < kTileBlocks; ++k)
-                keep |= (rb < meta_valid(ti.meta[k]) && off + meta_j0(ti.meta[k]) + rb <= Plast ? 1u : 0u) << k;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_IEMPTY + is]);
-            if (off != cur) {
-                cur = off;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) rope_cos_sin(off - Pbase, theta_s[8 * ch + e], c[e], s[e]);
-            }
+            if (!warp_wait(&bars[B_AFULL + st], (j / kStages) & 1, abort_flag, p.d_status)) break;
+            const uint4 c4 = *reinterpret_cast<const uint4 *>(sm + kOffAngle + st * 256 + 16 * ch);
+            const uint4 s4 = *reinterpret_cast<const uint4 *>(sm + kOffAngle + st * 256 + 128 + 16 * ch);
+            const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
             if (!warp_wait(&bars[B_KCFULL], j & 1, abort_flag, p.d_status)) break;
             if (!warp_wait(&bars[B_KEMPTY + st], ((j / kStages) & 1) ^ 1, abort_flag, p.d_status)) break;
             uint8_t *kt = sm + kOffK + st * kTileBytes;
+            // all 8 blocks (those behind the tile's last hold old codes, whose scores are masked), loads
+            // ahead of the stores they could otherwise not pass
 #pragma unroll
-            for (int k = 0; k < kTileBlocks; ++k) {
-                if (k < n) {
-                    const uint2 lo = *reinterpret_cast<const uint2 *>(kc + k * kCodeBlock);
-                    const uint2 hi = *reinterpret_cast<const uint2 *>(kc + k * kCodeBlock + kHalfDim);
-                    const uint32_t lw[2] = {lo.x, lo.y}, hw[2] = {hi.x, hi.y};
-                    uint32_t ol[4], oh[4];
+            for (int k0 = 0; k0 < kTileBlocks; k0 += 4) {
+                uint2 lo[4], hi[4];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        uint32_t a[2], b[2];
-                        codes_to_f16(lw[u], a[0], a[1]);
-                        codes_to_f16(hw[u], b[0], b[1]);
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int e = 4 * u + 2 * x;
-                            float a0, a1, b0, b1, ac0, ac1, bc0, bc1;
-                            f16x2_to_f32(a[x], a0, a1);
-                            f16x2_to_f32(b[x], b0, b1);
-                            mul2(ac0, ac1, a0, a1, c[e], c[e + 1]);
-                            mul2(bc0, bc1, b0, b1, c[e], c[e + 1]);
-                            fma2v(ac0, ac1, -b0, -b1, s[e], s[e + 1], ac0, ac1);
-                            fma2v(bc0, bc1, a0, a1, s[e], s[e + 1], bc0, bc1);
-                            ol[2 * u + x] = pack_h2(ac0, ac1);
-                            oh[2 * u + x] = pack_h2(bc0, bc1);
-                        }
-                    }
-                    *reinterpret_cast<uint4 *>(kt + k * kBoxBytes + ksw) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
-                    *reinterpret_cast<uint4 *>(kt + k * kBoxBytes + kHalfPlane + ksw) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+                for (int k = 0; k < 4; ++k) {
+                    lo[k] = *reinterpret_cast<const uint2 *>(kc + (k0 + k) * kCodeBlock);
+                    hi[k] = *reinterpret_cast<const uint2 *>(kc + (k0 + k) * kCodeBlock + kHalfDim);
                 }
-            }
-            fence_proxy_async_smem();   // generic writes become visible to the tensor core
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&bars[B_KCEMPTY]);
-                mbar_arrive(&bars[B_KFULL + st]);
-            }
-            if (!warp_wait(&bars[B_VCFULL], j & 1, abort_flag, p.d_status)) break;
-            if (!warp_wait(&bars[B_VEMPTY + st], ((j / kStages) & 1) ^ 1, abort_flag, p.d_status)) break;
-            uint8_t *vt = sm + kOffV + st * kTileBytes;
 #pragma unroll
-            for (int k = 0; k < kTileBlocks; ++k) {
-                if (k < n) {
-                    uint4 w = *reinterpret_cast<const uint4 *>(vc + k * kCodeBlock);
-                    if (!((keep >> k) & 1u)) w = make_uint4(0, 0, 0, 0);   // a weight of 0 does not undo a NaN
-                    uint4 x, y;
-                    codes_to_f16(w.x, x.x, x.y);
-                    codes_to_f16(w.y, x.z, x.w);
-                    codes_to_f16(w.z, y.x, y.y);
-                    codes_to_f16(w.w, y.z, y.w);
-                    *reinterpret_cast<uint4 *>(vt + k * kBoxBytes + v0) = x;
-                    *reinterpret_cast<uint4 *>(vt + k * kBoxBytes + v1) = y;
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t a[4], b[4], ol[4], oh[4];
+                    codes_to_f16(lo[k].x, a[0], a[1]);
+                    codes_to_f16(lo[k].y, a[2], a[3]);
+                    codes_to_f16(hi[k].x, b[0], b[1]);
+                    codes_to_f16(hi[k].y, b[2], b[3]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        ol[x] = h2_fma(b[x], s[x] ^ 0x80008000u, h2_mul(a[x], c[x]));
+                        oh[x] = h2_fma(a[x], s[x], h2_mul(b[x], c[x]));
+                    }
+                    uint8_t *kd = kt + (k0 + k) * kBoxBytes + ksw;
+                    *reinterpret_cast<uint4 *>(kd) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
+                    *reinterpret_cast<uint4 *>(kd + kHalfPlane) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&bars[B_VCEMPTY]);
-                mbar_arrive(&bars[B_VFULL + st]);
+                mbar_arrive(&bars[B_KCEMPTY]);
+                mbar_arrive(&bars[B_KFULL + st]);
             }
         }
     }

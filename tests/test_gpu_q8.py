@@ -10,7 +10,8 @@ from tests._q8_cases import (BLK, D, U_BF16, U_F16, PoolCase, bf16, check, evict
 pytestmark = pytest.mark.gpu
 
 HEADS = [(8, 8), (32, 8), (6, 2), (40, 8), (16, 1), (22, 2), (32, 1), (25, 1)]
-PREFILL_U = dict(u_qk=2 * U_F16, u_p=U_F16)      # query and key both rounded to f16
+# the query rounded to f16; the key's cos and sin, one product and the sum
+PREFILL_U = dict(u_qk=4 * U_F16, u_p=U_F16)
 
 
 def _requests(n=5, seed=0):
