@@ -9,8 +9,7 @@
 // share one offset.  Words that no row of the CTA sees are not visited: a long prompt's first rows
 // skip its later keys.  All MMA operands are f16:
 //   Q'  R(p_i - P0) q_i 2^-e_i, the row's largest element in [1, 2) (P0: the CTA's first position):
-//       prepared by a kernel before, so that the attention kernel loads it with plain bulk copies of
-//       rows already laid out as the tensor core reads them;
+//       prepared by a kernel before, in rows already laid out as the tensor core reads them;
 //   K'  R(o - P0) k_t: codes rotated without their scale, which multiplies the scores instead (one
 //       factor per 16 columns, in the instruction that subtracts the maximum);
 //   P'  w 2^(log2 s_v - r) with a running reference r >= max(s + log2 s_v) - 8, so that neither
@@ -23,12 +22,13 @@
 // 16 warps by role:
 //   warp 0      table walk: per tile the words' metadata and scales into a ring of records, and the
 //               blocks' codes (2 KiB per block, contiguous) into shared memory by bulk copies
-//   warp 2      MMA issuer (and owner of tensor memory)
+//   warps 2, 1  MMA issuers of row tiles 0 and 1 (warp 2 owns tensor memory)
+//   warp 3      the query tiles, then each tile's angles
 //   warps 4-7, 8-11   softmax of row tile 0 and 1, one row per thread
-//   warps 12-15 K codes to rotated f16; warps 1 and 3 (after loading the query tiles) the angles of the
-//               next tile, and V codes to f16, slots that no row sees as zeros.  Operand tiles are
-//               128-byte swizzled, two stages each; codes have one stage each
-// Tensor memory (512 columns): S0, S1 (P over their first halves), O0, O1, 128 columns each.
+//   warps 12-15 codes to f16: K rotated, V with the slots that no row sees as zeros, into the
+//               128-byte-swizzled operand tiles (two stages each; codes have one)
+// Tensor memory (512 columns): per row tile two score buffers of 64 columns (P over their first
+// halves), then O0, O1 of 128 columns.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -57,29 +57,32 @@ struct TileInfo {
     int n, off, full, pad;    // full: every key of 8 blocks is visible to every row
 };
 
-constexpr int kOffQ = 0;
+constexpr int kOffQ = 0;                                     // 2 row tiles
 constexpr int kOffK = kOffQ + 2 * kTileBytes;
 constexpr int kOffV = kOffK + kStages * kTileBytes;
-constexpr int kOffKC = kOffV + kStages * kTileBytes;
+constexpr int kOffKC = kOffV + kStages * kTileBytes;         // codes: one stage each
 constexpr int kOffVC = kOffKC + kCodeBytes;
 constexpr int kOffInfo = kOffVC + kCodeBytes;
 constexpr int kOffBar = kOffInfo + kInfoStages * static_cast<int>(sizeof(TileInfo));
+// barriers: codes landed / converted; per stage operand tile written / read, angles; records; per row tile
+// and score buffer scores / weights / product done
 constexpr int B_KCFULL = 0, B_KCEMPTY = 1, B_VCFULL = 2, B_VCEMPTY = 3, B_KFULL = 4, B_KEMPTY = B_KFULL + kStages,
-              B_VFULL = B_KEMPTY + kStages, B_VEMPTY = B_VFULL + kStages, B_IFULL = B_VEMPTY + kStages,
-              B_IEMPTY = B_IFULL + kInfoStages, B_SFULL = B_IEMPTY + kInfoStages, B_PFULL = B_SFULL + 2,
-              B_ODONE = B_PFULL + 2, B_QFULL = B_ODONE + 2, B_DRAIN = B_QFULL + 1, B_AFULL = B_DRAIN + 1,
-              kNumBars = B_AFULL + 2;
+              B_VFULL = B_KEMPTY + kStages, B_VEMPTY = B_VFULL + kStages, B_AFULL = B_VEMPTY + kStages,
+              B_IFULL = B_AFULL + kStages, B_IEMPTY = B_IFULL + kInfoStages, B_SFULL = B_IEMPTY + kInfoStages,
+              B_PFULL = B_SFULL + 4, B_ODONE = B_PFULL + 4, B_QFULL = B_ODONE + 4, B_DRAIN = B_QFULL + 1,
+              kNumBars = B_DRAIN + 2;
 constexpr int kOffAngle = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // two tables of f16 cos [64], sin [64]
 constexpr int kOffMisc = kOffAngle + 2 * 256;
 constexpr int kOffSlope = kOffMisc + 16;
 constexpr size_t kSmem = kOffSlope + 32 * 4 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
-constexpr int kInfoConsumers = 15;          // 8 softmax warps, the MMA warp, 4 + 2 conversion warps
+constexpr int kColO = 256;                  // tensor memory columns of O (S from 0)
+constexpr int kInfoConsumers = 15;          // 8 softmax, 2 MMA, 4 conversion warps, the angle warp
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: P' stays below 2^8 between rescales of O
 
-// kind::f16 with f16 A/B and fp32 accumulation, 128 x 128.
-constexpr uint32_t idesc_f16(bool b_mn_major) {
-    return (1u << 4) | (b_mn_major ? (1u << 16) : 0u) | (16u << 17) | (8u << 24);
+// kind::f16 with f16 A/B and fp32 accumulation, M = 128.
+constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
+    return (1u << 4) | (b_mn_major ? (1u << 16) : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 
 // size bytes (a multiple of 16), both addresses 16-byte aligned
@@ -172,25 +175,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
         mbar_init(&bars[B_KCFULL], 1);
         mbar_init(&bars[B_KCEMPTY], 4);
         mbar_init(&bars[B_VCFULL], 1);
-        mbar_init(&bars[B_VCEMPTY], 2);
+        mbar_init(&bars[B_VCEMPTY], 4);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars[B_KFULL + i], 4);
-            mbar_init(&bars[B_KEMPTY + i], 1);
-            mbar_init(&bars[B_VFULL + i], 2);
-            mbar_init(&bars[B_AFULL + i], 2);
-            mbar_init(&bars[B_VEMPTY + i], 1);
+            mbar_init(&bars[B_KEMPTY + i], 2);
+            mbar_init(&bars[B_VFULL + i], 4);
+            mbar_init(&bars[B_VEMPTY + i], 2);
+            mbar_init(&bars[B_AFULL + i], 1);
         }
         for (int i = 0; i < kInfoStages; ++i) {
             mbar_init(&bars[B_IFULL + i], 1);
             mbar_init(&bars[B_IEMPTY + i], kInfoConsumers);
         }
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < 4; ++t) {
             mbar_init(&bars[B_SFULL + t], 1);
             mbar_init(&bars[B_PFULL + t], 4);
             mbar_init(&bars[B_ODONE + t], 1);
         }
         mbar_init(&bars[B_QFULL], 1);
         mbar_init(&bars[B_DRAIN], 1);
+        mbar_init(&bars[B_DRAIN + 1], 1);
         *abort_flag = 0;
         if (mt == 0 && kvh == 0 && n_all > p.max_words) set_status(p.d_status, LAZY_DSTATUS_BAD_TABLE);
         fence_barrier_init();
@@ -209,18 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
         const bool leader = tc::elect_one();
         if (warp == 0) {
             // ======================================================== table walk and code copies
-            int j = 0, n_kc = 0, n_vc = 0;   // tiles, K and V copies issued
+            int j = 0, n_kc = 0;   // tiles whose V, K copies were issued
             bool ok = true;
-            int n_v = 0;        // tile n_vc: its blocks, and this lane's block
-            size_t bh_v = 0;
-            auto load_v = [&]() {
-                if (!warp_wait(&bars[B_VCEMPTY], (n_vc & 1) ^ 1, abort_flag, p.d_status)) return false;
-                if (leader) mbar_arrive_expect_tx(&bars[B_VCFULL], n_v * kCodeBlock);
-                __syncwarp();
-                if (lane < n_v) bulk_load(sm + kOffVC + lane * kCodeBlock, P.v_codes + bh_v * kCodeBlock, kCodeBlock, &bars[B_VCFULL]);
-                ++n_vc;
-                return true;
-            };
             // 32 words at a time, one per lane, with their blocks' metadata and scales: three dependent loads
             // serve up to four tiles
             uint32_t wl = 0u, mt_l = 0u, seen = 0u;
@@ -291,14 +285,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
                 __syncwarp();
                 if (lane < n) bulk_load(sm + kOffKC + lane * kCodeBlock, P.k_codes + bh * kCodeBlock, kCodeBlock, &bars[B_KCFULL]);
                 ++n_kc;
-                // V one tile behind, so that the record of tile j never waits for the V of tile j - 2
-                if (j > 0 && !(ok = load_v())) break;
-                n_v = n;
-                bh_v = bh;
+                ok = warp_wait(&bars[B_VCEMPTY], (j & 1) ^ 1, abort_flag, p.d_status);
+                if (!ok) break;
+                if (leader) mbar_arrive_expect_tx(&bars[B_VCFULL], n * kCodeBlock);
+                __syncwarp();
+                if (lane < n) bulk_load(sm + kOffVC + lane * kCodeBlock, P.v_codes + bh * kCodeBlock, kCodeBlock, &bars[B_VCFULL]);
                 ++j;
                 w += n;
             }
-            if (ok && j > 0) ok = load_v();
             if (ok) {
                 const int is = j % kInfoStages;
                 if (warp_wait(&bars[B_IEMPTY + is], ((j / kInfoStages) & 1) ^ 1, abort_flag, p.d_status)) {
@@ -311,75 +305,98 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
             }
             // every copy lands before the kernel can end, whatever stopped the walk
             if (n_kc > 0) mbar_wait(&bars[B_KCFULL], (n_kc - 1) & 1);
-            if (n_vc > 0) mbar_wait(&bars[B_VCFULL], (n_vc - 1) & 1);
-        } else if (warp == 2) {
-            // ======================================================== MMA issuer
-            // Order: QK_0(0) QK_1(0) | PV_0(0) QK_0(1) | PV_1(0) QK_1(1) | PV_0(1) QK_0(2) | ...
-            // One row tile's softmax runs while the tensor core works on the other's MMAs;
-            // QK_t(j + 1) follows PV_t(j) in issue order, which is what lets P_t live in S_t.
-            constexpr uint32_t idq = idesc_f16(false), idv = idesc_f16(true);
-            const uint64_t dQ = tc::smem_desc(smem_u32(sm + kOffQ), 16, 1024), dK0 = tc::smem_desc(smem_u32(sm + kOffK), 16, 1024);
+            if (j > 0) mbar_wait(&bars[B_VCFULL], (j - 1) & 1);
+        } else if (warp < 3) {
+            // ======================================================== MMA issuers (warp 2: row tile 0, warp 1: row tile 1)
+            // Step i is half a tile (64 keys), its scores in buffer i & 1:
+            //   QK(0) QK(1) | PV(0) QK(2) | PV(1) QK(3) | ...
+            // Scores are a step ahead of the softmax, so that neither it nor the tensor core waits for a round
+            // trip.  QK(i + 2) follows PV(i) in issue order, which lets P(i) live in S(i).  One warp per row
+            // tile: a step's waits and issues take one warp longer than the products themselves.
+            const int t = warp == 2 ? 0 : 1;
+            constexpr uint32_t idq = idesc_f16(64, false), idv = idesc_f16(128, true);
+            const uint64_t dQ = tc::smem_desc(smem_u32(sm + kOffQ + t * kTileBytes), 16, 1024);
+            const uint64_t dK0 = tc::smem_desc(smem_u32(sm + kOffK), 16, 1024);
             const uint64_t dV0 = tc::smem_desc(smem_u32(sm + kOffV), kHalfPlane, 1024);
-            auto qk = [&](int t, int stage) {
-                const uint64_t qb = dQ + static_cast<uint64_t>((t * kTileBytes) >> 4);
-                const uint64_t kb = dK0 + static_cast<uint64_t>((stage * kTileBytes) >> 4);
+            const uint32_t tS = tbase + 128 * t, tO = tbase + kColO + 128 * t;
+            // a step: blocks (0 ends the walk), and stage | half << 1 | (last of its tile) << 2
+            struct Step {
+                int n, at;
+            };
+            int tj = -1, tn = 0, th = 0;
+            bool ok = true;
+            auto fetch = [&]() {
+                if (tn > 4 * (th + 1)) {
+                    ++th;
+                } else {
+                    ++tj;
+                    th = 0;
+                    // the conversion warps have read the tile's record before they signal its keys
+                    ok = warp_wait(&bars[B_KFULL + tj % kStages], (tj / kStages) & 1, abort_flag, p.d_status);
+                    const int is = tj % kInfoStages;
+                    tn = ok ? info[is].n : 0;
+                    __syncwarp();
+                    if (leader) mbar_arrive(&bars[B_IEMPTY + is]);
+                    tc::fence_after_sync();
+                }
+                return Step{min(4, tn - 4 * th), (tj % kStages) | th << 1 | (tn <= 4 * (th + 1) ? 4 : 0)};
+            };
+            auto qk = [&](int buf, const Step &st) {
+                const uint64_t kb = dK0 + static_cast<uint64_t>(((st.at & 1) * kTileBytes + ((st.at >> 1) & 1) * 64 * 128) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
                     const uint64_t o = static_cast<uint64_t>(((kk >> 2) * kHalfPlane + (kk & 3) * 32) >> 4);
-                    tc::mma_ss(tbase + 128 * t, qb + o, kb + o, idq, kk > 0 ? 1u : 0u);
+                    tc::mma_ss(tS + 64 * buf, dQ + o, kb + o, idq, kk > 0 ? 1u : 0u);
                 }
-                tc::commit(&bars[B_SFULL + t]);
-                if (t == 1) tc::commit(&bars[B_KEMPTY + stage]);
+                tc::commit(&bars[B_SFULL + 2 * t + buf]);
+                if (st.at & 4) tc::commit(&bars[B_KEMPTY + (st.at & 1)]);
             };
-            int n = 0;
-            bool ok = warp_wait(&bars[B_QFULL], 0, abort_flag, p.d_status) && warp_wait(&bars[B_IFULL], 0, abort_flag, p.d_status);
-            if (ok) {
-                n = info[0].n;
-                __syncwarp();
-                if (leader) mbar_arrive(&bars[B_IEMPTY]);
-                if (n > 0) {
-                    ok = warp_wait(&bars[B_KFULL], 0, abort_flag, p.d_status);
-                    tc::fence_after_sync();
-                    if (ok && leader) {
-                        qk(0, 0);
-                        qk(1, 0);
-                    }
+            Step s0 = {0, 0}, s1 = {0, 0};
+            if (warp_wait(&bars[B_QFULL], 0, abort_flag, p.d_status)) {
+                s0 = fetch();
+                if (s0.n > 0) {
+                    if (leader) qk(0, s0);
+                    __syncwarp();
+                    s1 = fetch();
+                    if (leader && s1.n > 0) qk(1, s1);
                     __syncwarp();
                 }
             }
-            for (int j = 0; ok && n > 0; ++j) {
-                const int is = (j + 1) % kInfoStages, ksn = (j + 1) % kStages, vs = j % kStages;
-                if (!warp_wait(&bars[B_IFULL + is], ((j + 1) / kInfoStages) & 1, abort_flag, p.d_status)) break;
-                const int n_next = info[is].n;
+            int vj = 0;   // tile of step s0
+            for (int i = 0; s0.n > 0; ++i) {
+                const int buf = i & 1, vs = s0.at & 1, half = (s0.at >> 1) & 1;
+                if (half == 0 && !warp_wait(&bars[B_VFULL + vs], (vj / kStages) & 1, abort_flag, p.d_status)) break;
+                if (!warp_wait(&bars[B_PFULL + 2 * t + buf], (i >> 1) & 1, abort_flag, p.d_status)) break;
+                tc::fence_after_sync();
+                if (leader) {
+                    const uint64_t vb = dV0 + static_cast<uint64_t>((vs * kTileBytes + half * 4 * kBoxBytes) >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < s0.n)
+                            tc::mma_ts(tO, tS + 64 * buf + 8 * k, vb + static_cast<uint64_t>((k * kBoxBytes) >> 4), idv,
+                                       (i > 0 || k > 0) ? 1u : 0u);
+                    // one barrier per buffer: S(i) full says that PV(i - 2) is done, so a wait for PV(i - 1)
+                    // meets a barrier at most one phase behind
+                    tc::commit(&bars[B_ODONE + 2 * t + buf]);
+                    if (s0.at & 4) tc::commit(&bars[B_VEMPTY + vs]);
+                }
                 __syncwarp();
-                if (leader) mbar_arrive(&bars[B_IEMPTY + is]);
-                if (n_next > 0 && !warp_wait(&bars[B_KFULL + ksn], ((j + 1) / kStages) & 1, abort_flag, p.d_status)) break;
-                if (!warp_wait(&bars[B_VFULL + vs], (j / kStages) & 1, abort_flag, p.d_status)) break;
-                const uint64_t vb = dV0 + static_cast<uint64_t>((vs * kTileBytes) >> 4);
-#pragma unroll 1
-                for (int t = 0; t < 2; ++t) {
-                    ok = warp_wait(&bars[B_PFULL + t], j & 1, abort_flag, p.d_status);
+                if (s0.at & 4) ++vj;
+                s0 = s1;
+                if (s1.n > 0) {
+                    s1 = fetch();
                     if (!ok) break;
-                    tc::fence_after_sync();
-                    if (leader) {
-                        for (int k = 0; k < n; ++k)
-                            tc::mma_ts(tbase + 256 + 128 * t, tbase + 128 * t + 8 * k,
-                                       vb + static_cast<uint64_t>((k * kBoxBytes) >> 4), idv, (j > 0 || k > 0) ? 1u : 0u);
-                        tc::commit(&bars[B_ODONE + t]);
-                        if (t == 1) tc::commit(&bars[B_VEMPTY + vs]);
-                        if (n_next > 0) qk(t, ksn);
-                    }
+                    if (leader && s1.n > 0) qk(buf, s1);
                     __syncwarp();
                 }
-                n = n_next;
             }
             // every MMA has completed before tensor memory is freed
-            if (leader) tc::commit(&bars[B_DRAIN]);
+            if (leader) tc::commit(&bars[B_DRAIN + t]);
             __syncwarp();
-            mbar_wait(&bars[B_DRAIN], 0);
+            mbar_wait(&bars[B_DRAIN + t], 0);
         } else {
-            // ======================================================== query tiles, angles, V codes (warps 1 and 3)
-            if (warp == 3 && leader) {
+            // ======================================================== query tiles and angles
+            if (leader) {
                 mbar_arrive_expect_tx(&bars[B_QFULL], 2 * kTileBytes);
                 const uint16_t *q = p.q_prep + unit_rows(p, mt, kvh, r) * kHeadDim;
 #pragma unroll
@@ -387,79 +404,32 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
                     bulk_load(sm + kOffQ + t * kHalfPlane, q + t * (kHalfPlane / 2), kHalfPlane, &bars[B_QFULL]);
             }
             __syncwarp();
-            const int pair = (warp == 3 ? 32 : 0) + lane;
-            const double th = p.rope.theta[pair];
+            // tile j's angles into table j & 1, free since the K of tile j - 2 is done
+            const double th0 = p.rope.theta[lane], th1 = p.rope.theta[lane + 32];
             int cur = INT_MIN;
-            float c = 1.f, s = 0.f;
-            // angles of tile j (this warp's 32 pairs) into table j & 1, free since the K of tile j - 2 is done;
-            // returns the tile's blocks, -1 if a wait gave up
-            auto angles = [&](int j) -> int {
+            float c0 = 1.f, s0 = 0.f, c1 = 1.f, s1 = 0.f;
+            for (int j = 0;; ++j) {
                 const int is = j % kInfoStages, st = j % kStages;
-                if (!warp_wait(&bars[B_IFULL + is], (j / kInfoStages) & 1, abort_flag, p.d_status)) return -1;
+                if (!warp_wait(&bars[B_IFULL + is], (j / kInfoStages) & 1, abort_flag, p.d_status)) break;
                 const int n = info[is].n, off = info[is].off;
-                if (n == 0) return 0;
-                if (off != cur) {
-                    cur = off;
-                    rope_cos_sin(off - Pbase, th, c, s);
-                }
-                if (!warp_wait(&bars[B_KFULL + st], ((j / kStages) & 1) ^ 1, abort_flag, p.d_status)) return -1;
-                __half *tab = reinterpret_cast<__half *>(sm + kOffAngle + st * 256);
-                tab[pair] = __float2half_rn(c);
-                tab[kHalfDim + pair] = __float2half_rn(s);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[B_AFULL + st]);
-                return n;
-            };
-            // V: thread (ch, rb) takes dims 16 ch .. + 15 of slots rb and rb + 8 of every block
-            const int ch = lane & 7, rb = (lane >> 3) + (warp == 3 ? 4 : 0);
-            const uint8_t *vc = sm + kOffVC + rb * kHeadDim + 16 * ch;
-            const uint32_t vrow = (ch >> 2) * kHalfPlane + rb * 128;
-            const uint32_t v0 = vrow + (((2 * (ch & 3)) ^ rb) << 4), v1 = vrow + (((2 * (ch & 3) + 1) ^ rb) << 4);
-            int n = angles(0);
-            for (int j = 0; n > 0; ++j) {
-                const int is = j % kInfoStages, st = j % kStages;
-                const int n_next = angles(j + 1);
-                const TileInfo &ti = info[is];
-                uint32_t keep = 0u;   // bit k, bit 8 + k: some row may see slot rb, rb + 8 of block k
-#pragma unroll
-                for (int k = 0; k < kTileBlocks; ++k) {
-                    const int lim = min(meta_valid(ti.meta[k]), Plast - ti.off - meta_j0(ti.meta[k]) + 1);
-                    keep |= (rb < lim ? 1u << k : 0u) | (rb + 8 < lim ? 256u << k : 0u);
-                }
+                if (n == 0) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_IEMPTY + is]);
-                if (!warp_wait(&bars[B_VCFULL], j & 1, abort_flag, p.d_status)) break;
-                if (!warp_wait(&bars[B_VEMPTY + st], ((j / kStages) & 1) ^ 1, abort_flag, p.d_status)) break;
-                uint8_t *vt = sm + kOffV + st * kTileBytes;
-                // blocks behind the tile's last hold old codes that no MMA reads
-#pragma unroll
-                for (int k0 = 0; k0 < kTileBlocks; k0 += 2) {
-                    uint4 w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = *reinterpret_cast<const uint4 *>(vc + (k0 + (k >> 1)) * kCodeBlock + (k & 1) * 8 * kHeadDim);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (!((keep >> (k0 + (k >> 1) + 8 * (k & 1))) & 1u)) w[k] = make_uint4(0, 0, 0, 0);   // 0 * NaN
-                        uint4 x, y;
-                        codes_to_f16(w[k].x, x.x, x.y);
-                        codes_to_f16(w[k].y, x.z, x.w);
-                        codes_to_f16(w[k].z, y.x, y.y);
-                        codes_to_f16(w[k].w, y.z, y.w);
-                        uint8_t *vd = vt + (k0 + (k >> 1)) * kBoxBytes + (k & 1) * 1024;
-                        *reinterpret_cast<uint4 *>(vd + v0) = x;
-                        *reinterpret_cast<uint4 *>(vd + v1) = y;
-                    }
+                if (off != cur) {
+                    cur = off;
+                    rope_cos_sin(off - Pbase, th0, c0, s0);
+                    rope_cos_sin(off - Pbase, th1, c1, s1);
                 }
-                fence_proxy_async_smem();   // generic writes become visible to the tensor core
+                if (!warp_wait(&bars[B_KFULL + st], ((j / kStages) & 1) ^ 1, abort_flag, p.d_status)) break;
+                __half *tab = reinterpret_cast<__half *>(sm + kOffAngle + st * 256);
+                tab[lane] = __float2half_rn(c0);
+                tab[lane + 32] = __float2half_rn(c1);
+                tab[kHalfDim + lane] = __float2half_rn(s0);
+                tab[kHalfDim + lane + 32] = __float2half_rn(s1);
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bars[B_VCEMPTY]);
-                    mbar_arrive(&bars[B_VFULL + st]);
-                }
-                n = n_next;
+                if (lane == 0) mbar_arrive(&bars[B_AFULL + st]);
             }
-            if (warp == 3) mbar_wait(&bars[B_QFULL], 0);   // landed before the kernel can end
+            mbar_wait(&bars[B_QFULL], 0);   // landed before the kernel can end
         }
     } else if (warp < 12) {
         // ============================================================ softmax (one row per thread)
@@ -473,65 +443,56 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
         const float slope = ALIBI ? slope_s[g] : 0.f;
         const float hm = P.row_scale[unit_rows(p, mt, kvh, r) + kTileRows * t + row];   // softmax scale log2(e) 2^e
         const uint32_t lane_off = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t tS = tbase + 128 * t, tO = tbase + 256 + 128 * t;
+        const uint32_t tS = tbase + 128 * t + lane_off, tO = tbase + kColO + 128 * t + lane_off;
         float m_run = -INFINITY, l_run = 0.f, mo = -INFINITY;
-        int j = 0;
+        int i = 0;   // steps of 64 keys
         bool ok = true;
-        for (;; ++j) {
+        for (int j = 0; ok; ++j) {
             const int is = j % kInfoStages;
             ok = warp_wait(&bars[B_IFULL + is], (j / kInfoStages) & 1, abort_flag, p.d_status);
             if (!ok) break;
             const TileInfo &ti = info[is];
             const int n = ti.n;
             if (n == 0) break;
-            // visible keys of each block for this row, five bits per block
-            uint64_t limp = 0;
-            if (!ti.full) {
-#pragma unroll
-                for (int k = 0; k < kTileBlocks; ++k) {
-                    const int nv = k < n ? meta_valid(ti.meta[k]) : 0;
-                    limp |= static_cast<uint64_t>(max(0, min(nv, prow - ti.off - meta_j0(ti.meta[k]) + 1))) << (5 * k);
-                }
-            }
-            ok = warp_wait(&bars[B_SFULL + t], j & 1, abort_flag, p.d_status);
-            if (!ok) break;
-            tc::fence_after_sync();
-            // The row in two halves of 64 columns, first for its maxima and again for the weights: tensor
-            // memory is read twice, but the loop is a quarter of the code of one over all 128 columns in
-            // registers, whose instructions did not fit the cache beside the other roles'.
-            uint32_t sv[64];
-            auto f = [&](int c) { return __uint_as_float(sv[c]); };
-            auto load = [&](int h) {
-                tc::ld32(tS + lane_off + 64 * h, *reinterpret_cast<uint32_t(*)[32]>(sv));
-                tc::ld32(tS + lane_off + 64 * h + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+#pragma unroll 1
+            for (int k0 = 0; k0 < n; k0 += 4, ++i) {
+                const int buf = i & 1;
+                ok = warp_wait(&bars[B_SFULL + 2 * t + buf], (i >> 1) & 1, abort_flag, p.d_status);
+                if (!ok) break;
+                tc::fence_after_sync();
+                uint32_t sv[64];
+                tc::ld32(tS + 64 * buf, *reinterpret_cast<uint32_t(*)[32]>(sv));
+                tc::ld32(tS + 64 * buf + 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32));
+                const float4 ks4 = *reinterpret_cast<const float4 *>(&ti.ks[k0]), lv4 = *reinterpret_cast<const float4 *>(&ti.lv[k0]);
+                const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
                 tc::wait_ld();
+                auto f = [&sv](int c) { return __uint_as_float(sv[c]); };
                 if (ALIBI) {
                     // scores with the in-block part of the bias; the block part joins the maxima and offsets
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float fk = ti.ks[4 * h + k] * hm;
+                        const float fk = ks[k] * hm;
 #pragma unroll
                         for (int c = 16 * k; c < 16 * k + 16; ++c)
                             sv[c] = __float_as_uint(fmaf(f(c), fk, slope * static_cast<float>(c & 15)));
                     }
                 }
                 if (!ti.full) {
-                    const uint32_t l4 = static_cast<uint32_t>(limp >> (20 * h));
+                    // slots that this row sees of each block; blocks behind the tile's last have none
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int lim = static_cast<int>((l4 >> (5 * k)) & 31u);
+                        const uint32_t m = ti.meta[k0 + k];
+                        const int lim = min(meta_valid(m), prow - ti.off - meta_j0(m) + 1);
 #pragma unroll
                         for (int c = 16 * k; c < 16 * k + 16; ++c) sv[c] = (c & 15) < lim ? sv[c] : 0xFF800000u;
                     }
                 }
-            };
-            // factor of a block's scores; at least the smallest normal number, so that -inf stays -inf
-            auto factor = [&](int k) { return ALIBI ? 1.f : fmaxf(ti.ks[k] * hm, 0x1p-126f); };
-            auto bias = [&](int k) { return ALIBI ? slope * static_cast<float>(ti.off + meta_j0(ti.meta[k]) - prow) : 0.f; };
-            float m_new = m_run, mo_new = -INFINITY;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                load(h);
+                // factor of a block's scores; at least the smallest normal number, so that -inf stays -inf
+                auto factor = [&](int k) { return ALIBI ? 1.f : fmaxf(ks[k] * hm, 0x1p-126f); };
+                auto bias = [&](int k) {
+                    return ALIBI ? slope * static_cast<float>(ti.off + meta_j0(ti.meta[k0 + k]) - prow) : 0.f;
+                };
+                float m_new = m_run, mo_new = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float a = max3(f(16 * k), f(16 * k + 1), f(16 * k + 2)), b = f(16 * k + 15);
@@ -540,31 +501,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
                         a = max3(a, f(16 * k + c), f(16 * k + c + 1));
                         b = max3(b, f(16 * k + c + 2), f(16 * k + c + 3));
                     }
-                    const float s = fmaf(fmaxf(a, b), factor(4 * h + k), bias(4 * h + k));
+                    const float s = fmaf(fmaxf(a, b), factor(k), bias(k));
                     m_new = fmaxf(m_new, s);
-                    mo_new = fmaxf(mo_new, s + ti.lv[4 * h + k]);
+                    mo_new = fmaxf(mo_new, s + lv[k]);
                 }
-            }
-            const float mu = m_new == -INFINITY ? 0.f : m_new;
-            if (m_new != m_run) {
-                l_run *= fast_exp2(m_run - mu);
-                m_run = m_new;
-            }
-            const bool need = mo_new > mo + kRescaleThreshold;
-            float scale = 1.f;
-            if (need) {
-                scale = fast_exp2(mo - mo_new);
-                mo = mo_new;
-            }
-            const float mou = mo == -INFINITY ? 0.f : mo;
-            float ls0 = 0.f, ls1 = 0.f;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                load(h);
+                const float mu = m_new == -INFINITY ? 0.f : m_new;
+                if (m_new != m_run) {
+                    l_run *= fast_exp2(m_run - mu);
+                    m_run = m_new;
+                }
+                const bool need = mo_new > mo + kRescaleThreshold;
+                float scale = 1.f;
+                if (need) {
+                    scale = fast_exp2(mo - mo_new);
+                    mo = mo_new;
+                }
+                const float mou = mo == -INFINITY ? 0.f : mo;
+                float ls0 = 0.f, ls1 = 0.f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float fk = factor(4 * h + k), nm = bias(4 * h + k) - mu;
-                    const float F = fast_exp2(fminf(mu + ti.lv[4 * h + k] - mou, 126.f));
+                    const float fk = factor(k), nm = bias(k) - mu;
+                    const float F = fast_exp2(fminf(mu + lv[k] - mou, 126.f));
 #pragma unroll
                     for (int e = 8 * k; e < 8 * k + 8; ++e) {
                         float x0, x1;
@@ -575,31 +532,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
                         sv[e] = pack_h2(p0, p1);
                     }
                 }
-                // P over columns of S that have been read
-                tc::st32(tS + lane_off + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(sv));
+                l_run += ls0 + ls1;
+                tc::st32(tS + 64 * buf, *reinterpret_cast<uint32_t(*)[32]>(sv));
+                if (i > 0 && __any_sync(0xffffffffu, need)) {
+                    ok = warp_wait(&bars[B_ODONE + 2 * t + (buf ^ 1)], ((i - 1) >> 1) & 1, abort_flag, p.d_status);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tc::ld32(tO + 32 * c, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+                        tc::st32(tO + 32 * c, o);
+                    }
+                }
+                tc::wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_PFULL + 2 * t + buf]);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_IEMPTY + is]);
-            l_run += ls0 + ls1;
-            if (j > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tc::ld32(tO + lane_off + 32 * c, o);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
-                    tc::st32(tO + lane_off + 32 * c, o);
-                }
-            }
-            tc::wait_st();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_PFULL + t]);
         }
         // ------------------------------------------------------------ epilogue: O 2^(mo - m) / l
-        bool have = ok && j > 0;
-        if (have) have = warp_wait(&bars[B_ODONE + t], (j - 1) & 1, abort_flag, p.d_status);
+        bool have = ok && i > 0;
+        if (have) have = warp_wait(&bars[B_ODONE + 2 * t + ((i - 1) & 1)], ((i - 1) >> 1) & 1, abort_flag, p.d_status);
         have = __all_sync(0xffffffffu, have);
         if (have) tc::fence_after_sync();
         const bool some = have && m_run != -INFINITY;
@@ -619,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
         for (int c = 0; c < 4; ++c) {
             uint32_t ob[32];
             if (have) {
-                tc::ld32(tO + lane_off + 32 * c, ob);
+                tc::ld32(tO + 32 * c, ob);
                 tc::wait_ld();
             }
 #pragma unroll
@@ -641,58 +600,101 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
             }
         }
     } else {
-        // ============================================================ K codes to rotated f16 tiles
-        // thread (ch, rb): pairs 8 ch .. + 7 of slot rb of every block.  (a, b) -> (a c - b s, b c + a s) in f16
+        // ============================================================ codes to f16 operand tiles
+        // Thread (ch, rb) takes elements 8 ch .. + 7 (a) and 64 above (b) of slot rb of every block.  Where rb is
+        // odd b is loaded first: two rows' 8-byte loads then cover all banks.  K: (a, b) -> (a c - b s, b c + a s);
+        // with b in a's place the same formulas with -s give b c + a s first.
         const int tid = threadIdx.x - 384;
-        const int ch = tid & 7, rb = tid >> 3;
-        const uint8_t *kc = sm + kOffKC + rb * kHeadDim + 8 * ch;
-        const uint32_t ksw = rb * 128 + ((ch ^ (rb & 7)) << 4);
+        const int ch = tid & 7, rb = tid >> 3, up = rb & 1;
+        const uint32_t at = rb * kHeadDim + 8 * ch;                        // in a block's codes
+        const uint32_t sw = rb * 128 + ((ch ^ (rb & 7)) << 4);             // in a half plane of its operand tile
+        const uint32_t flip = up ? 0x80008000u : 0u;
+        const uint8_t *kc = sm + kOffKC + at, *vc = sm + kOffVC + at;
+        const int first = up * kHalfDim, second = kHalfDim - first;
         for (int j = 0;; ++j) {
             const int is = j % kInfoStages, st = j % kStages;
             if (!warp_wait(&bars[B_IFULL + is], (j / kInfoStages) & 1, abort_flag, p.d_status)) break;
-            const int n = info[is].n;
-            if (n == 0) break;
+            const TileInfo &ti = info[is];
+            if (ti.n == 0) {
+                // the end, for the MMA issuers
+                if (lane == 0) mbar_arrive(&bars[B_KFULL + st]);
+                break;
+            }
+            uint32_t keep = 0u;   // bit k: some row may see slot rb of block k
+#pragma unroll
+            for (int k = 0; k < kTileBlocks; ++k)
+                keep |= (rb < min(meta_valid(ti.meta[k]), Plast - ti.off - meta_j0(ti.meta[k]) + 1) ? 1u : 0u) << k;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_IEMPTY + is]);
             if (!warp_wait(&bars[B_AFULL + st], (j / kStages) & 1, abort_flag, p.d_status)) break;
             const uint4 c4 = *reinterpret_cast<const uint4 *>(sm + kOffAngle + st * 256 + 16 * ch);
             const uint4 s4 = *reinterpret_cast<const uint4 *>(sm + kOffAngle + st * 256 + 128 + 16 * ch);
-            const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+            const uint32_t c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x ^ flip, s4.y ^ flip, s4.z ^ flip, s4.w ^ flip};
             if (!warp_wait(&bars[B_KCFULL], j & 1, abort_flag, p.d_status)) break;
             if (!warp_wait(&bars[B_KEMPTY + st], ((j / kStages) & 1) ^ 1, abort_flag, p.d_status)) break;
-            uint8_t *kt = sm + kOffK + st * kTileBytes;
+            uint8_t *kt = sm + kOffK + st * kTileBytes + sw;
             // all 8 blocks (those behind the tile's last hold old codes, whose scores are masked), loads
             // ahead of the stores they could otherwise not pass
 #pragma unroll
             for (int k0 = 0; k0 < kTileBlocks; k0 += 4) {
-                uint2 lo[4], hi[4];
+                uint2 x[4], y[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    lo[k] = *reinterpret_cast<const uint2 *>(kc + (k0 + k) * kCodeBlock);
-                    hi[k] = *reinterpret_cast<const uint2 *>(kc + (k0 + k) * kCodeBlock + kHalfDim);
+                    x[k] = *reinterpret_cast<const uint2 *>(kc + (k0 + k) * kCodeBlock + first);
+                    y[k] = *reinterpret_cast<const uint2 *>(kc + (k0 + k) * kCodeBlock + second);
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    uint32_t a[4], b[4], ol[4], oh[4];
-                    codes_to_f16(lo[k].x, a[0], a[1]);
-                    codes_to_f16(lo[k].y, a[2], a[3]);
-                    codes_to_f16(hi[k].x, b[0], b[1]);
-                    codes_to_f16(hi[k].y, b[2], b[3]);
+                    uint32_t a[4], b[4], oa[4], ob[4];
+                    codes_to_f16(x[k].x, a[0], a[1]);
+                    codes_to_f16(x[k].y, a[2], a[3]);
+                    codes_to_f16(y[k].x, b[0], b[1]);
+                    codes_to_f16(y[k].y, b[2], b[3]);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        ol[x] = h2_fma(b[x], s[x] ^ 0x80008000u, h2_mul(a[x], c[x]));
-                        oh[x] = h2_fma(a[x], s[x], h2_mul(b[x], c[x]));
+                    for (int u = 0; u < 4; ++u) {
+                        oa[u] = h2_fma(b[u], s[u] ^ 0x80008000u, h2_mul(a[u], c[u]));
+                        ob[u] = h2_fma(a[u], s[u], h2_mul(b[u], c[u]));
                     }
-                    uint8_t *kd = kt + (k0 + k) * kBoxBytes + ksw;
-                    *reinterpret_cast<uint4 *>(kd) = make_uint4(ol[0], ol[1], ol[2], ol[3]);
-                    *reinterpret_cast<uint4 *>(kd + kHalfPlane) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+                    uint8_t *kd = kt + (k0 + k) * kBoxBytes;
+                    *reinterpret_cast<uint4 *>(kd + up * kHalfPlane) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
+                    *reinterpret_cast<uint4 *>(kd + (up ^ 1) * kHalfPlane) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
                 }
             }
-            fence_proxy_async_smem();
+            fence_proxy_async_smem();   // generic writes become visible to the tensor core
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&bars[B_KCEMPTY]);
                 mbar_arrive(&bars[B_KFULL + st]);
+            }
+            if (!warp_wait(&bars[B_VCFULL], j & 1, abort_flag, p.d_status)) break;
+            if (!warp_wait(&bars[B_VEMPTY + st], ((j / kStages) & 1) ^ 1, abort_flag, p.d_status)) break;
+            uint8_t *vt = sm + kOffV + st * kTileBytes + sw;
+            // (blocks behind the tile's last hold old codes that no MMA reads)
+#pragma unroll
+            for (int k0 = 0; k0 < kTileBlocks; k0 += 4) {
+                uint2 x[4][2];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    x[k][0] = *reinterpret_cast<const uint2 *>(vc + (k0 + k) * kCodeBlock + first);
+                    x[k][1] = *reinterpret_cast<const uint2 *>(vc + (k0 + k) * kCodeBlock + second);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint2 w = x[k][h];
+                        if (!((keep >> (k0 + k)) & 1u)) w = make_uint2(0u, 0u);   // a weight of 0 does not undo a NaN
+                        uint4 o;
+                        codes_to_f16(w.x, o.x, o.y);
+                        codes_to_f16(w.y, o.z, o.w);
+                        *reinterpret_cast<uint4 *>(vt + (k0 + k) * kBoxBytes + (up ^ h) * kHalfPlane) = o;
+                    }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars[B_VCEMPTY]);
+                mbar_arrive(&bars[B_VFULL + st]);
             }
         }
     }
