@@ -78,7 +78,7 @@ constexpr size_t kSmem = kOffSlope + 32 * 4 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kColO = 256;                  // tensor memory columns of O (S from 0)
 constexpr int kInfoConsumers = 15;          // 8 softmax, 2 MMA, 4 conversion warps, the angle warp
-constexpr float kRescaleThreshold = 8.0f;   // log2 units: P' stays below 2^8 between rescales of O
+constexpr float kSlack = 8.0f;   // log2 units by which a maximum may pass its reference
 
 // kind::f16 with f16 A/B and fp32 accumulation, M = 128.
 constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
                 auto bias = [&](int k) {
                     return ALIBI ? slope * static_cast<float>(ti.off + meta_j0(ti.meta[k0 + k]) - prow) : 0.f;
                 };
-                float m_new = m_run, mo_new = -INFINITY;
+                float m_new = -INFINITY, mo_new = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float a = max3(f(16 * k), f(16 * k + 1), f(16 * k + 2)), b = f(16 * k + 15);
@@ -505,34 +505,43 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
                     m_new = fmaxf(m_new, s);
                     mo_new = fmaxf(mo_new, s + lv[k]);
                 }
-                const float mu = m_new == -INFINITY ? 0.f : m_new;
-                if (m_new != m_run) {
-                    l_run *= fast_exp2(m_run - mu);
-                    m_run = m_new;
-                }
-                const bool need = mo_new > mo + kRescaleThreshold;
+                // References move only when the maxima pass them by kSlack (log2 units): weights stay below 2^8,
+                // and most steps need no rescaling.
+                const bool need = mo_new > mo + kSlack;
                 float scale = 1.f;
-                if (need) {
-                    scale = fast_exp2(mo - mo_new);
-                    mo = mo_new;
-                }
-                const float mou = mo == -INFINITY ? 0.f : mo;
-                float ls0 = 0.f, ls1 = 0.f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float fk = factor(k), nm = bias(k) - mu;
-                    const float F = fast_exp2(fminf(mu + lv[k] - mou, 126.f));
-#pragma unroll
-                    for (int e = 8 * k; e < 8 * k + 8; ++e) {
-                        float x0, x1;
-                        fma2v(x0, x1, f(2 * e), f(2 * e + 1), fk, fk, nm, nm);
-                        float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                        add2(ls0, ls1, p0, p1);
-                        mul2(p0, p1, p0, p1, F, F);
-                        sv[e] = pack_h2(p0, p1);
+                if (__any_sync(0xffffffffu, need || m_new > m_run + kSlack)) {
+                    m_new = fmaxf(m_new, m_run);
+                    if (m_new > m_run) {
+                        l_run *= fast_exp2(m_run - m_new);
+                        m_run = m_new;
+                    }
+                    if (need) {
+                        scale = fast_exp2(mo - mo_new);
+                        mo = mo_new;
                     }
                 }
-                l_run += ls0 + ls1;
+                const float mu = m_run == -INFINITY ? 0.f : m_run, mou = mo == -INFINITY ? 0.f : mo;
+                // Weights for the products, w' = 2^(s - m + e) with e = m + log2 s_v - r; the row sum takes a block's
+                // sum times 2^-e.  e is kept above -40, where w' is 0 in f16 either way: the sum of a block
+                // whose values are that much smaller than others still counts its weights.
+                float ls = 0.f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float e = fmaxf(mu + lv[k] - mou, -40.f);
+                    const float fk = factor(k), nm = bias(k) - mu + e;
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int c = 8 * k; c < 8 * k + 8; ++c) {
+                        float x0, x1;
+                        fma2v(x0, x1, f(2 * c), f(2 * c + 1), fk, fk, nm, nm);
+                        x0 = fast_exp2(x0);
+                        x1 = fast_exp2(x1);
+                        add2(s0, s1, x0, x1);
+                        sv[c] = pack_h2(x0, x1);
+                    }
+                    ls = fmaf(s0 + s1, fast_exp2(-e), ls);
+                }
+                l_run += ls;
                 tc::st32(tS + 64 * buf, *reinterpret_cast<uint32_t(*)[32]>(sv));
                 if (i > 0 && __any_sync(0xffffffffu, need)) {
                     ok = warp_wait(&bars[B_ODONE + 2 * t + (buf ^ 1)], ((i - 1) >> 1) & 1, abort_flag, p.d_status);
@@ -544,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
                         tc::ld32(tO + 32 * c, o);
                         tc::wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * scale);
+                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * scale);
                         tc::st32(tO + 32 * c, o);
                     }
                 }
