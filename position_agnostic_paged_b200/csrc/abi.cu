@@ -52,6 +52,19 @@ bool make_rows_map(CUtensorMap *map, const void *base, int64_t rows, int box_row
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// An 8-bit pool viewed as rows of 128 codes; boxes of one block of one head (16 rows), 128-byte swizzle.
+bool make_codes_map(CUtensorMap *map, const void *base, int64_t rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || rows <= 0) return false;
+    cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {128};
+    cuuint32_t box[2] = {128, 16};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The same pool viewed as (d, token, head, block): one box covers `box_blocks`
 // consecutive blocks of one head and one 64-element half (2 KiB per block), laid
 // out in shared memory exactly like that many single-block boxes stacked.
@@ -244,12 +257,15 @@ int lane_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_
     p.ws_ml = reinterpret_cast<float4 *>(p.a.ws_acc + rows * 128);
     p.ws_lse = reinterpret_cast<float *>(p.ws_ml + rows);
     p.mass = mass;
-    p.k = static_cast<const uint8_t *>(k);
-    p.v = static_cast<const uint8_t *>(v);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.warps_per_head = pl.warps_per_head;
-    return launch_rc(launch_decode_lane(p, q8, static_cast<cudaStream_t>(stream)));
+    CUtensorMap tk, tv;
+    const int64_t pool_rows = static_cast<int64_t>(num_blocks) * p.a.hkv * 16;
+    if (q8 ? !make_codes_map(&tk, k, pool_rows) || !make_codes_map(&tv, v, pool_rows)
+           : !make_rows_map(&tk, k, pool_rows) || !make_rows_map(&tv, v, pool_rows))
+        return LAZY_ECUDA;
+    return launch_rc(launch_decode_lane(tk, tv, p, q8, static_cast<cudaStream_t>(stream)));
 }
 
 int prefill_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *cu_q, const int32_t *q_pos0,

@@ -13,14 +13,15 @@
 // acc) to the workspace slot (warp + request), which is unique because each new partial moves on
 // to the next warp or the next request.  The second kernel joins a request's partials in order.
 //
-// Data path.  Every lane copies with cp.async exactly the 16-byte pieces it will feed to the
-// tensor cores itself, so a warp's stages are lane-private FIFOs: no barriers, no bank
-// conflicts, no producer warp.  The K index order of an MMA is free as long as both operands use
+// Data path.  Each warp is its own producer: lane 0 loads the warp's next words by TMA (128-byte
+// swizzle) into the warp's stages, so there are no barriers between warps.  (With cp.async the
+// loads of table words, and spilled registers, waited in the L1's queue behind all copies in flight:
+// 213 us for the 8B step below.)  The K index order of an MMA is free as long as both operands use
 // the same one, and so is the order of output rows; both are chosen to make a lane's share
-// contiguous:
-//   K (rows = keys as the A operand): lane (rr, c) takes 16-byte pieces c, c + 4, ... of key rows
-//     rr and rr + 8, a full 32-byte sector per two lanes;
-//   V^T (rows = head dims as the A operand): lane (rr, c) takes piece(s) rr of key rows 2c, 2c+1,
+// contiguous, and a quarter warp's 16-byte reads cover all banks:
+//   K (rows = keys as the A operand): lane (rr, c) takes 16-byte pieces 2c, 2c + 1 of each 128-byte
+//     row, key rows rr and rr + 8;
+//   V^T (rows = head dims as the A operand): lane (rr, c) takes piece rr of key rows 2c, 2c+1,
 //     2c+8, 2c+9 and pairs keys with byte permutes.
 // e4m3 codes become f16 (exact); the query is scaled by a power of two to [1, 2) and rounded to f16
 // (2^-12 of its largest element); weights are f16 against a running reference that includes the
@@ -39,14 +40,9 @@ namespace lazy {
 
 namespace {
 
-constexpr int kMinWords = 2;   // least words per warp
+constexpr int kMinWords = 2;       // least words per warp
+constexpr float kSlack = 8.f;      // log2 units by which a score may pass its reference
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -87,28 +83,29 @@ template <bool Q8, int NT, bool MASS>
 struct Cfg {
     static constexpr int QP = Q8 ? (MASS ? 2 : 1) : 3;
     static constexpr bool kRegQ = NT == 1;                     // query fragments in registers, else in shared memory
-    static constexpr int kPieces = Q8 ? 4 : 8;                 // 16-byte pieces of K (and of V) per lane and word
-    static constexpr int kStageBytes = 2 * kPieces * 512;
+    static constexpr int kTile = Q8 ? 2048 : 4096;             // bytes of K (and of V) per word
+    static constexpr int kStageBytes = 2 * kTile;
     static constexpr int kQBytes = kRegQ ? 0 : NT * QP * 8 * 32 * 8;      // query fragments per warp
-    static constexpr int kLeast = 2 * kStageBytes + kQBytes + 512;        // shared memory per warp, two stages
+    static constexpr int kExtra = kQBytes + 512 + 64;                     // query fragments, angles, barriers
+    static constexpr int kLeast = 2 * kStageBytes + kExtra;               // shared memory per warp, two stages
     // CTAs per SM by registers (4 warps each); where the query fragments leave no room for two stages of so
     // many warps (bf16 with block mass, G > 8): one CTA of as many warps as fit
     static constexpr int kOcc0 = NT == 4 ? 2 : (NT == 2 || !Q8) ? 3 : 4;
-    static constexpr bool kFits = kOcc0 * (4 * kLeast + 1024) <= 227 * 1024;
+    static constexpr bool kFits = kOcc0 * (4 * kLeast + 2048) <= 227 * 1024;
     static constexpr int kOcc = kFits ? kOcc0 : 1;
-    static constexpr int kWarps = kFits ? 4 : 226 * 1024 / kLeast;
-    static constexpr int kStages0 = ((227 * 1024 / kOcc - 1024) / kWarps - kQBytes - 512) / kStageBytes;
+    static constexpr int kWarps = kFits ? 4 : 225 * 1024 / kLeast;
+    static constexpr int kStages0 = ((227 * 1024 / kOcc - 2048) / kWarps - kExtra) / kStageBytes;
     static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
-    static constexpr int kWarpBytes = kStages * kStageBytes + kQBytes + 512;
-    static constexpr int kSmem = kWarps * kWarpBytes;
+    static constexpr int kSmem = kWarps * (kStages * kStageBytes + kExtra) + 1024;   // stages 1 KiB aligned
     static_assert(kStages >= 2 && kWarps <= 8, "pipeline depth");
 };
 
-// Head dims of the query fragment: register pair x of k-step s holds dims qdim(s) + {0, 1} and + {2, 3}
-// (s < 4; k-step s + 4 the dims 64 above: the rotation pairs).
+// First of the four head dims of the query fragment's registers for k-step s: codes hold 16 dims per piece,
+// so lane c has dims 32c .. + 31 and its rotation pairs lie in lane c ^ 2; bf16 rows are two halves of 64
+// dims, 16c .. + 15 of each, and pairs lie in k-steps s and s + 4.
 template <bool Q8>
 __device__ __forceinline__ int qdim(int s, int c) {
-    return Q8 ? 16 * c + 4 * s : 32 * (s >> 1) + 8 * c + 4 * (s & 1);
+    return Q8 ? 32 * c + 4 * s : 16 * c + 4 * (s & 3) + 64 * (s >> 2);
 }
 // First head dim of output tile t's row pair (rows rr and rr + 8 hold odim and odim + 1).
 template <bool Q8>
@@ -117,10 +114,13 @@ __device__ __forceinline__ int odim(int t, int rr) {
 }
 
 template <bool Q8, int NT, bool MASS>
-__global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT, MASS>::kOcc)) decode_lane_kernel(const LaneParams p) {
+__global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT, MASS>::kOcc))
+    decode_lane_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ LaneParams p) {
     using C = Cfg<Q8, NT, MASS>;
     constexpr int QP = C::QP, S = C::kStages, kWarps = C::kWarps;
-    extern __shared__ __align__(16) uint8_t smem_raw[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = lane & 3, rr = lane >> 2;
     const AttnParams &a = p.a;
@@ -135,74 +135,65 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
     if (wi > (total - 1) / per) return;
     const int lo = wi * per, cnt = min(total - lo, per);
 
-    uint8_t *ws = smem_raw + warp * C::kWarpBytes;
-    const uint32_t fifo = smem_u32(ws) + lane * 16;
-    uint2 *qs = reinterpret_cast<uint2 *>(ws + S * C::kStageBytes);              // [NT][QP][8][32]
-    float2 *cs = reinterpret_cast<float2 *>(ws + S * C::kStageBytes + C::kQBytes);   // [64]
+    uint8_t *stages = sm + warp * S * C::kStageBytes;
+    uint8_t *extra = sm + kWarps * S * C::kStageBytes + warp * C::kExtra;
+    uint2 *qs = reinterpret_cast<uint2 *>(extra);                              // [NT][QP][8][32]
+    float2 *cs = reinterpret_cast<float2 *>(extra + C::kQBytes);               // [64]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(extra + C::kQBytes + 512);   // [S]
+    if (lane < S) mbar_init(&bars[lane], 1);
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    __syncwarp();
 
-    // ---- the words of this warp, 32 at a time, one per lane
-    uint32_t w_cur = 0, m_cur = 0, w_nxt = 0, m_nxt = 0;
-    float ks_cur = 0.f, lv_cur = 0.f, ks_nxt = 0.f, lv_nxt = 0.f;
-    auto fetch = [&](int k0, uint32_t &w, uint32_t &m, float &ks, float &lv) {
-        w = 0u;
+    // ---- the words of this warp, 32 at a time, one per lane; metadata and scales are loaded a batch
+    // ahead of their use and words two, so that no load is waited for
+    uint32_t w_cur, m_cur, w_nxt, m_nxt, w_2nd;
+    float ks_cur, vs_cur, ks_nxt, vs_nxt;
+    auto word_at = [&](int k) { return k < cnt ? a.table[base + lo + k] : 0u; };
+    auto meta_at = [&](int k, uint32_t w, uint32_t &m, float &ks, float &vs) {
         m = 0u;
-        ks = 0.f;
-        lv = 0.f;
-        if (k0 + lane < cnt) {
-            w = a.table[base + lo + k0 + lane];
+        ks = vs = 1.f;
+        if (k < cnt) {
             const uint32_t b = word_block(w);
             if (b < static_cast<uint32_t>(a.num_blocks)) {
                 m = a.blk_meta[b];
                 if (Q8) {
                     ks = p.k_scale[static_cast<size_t>(b) * hkv + kvh];
-                    lv = fast_log2(p.v_scale[static_cast<size_t>(b) * hkv + kvh]);
+                    vs = p.v_scale[static_cast<size_t>(b) * hkv + kvh];
                 }
             } else {
                 set_status(a.d_status, LAZY_DSTATUS_BAD_BLOCK);
             }
         }
     };
-    fetch(0, w_cur, m_cur, ks_cur, lv_cur);
-    fetch(32, w_nxt, m_nxt, ks_nxt, lv_nxt);
+    w_cur = word_at(lane);
+    w_nxt = word_at(32 + lane);
+    w_2nd = word_at(64 + lane);
+    meta_at(lane, w_cur, m_cur, ks_cur, vs_cur);
+    meta_at(32 + lane, w_nxt, m_nxt, ks_nxt, vs_nxt);
 
-    const size_t k_lane = Q8 ? rr * 128 + c * 16 : rr * 256 + c * 16;
-    const size_t v_lane = Q8 ? c * 256 + rr * 16 : c * 512 + rr * 16;
-    constexpr size_t kTile = Q8 ? 2048 : 4096;
-    // copies of word k (of this warp) into stage k % S; `kb` is the batch that w_cur holds
+    // copies of word k (of this warp) into stage k % S; `kb` is the batch that w_cur holds.  A word without
+    // tokens, or without a block, completes its phase with no data.
     auto issue = [&](int k, int kb) {
         if (k < cnt) {
             const bool nx = (k >> 5) != kb;
             const uint32_t w = __shfl_sync(0xffffffffu, nx ? w_nxt : w_cur, k & 31);
             const uint32_t m = __shfl_sync(0xffffffffu, nx ? m_nxt : m_cur, k & 31);
-            if (meta_valid(m) > 0) {
-                const size_t tile = (static_cast<size_t>(word_block(w)) * hkv + kvh) * kTile;
-                const uint8_t *ks = p.k + tile + k_lane, *vs = p.v + tile + v_lane;
-                const uint32_t d = fifo + (k % S) * C::kStageBytes;
-                if (Q8) {
-                    cp16(d, ks);
-                    cp16(d + 512, ks + 64);
-                    cp16(d + 1024, ks + 1024);
-                    cp16(d + 1536, ks + 1088);
-                    cp16(d + 2048, vs);
-                    cp16(d + 2560, vs + 128);
-                    cp16(d + 3072, vs + 1024);
-                    cp16(d + 3584, vs + 1152);
+            if (lane == 0) {
+                uint64_t *bar = &bars[k % S];
+                if (meta_valid(m) > 0) {
+                    uint8_t *d = stages + (k % S) * C::kStageBytes;
+                    const int row = (static_cast<int>(word_block(w)) * hkv + kvh) * kBlockTokens;
+                    mbar_arrive_expect_tx(bar, C::kStageBytes);
+                    tma_load_2d(d, &tmK, 0, row, bar);
+                    if (!Q8) tma_load_2d(d + kBoxBytes, &tmK, kHalfDim, row, bar);
+                    tma_load_2d(d + C::kTile, &tmV, 0, row, bar);
+                    if (!Q8) tma_load_2d(d + C::kTile + kBoxBytes, &tmV, kHalfDim, row, bar);
                 } else {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        cp16(d + 512 * x, ks + 64 * x);
-                        cp16(d + 512 * (4 + x), ks + 2048 + 64 * x);
-                    }
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int row = (x & 1) * 256 + (x >> 1) * 2048;   // key rows 2c, 2c+1, 2c+8, 2c+9
-                        cp16(d + 4096 + 512 * x, vs + row);
-                        cp16(d + 4096 + 512 * (4 + x), vs + row + 128);
-                    }
+                    mbar_arrive(bar);
                 }
             }
         }
-        cp_commit();
     };
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) issue(k, 0);
@@ -220,7 +211,9 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             hi = min(hi, r + step);
         }
     }
-    const double th0 = a.rope.theta[lane], th1 = a.rope.theta[lane + 32];
+    // kept in registers: a per-lane read of the parameter table takes 32 turns
+    double th0 = a.rope.theta[lane], th1 = a.rope.theta[lane + 32];
+    asm volatile("" : "+d"(th0), "+d"(th1));
 
     int r_beg = a.table_indptr[r] - base, r_end = a.table_indptr[r + 1] - base;
     int qpos = 0, cur_off = -1;
@@ -245,7 +238,7 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             float am = 0.f;
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
-                const int d = qdim<Q8>(s & 3, c) + 64 * (s >> 2);
+                const int d = qdim<Q8>(s, c);
                 uint32_t w0 = 0u, w1 = 0u;
                 if (g < G) {
                     w0 = q[d >> 1];
@@ -294,27 +287,42 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             const int g = 8 * n + rr;
             const uint32_t *q = reinterpret_cast<const uint32_t *>(
                 a.q_raw + (static_cast<size_t>(r) * a.hq + kvh * G + min(g, G - 1)) * kHeadDim);
+            const float sg = c < 2 ? -1.f : 1.f;   // codes: of the partner's sine
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int d = qdim<Q8>(s, c);
+            for (int s = 0; s < 8; s += Q8 ? 2 : 1) {
+                if (!Q8 && s >= 4) break;
+                // two k-steps: codes s, s + 1; bf16 s, s + 4
+                const int t = Q8 ? s + 1 : s + 4;
                 float x[8];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    uint32_t wa, wb;
-                    if (C::kRegQ) {
-                        wa = qraw[s][y];
-                        wb = qraw[C::kRegQ ? s + 4 : 0][y];
+                for (int y = 0; y < 4; ++y) {
+                    const int st = y < 2 ? s : t, d = qdim<Q8>(st, c) + 2 * (y & 1);
+                    uint32_t w;
+                    if (C::kRegQ)
+                        w = qraw[C::kRegQ ? st : 0][y & 1];
+                    else
+                        w = g < G ? q[d >> 1] : 0u;
+                    const float4 z = *reinterpret_cast<const float4 *>(&cs[d & 63]);   // (cos, sin) of two pairs
+                    const float o0 = bf16_lo(w) * qn[n], o1 = bf16_hi(w) * qn[n];
+                    if (Q8) {
+                        const float p0 = __shfl_xor_sync(0xffffffffu, o0, 2), p1 = __shfl_xor_sync(0xffffffffu, o1, 2);
+                        x[2 * y] = o0 * z.x + sg * p0 * z.y;
+                        x[2 * y + 1] = o1 * z.z + sg * p1 * z.w;
                     } else {
-                        wa = g < G ? q[(d >> 1) + y] : 0u;
-                        wb = g < G ? q[(d >> 1) + y + 32] : 0u;
+                        x[2 * y] = o0;
+                        x[2 * y + 1] = o1;
                     }
-                    const float4 z = *reinterpret_cast<const float4 *>(&cs[d + 2 * y]);   // (cos, sin) of two pairs
-                    const float a0 = bf16_lo(wa) * qn[n], a1 = bf16_hi(wa) * qn[n];
-                    const float b0 = bf16_lo(wb) * qn[n], b1 = bf16_hi(wb) * qn[n];
-                    x[2 * y] = a0 * z.x - b0 * z.y;
-                    x[2 * y + 1] = a1 * z.z - b1 * z.w;
-                    x[4 + 2 * y] = b0 * z.x + a0 * z.y;
-                    x[4 + 2 * y + 1] = b1 * z.z + a1 * z.w;
+                }
+                if (!Q8) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float4 z = *reinterpret_cast<const float4 *>(&cs[qdim<Q8>(s, c) + 2 * y]);
+                        const float a0 = x[2 * y], a1 = x[2 * y + 1], b0 = x[4 + 2 * y], b1 = x[5 + 2 * y];
+                        x[2 * y] = a0 * z.x - b0 * z.y;
+                        x[2 * y + 1] = a1 * z.z - b1 * z.w;
+                        x[4 + 2 * y] = b0 * z.x + a0 * z.y;
+                        x[5 + 2 * y] = b1 * z.z + a1 * z.w;
+                    }
                 }
 #pragma unroll
                 for (int part = 0; part < QP; ++part) {
@@ -333,13 +341,13 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
                         }
                     }
                     if (C::kRegQ) {
-                        qb[part][s][0] = w[0];
-                        qb[part][s][1] = w[1];
-                        qb[part][C::kRegQ ? s + 4 : 0][0] = w[2];
-                        qb[part][C::kRegQ ? s + 4 : 0][1] = w[3];
+                        qb[part][C::kRegQ ? s : 0][0] = w[0];
+                        qb[part][C::kRegQ ? s : 0][1] = w[1];
+                        qb[part][C::kRegQ ? t : 0][0] = w[2];
+                        qb[part][C::kRegQ ? t : 0][1] = w[3];
                     } else {
                         qs[((n * QP + part) * 8 + s) * 32 + lane] = make_uint2(w[0], w[1]);
-                        qs[((n * QP + part) * 8 + s + 4) * 32 + lane] = make_uint2(w[2], w[3]);
+                        qs[((n * QP + part) * 8 + t) * 32 + lane] = make_uint2(w[2], w[3]);
                     }
                 }
             }
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
                         *reinterpret_cast<float4 *>(o + odim<Q8>(t, rr)) =
                             make_float4(oacc[n][t][j], oacc[n][t][j + 2], oacc[n][t + 1][j], oacc[n][t + 1][j + 2]);
                     }
-                    if (rr == 0) p.ws_ml[slot * G + g] = make_float4(m_run[n][j], l, Q8 ? mo[n][j] : m_run[n][j], 0.f);
+                    if (rr == 0) p.ws_ml[slot * G + g] = make_float4(m_run[n][j], l, mo[n][j], 0.f);
                 }
             }
     };
@@ -376,11 +384,18 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             w_cur = w_nxt;
             m_cur = m_nxt;
             ks_cur = ks_nxt;
-            lv_cur = lv_nxt;
-            fetch(k + 32, w_nxt, m_nxt, ks_nxt, lv_nxt);
+            vs_cur = vs_nxt;
+            w_nxt = w_2nd;
+            w_2nd = word_at(k + 64 + lane);
+            meta_at(k + 32 + lane, w_nxt, m_nxt, ks_nxt, vs_nxt);
         }
+        __syncwarp();   // every lane has read the stage that is loaded next
         issue(k + S - 1, k >> 5);
-        cp_wait<S - 1>();
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars[k % S], (k / S) & 1))) {
+            set_status(a.d_status, LAZY_DSTATUS_TIMEOUT);
+            for (int i = k; i < min(cnt, k + S); ++i) mbar_wait(&bars[i % S], (i / S) & 1);   // copies in flight
+            break;
+        }
         if (lo + k >= r_end) {
             end_request();
             do {
@@ -393,7 +408,7 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
         const uint32_t w = __shfl_sync(0xffffffffu, w_cur, k & 31);
         const uint32_t meta = __shfl_sync(0xffffffffu, m_cur, k & 31);
         const float ksc = Q8 ? __shfl_sync(0xffffffffu, ks_cur, k & 31) : 1.f;
-        const float lv = Q8 ? __shfl_sync(0xffffffffu, lv_cur, k & 31) : 0.f;
+        const float lv = Q8 ? fast_log2(__shfl_sync(0xffffffffu, vs_cur, k & 31)) : 0.f;
         const int i_req = lo + k - r_beg;                       // index of the word in its request
         const int off = word_offset(w);
         const int pos0 = off + meta_j0(meta);
@@ -406,15 +421,16 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
         }
         if (cur_off < 0 || (off != cur_off && !a.alibi)) rotate(off);
 
-        const uint32_t st = fifo + (k % S) * C::kStageBytes;
+        const uint32_t st = smem_u32(stages) + (k % S) * C::kStageBytes;
         // ---- S^T [16 keys][8 heads] = K q^T
         float sa[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) sa[n][0] = sa[n][1] = sa[n][2] = sa[n][3] = 0.f;
 #pragma unroll
-        for (int m = 0; m < C::kPieces / 2; ++m) {
-            // piece m of key rows rr and rr + 8: two (bf16) or four (e4m3) k-steps
-            const uint4 ra = lds16(st + 512 * m), rb = lds16(st + 512 * (C::kPieces / 2 + m));
+        for (int m = 0; m < (Q8 ? 2 : 4); ++m) {
+            // piece 2c + (m & 1) of key rows rr and rr + 8 (bf16: of half m >> 1): four or two k-steps
+            const uint32_t ka = st + (m >> 1) * kBoxBytes + rr * 128 + (((2 * c + (m & 1)) ^ rr) << 4);
+            const uint4 ra = lds16(ka), rb = lds16(ka + 1024);
             const uint32_t aw[4] = {ra.x, ra.y, ra.z, ra.w}, bw[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
             for (int u = 0; u < (Q8 ? 4 : 2); ++u) {
@@ -442,12 +458,14 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
                     }
             }
         }
-        // ---- softmax over the word's keys (rr and rr + 8 in this lane)
+        // ---- softmax over the word's keys (rr and rr + 8 in this lane).  References (m_run for the row sums, mo
+        // for score + log2 of the V scale) move only when some score passes them by kSlack: weights stay
+        // below 2^8 and most words need neither the maxima nor rescaling.
         const bool vis0 = rr < lim, vis1 = rr + 8 < lim;
         uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float bm[2];
+            bool past = false;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float f = hm[n][j] * ksc;
@@ -459,22 +477,19 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
                 }
                 sa[n][j] = vis0 ? s0 : -INFINITY;
                 sa[n][j + 2] = vis1 ? s1 : -INFINITY;
-                bm[j] = fmaxf(sa[n][j], sa[n][j + 2]);
+                const float top = fmaxf(sa[n][j], sa[n][j + 2]);
+                past |= top > m_run[n][j] + kSlack || (Q8 && top + lv > mo[n][j] + kSlack);
             }
+            if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-                bm[0] = fmaxf(bm[0], __shfl_xor_sync(0xffffffffu, bm[0], x));
-                bm[1] = fmaxf(bm[1], __shfl_xor_sync(0xffffffffu, bm[1], x));
-            }
-            float pr[4];
+                for (int j = 0; j < 2; ++j) {
+                    float bm = fmaxf(sa[n][j], sa[n][j + 2]);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float mn = fmaxf(m_run[n][j], bm[j]);
-                const float mu = mn == -INFINITY ? 0.f : mn;
-                if (mn != m_run[n][j]) {
-                    const float sc = fast_exp2(m_run[n][j] - mu);
-                    l_run[n][j] *= sc;
-                    if (!Q8) {
+                    for (int x = 4; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
+                    const float mn = fmaxf(m_run[n][j], bm), mon = Q8 ? fmaxf(mo[n][j], bm + lv) : mn;
+                    if (mn != m_run[n][j]) l_run[n][j] *= fast_exp2(m_run[n][j] - mn);
+                    if (mon != mo[n][j]) {
+                        const float sc = fast_exp2(mo[n][j] - mon);
 #pragma unroll
                         for (int t = 0; t < 8; ++t) {
                             oacc[n][t][j] *= sc;
@@ -482,7 +497,13 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
                         }
                     }
                     m_run[n][j] = mn;
+                    mo[n][j] = mon;
                 }
+            }
+            float pr[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float mu = m_run[n][j] == -INFINITY ? 0.f : m_run[n][j];
                 float p0 = fast_exp2(sa[n][j] - mu), p1 = fast_exp2(sa[n][j + 2] - mu);
                 float ps = p0 + p1;
                 if (MASS) {
@@ -493,18 +514,8 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
                 }
                 l_run[n][j] += ps;
                 if (Q8) {
-                    // weights for the V product, against the running maximum of score + log2(V scale)
-                    const float mon = fmaxf(mo[n][j], bm[j] + lv);
-                    const float mou = mon == -INFINITY ? 0.f : mon;
-                    if (mon != mo[n][j]) {
-                        const float sc = fast_exp2(mo[n][j] - mou);
-#pragma unroll
-                        for (int t = 0; t < 8; ++t) {
-                            oacc[n][t][j] *= sc;
-                            oacc[n][t][j + 2] *= sc;
-                        }
-                        mo[n][j] = mon;
-                    }
+                    // weights for the V product: w 2^(log2 s_v) against 2^mo
+                    const float mou = mo[n][j] == -INFINITY ? 0.f : mo[n][j];
                     const float f = fast_exp2(fminf(mu + lv - mou, 126.f));
                     p0 *= f;
                     p1 *= f;
@@ -517,11 +528,12 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             pb[n][1] = movmatrix_t(Q8 ? pack_f16(pr[2], pr[3]) : pack_bf16(pr[2], pr[3]));
         }
         // ---- O^T [128][8 heads] += V^T P^T
-        const uint32_t sv = st + C::kStageBytes / 2;
+        const uint32_t sv = st + C::kTile + 2 * c * 128;
+        const uint32_t x0 = (rr ^ (2 * c)) << 4, x1 = (rr ^ (2 * c + 1)) << 4;
 #pragma unroll
-        for (int m = 0; m < C::kPieces / 4; ++m) {
-            uint4 v0 = lds16(sv + 2048 * m), v1 = lds16(sv + 2048 * m + 512);
-            uint4 v2 = lds16(sv + 2048 * m + 1024), v3 = lds16(sv + 2048 * m + 1536);
+        for (int m = 0; m < (Q8 ? 1 : 2); ++m) {
+            uint4 v0 = lds16(sv + kBoxBytes * m + x0), v1 = lds16(sv + kBoxBytes * m + 128 + x1);
+            uint4 v2 = lds16(sv + kBoxBytes * m + 1024 + x0), v3 = lds16(sv + kBoxBytes * m + 1152 + x1);
             if (lim < kBlockTokens) {
                 // a weight of 0 does not undo a NaN in a slot that the query does not see
                 const uint4 z = make_uint4(0, 0, 0, 0);
@@ -554,7 +566,6 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
         }
     }
     end_request();
-    cp_wait<0>();
 }
 
 // ---------------------------------------------------------------------------- joining the partials
@@ -650,13 +661,13 @@ __global__ void __launch_bounds__(128) lane_combine_kernel(const LaneParams p) {
 }
 
 template <bool Q8, int NT, bool MASS>
-cudaError_t launch_t(const LaneParams &p, cudaStream_t s) {
+cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
     using C = Cfg<Q8, NT, MASS>;
     auto kern = decode_lane_kernel<Q8, NT, MASS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int ctas = (p.warps_per_head * p.a.hkv + C::kWarps - 1) / C::kWarps;
-    kern<<<ctas, C::kWarps * 32, C::kSmem, s>>>(p);
+    kern<<<ctas, C::kWarps * 32, C::kSmem, s>>>(tk, tv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int chunks = (p.a.max_words + kMassWords - 1) / kMassWords;
@@ -665,9 +676,9 @@ cudaError_t launch_t(const LaneParams &p, cudaStream_t s) {
 }
 
 template <bool Q8, bool MASS>
-cudaError_t launch_g(const LaneParams &p, cudaStream_t s) {
-    if (p.a.group <= 8) return launch_t<Q8, 1, MASS>(p, s);
-    return p.a.group <= 16 ? launch_t<Q8, 2, MASS>(p, s) : launch_t<Q8, 4, MASS>(p, s);
+cudaError_t launch_g(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
+    if (p.a.group <= 8) return launch_t<Q8, 1, MASS>(tk, tv, p, s);
+    return p.a.group <= 16 ? launch_t<Q8, 2, MASS>(tk, tv, p, s) : launch_t<Q8, 4, MASS>(tk, tv, p, s);
 }
 
 }  // namespace
@@ -692,9 +703,9 @@ LanePlan lane_plan(int num_req, int hkv, int max_words, int group, bool q8, bool
     return pl;
 }
 
-cudaError_t launch_decode_lane(const LaneParams &p, bool q8, cudaStream_t s) {
-    if (!q8) return launch_g<false, true>(p, s);
-    return p.mass ? launch_g<true, true>(p, s) : launch_g<true, false>(p, s);
+cudaError_t launch_decode_lane(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, bool q8, cudaStream_t s) {
+    if (!q8) return launch_g<false, true>(tk, tv, p, s);
+    return p.mass ? launch_g<true, true>(tk, tv, p, s) : launch_g<true, false>(tk, tv, p, s);
 }
 
 }  // namespace lazy

@@ -141,7 +141,6 @@ cudaError_t launch_kv_write_q8(const Q8WriteParams &p, cudaStream_t s);
 // reference, 0) [slot][G]; ws_lse: log2 of each word's weight sum [num_req][max_words][Hq].
 struct LaneParams {
     AttnParams a;
-    const uint8_t *k, *v;            // codes, or bf16 pools
     const float *k_scale, *v_scale;  // null for bf16 pools
     float4 *ws_ml;
     float *ws_lse;
@@ -153,7 +152,9 @@ struct LanePlan {
     int64_t slots;                   // partials in the workspace
 };
 LanePlan lane_plan(int num_req, int hkv, int max_words, int group, bool q8, bool mass, int sms);
-cudaError_t launch_decode_lane(const LaneParams &p, bool q8, cudaStream_t s);
+// tk, tv: the codes as rows of 128 bytes (one box = one block of one head), or the bf16 pools as rows of 128
+// elements (one box = half of one).
+cudaError_t launch_decode_lane(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, bool q8, cudaStream_t s);
 
 // Prefill over the 8-bit pool (prefill_q8.cu).  a.q_prep: prepared query tiles; row_scale: their row
 // factors [units][256]; units from a.pf_base run as `parts` CTAs each.
