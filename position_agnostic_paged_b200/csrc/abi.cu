@@ -110,10 +110,16 @@ int check_cfg(const lazy_attn_cfg *cfg) {
 void fill_rope(RopeTableHost &t, const lazy_attn_cfg *cfg) {
     // theta_i for the rotate-half pairs (i, i + d/2): the caller's table, else base^(-2i/d);
     // under ALiBi all zero, so that every rotation (pool write, query) is exactly the identity
+    // the powers of the last base, per host thread: 64 calls of pow take longer than a launch
+    thread_local float base = 0.f;
+    thread_local RopeTableHost powers;
+    if (!cfg->alibi_slopes && !cfg->rope_theta && base != cfg->rope_base) {
+        for (int i = 0; i < 64; ++i)
+            powers.theta[i] = std::pow(static_cast<double>(cfg->rope_base), -2.0 * i / 128.0);
+        base = cfg->rope_base;
+    }
     for (int i = 0; i < 64; ++i)
-        t.theta[i] = cfg->alibi_slopes ? 0.0
-                     : cfg->rope_theta ? cfg->rope_theta[i]
-                                       : std::pow(static_cast<double>(cfg->rope_base), -2.0 * i / 128.0);
+        t.theta[i] = cfg->alibi_slopes ? 0.0 : cfg->rope_theta ? cfg->rope_theta[i] : powers.theta[i];
 }
 
 float scale_log2(const lazy_attn_cfg *cfg) {

@@ -13,6 +13,7 @@ import os
 from dataclasses import dataclass
 
 import numpy as np
+import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblazy_attn.so")
@@ -64,6 +65,14 @@ class Cfg:
     alibi_slopes: tuple | None = None
 
     def c(self) -> LazyAttnCfg:
+        """The C structure, made once (the fields of a Cfg do not change)."""
+        st = self.__dict__.get("_c")
+        if st is None:
+            st = self._make_c()
+            object.__setattr__(self, "_c", st)
+        return st
+
+    def _make_c(self) -> LazyAttnCfg:
         st = LazyAttnCfg(self.num_q_heads, self.num_kv_heads, self.head_dim, self.block_size,
                          float(self.rope_base), float(self.softmax_scale), None, None)
         if self.alibi_slopes is not None:
@@ -182,7 +191,6 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
         return int(torch.cuda.current_stream().cuda_stream) or None
     return int(getattr(stream, "cuda_stream", stream)) or None
 
@@ -354,33 +362,30 @@ def decode_attn_noalloc(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: 
 # ---- the 8-bit pool, block mass and eviction.  These calls check what the C side cannot see: types
 # (two-byte and four-byte elements would be read as something else), contiguity, shapes and the device.
 
-def _take(name: str, t, kinds: tuple, shape: tuple | None = None):
-    if str(t.dtype)[6:] not in kinds:
-        raise ValueError(f"{name} must be {' or '.join(kinds)}, not {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+_BF16, _F32, _I32, _WORD = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int32, torch.uint32)
 
 
-_WORD = ("int32", "uint32")
+def _take(name: str, t, dtypes: tuple, shape: tuple | None = None):
+    if t.dtype in dtypes and t.is_contiguous() and (shape is None or t.shape == shape):
+        return
+    raise ValueError(f"{name} must be a contiguous tensor of {' or '.join(map(str, dtypes))}"
+                     + (f" with shape {shape}" if shape is not None else "")
+                     + f", not {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
-def _on(ts, stream):
-    """(device guard, stream handle) for a launch on the tensors' device, which need not be the current one."""
-    import contextlib
-
-    import torch
-    dev = {t.device for t in ts if t is not None}
-    if len(dev) != 1:
-        raise ValueError("all tensors must be on one device")
-    dev = dev.pop()
-    if dev.type != "cuda":
+def _launch(name: str, fn, ts, stream, *args):
+    """fn(*args, stream) on the tensors' device, which need not be the current one."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+    if dev < 0:
         raise ValueError("all tensors must be CUDA tensors")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    guard = contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-    return guard, _stream(stream)
+    if dev == torch.cuda.current_device():
+        _check(name, fn(*args, _stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _check(name, fn(*args, _stream(stream)))
 
 
 class Q8Pool:
@@ -392,9 +397,9 @@ class Q8Pool:
     def __init__(self, k_codes, v_codes, k_scale, v_scale, blk_meta):
         nb, hkv = int(k_codes.shape[0]), int(k_codes.shape[1])
         for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
-            _take(name, t, ("uint8", "float8_e4m3fn"), (nb, hkv, 16, 128))
+            _take(name, t, (torch.uint8, torch.float8_e4m3fn), (nb, hkv, 16, 128))
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            _take(name, t, ("float32",), (nb, hkv))
+            _take(name, t, _F32, (nb, hkv))
         _take("blk_meta", blk_meta, _WORD, (nb,))
         self.k_codes, self.v_codes, self.k_scale, self.v_scale, self.blk_meta = k_codes, v_codes, k_scale, v_scale, blk_meta
         self.num_blocks, self.num_kv_heads = nb, hkv
@@ -402,7 +407,6 @@ class Q8Pool:
     @classmethod
     def empty(cls, num_blocks: int, num_kv_heads: int, device="cuda") -> "Q8Pool":
         """A pool whose blocks hold no tokens."""
-        import torch
         codes = lambda: torch.zeros(num_blocks, num_kv_heads, 16, 128, dtype=torch.uint8, device=device)   # noqa: E731
         scale = lambda: torch.ones(num_blocks, num_kv_heads, dtype=torch.float32, device=device)           # noqa: E731
         return cls(codes(), codes(), scale(), scale(), torch.zeros(num_blocks, dtype=torch.int32, device=device))
@@ -427,29 +431,28 @@ def kv_write_q8(cfg: Cfg, k_raw, v_raw, slot, local_j, pool: Q8Pool, workspace=N
     c, q, n = cfg.c(), pool.c(), int(slot.numel())
     _heads(cfg, pool)
     for name, t in (("k_raw", k_raw), ("v_raw", v_raw)):
-        _take(name, t, ("bfloat16",), (n, cfg.num_kv_heads, 128))
+        _take(name, t, _BF16, (n, cfg.num_kv_heads, 128))
     for name, t in (("slot", slot), ("local_j", local_j)):
-        _take(name, t, ("int32",))
+        _take(name, t, _I32)
     if local_j.numel() != n:
         raise ValueError("slot and local_j must have one element per token")
-    guard, st = _on((k_raw, v_raw, slot, local_j, pool.k_codes, workspace, d_status), stream)
-    with guard:
-        _check("lazy_kv_write_q8", _lib.lazy_kv_write_q8(
+    _launch("lazy_kv_write_q8", _lib.lazy_kv_write_q8,
+            (k_raw, v_raw, slot, local_j, pool.k_codes, workspace, d_status), stream,
             ctypes.byref(c), _ptr(k_raw), _ptr(v_raw), n, _ptr(slot), _ptr(local_j), ctypes.byref(q),
-            _ptr(workspace), _nbytes(workspace), _ptr(d_status), st))
+            _ptr(workspace), _nbytes(workspace), _ptr(d_status))
 
 
 def _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass):
     n = int(q_pos.numel())
-    _take("q_raw", q_raw, ("bfloat16",), (n, cfg.num_q_heads, 128))
-    _take("out", out, ("bfloat16",), (n, cfg.num_q_heads, 128))
-    _take("q_pos", q_pos, ("int32",))
+    _take("q_raw", q_raw, _BF16, (n, cfg.num_q_heads, 128))
+    _take("out", out, _BF16, (n, cfg.num_q_heads, 128))
+    _take("q_pos", q_pos, _I32)
     _take("table", table, _WORD)
-    _take("table_indptr", table_indptr, ("int32",))
+    _take("table_indptr", table_indptr, _I32)
     if table_indptr.numel() != n + 1:
         raise ValueError("table_indptr must have one element more than q_pos")
     if block_mass is not None:
-        _take("block_mass", block_mass, ("float32",))
+        _take("block_mass", block_mass, _F32)
         if block_mass.numel() != table.numel():
             raise ValueError("block_mass must have one element per table word")
     return n
@@ -467,11 +470,10 @@ def decode_attn_q8(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: int, 
     c, q = cfg.c(), pool.c()
     _heads(cfg, pool)
     n = _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass)
-    guard, st = _on((q_raw, q_pos, table, table_indptr, pool.k_codes, out, workspace, block_mass, d_status), stream)
-    with guard:
-        _check("lazy_decode_attn_q8", _lib.lazy_decode_attn_q8(
+    _launch("lazy_decode_attn_q8", _lib.lazy_decode_attn_q8,
+            (q_raw, q_pos, table, table_indptr, pool.k_codes, out, workspace, block_mass, d_status), stream,
             ctypes.byref(c), _ptr(q_raw), _ptr(q_pos), n, _ptr(table), _ptr(table_indptr), int(max_words),
-            ctypes.byref(q), _ptr(out), _ptr(block_mass), _ptr(workspace), _nbytes(workspace), _ptr(d_status), st))
+            ctypes.byref(q), _ptr(out), _ptr(block_mass), _ptr(workspace), _nbytes(workspace), _ptr(d_status))
 
 
 def decode_mass_workspace_bytes(cfg: Cfg, num_req: int, max_words: int) -> int:
@@ -487,15 +489,13 @@ def decode_attn_mass(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: int
     n = _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass)
     nb = int(k_pool.shape[0])
     for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-        _take(name, t, ("bfloat16",), (nb, cfg.num_kv_heads, 16, 128))
+        _take(name, t, _BF16, (nb, cfg.num_kv_heads, 16, 128))
     _take("blk_meta", blk_meta, _WORD, (nb,))
-    guard, st = _on((q_raw, q_pos, table, table_indptr, blk_meta, k_pool, v_pool, out, block_mass, workspace, d_status),
-                    stream)
-    with guard:
-        _check("lazy_decode_attn_mass", _lib.lazy_decode_attn_mass(
+    _launch("lazy_decode_attn_mass", _lib.lazy_decode_attn_mass,
+            (q_raw, q_pos, table, table_indptr, blk_meta, k_pool, v_pool, out, block_mass, workspace, d_status), stream,
             ctypes.byref(c), _ptr(q_raw), _ptr(q_pos), n, _ptr(table), _ptr(table_indptr), int(max_words),
             _ptr(blk_meta), _ptr(k_pool), _ptr(v_pool), nb, _ptr(out), _ptr(block_mass), _ptr(workspace),
-            _nbytes(workspace), _ptr(d_status), st))
+            _nbytes(workspace), _ptr(d_status))
 
 
 def prefill_q8_workspace_bytes(cfg: Cfg, num_req: int, total_q: int, max_q: int, max_words: int,
@@ -511,19 +511,18 @@ def prefill_attn_q8(cfg: Cfg, q_raw, cu_q, q_pos0, max_q: int, table, table_indp
     c, q = cfg.c(), pool.c()
     _heads(cfg, pool)
     n, total_q = int(q_pos0.numel()), int(q_raw.shape[0])
-    _take("q_raw", q_raw, ("bfloat16",), (total_q, cfg.num_q_heads, 128))
-    _take("out", out, ("bfloat16",), (total_q, cfg.num_q_heads, 128))
+    _take("q_raw", q_raw, _BF16, (total_q, cfg.num_q_heads, 128))
+    _take("out", out, _BF16, (total_q, cfg.num_q_heads, 128))
     for name, t in (("cu_q", cu_q), ("q_pos0", q_pos0), ("table_indptr", table_indptr)):
-        _take(name, t, ("int32",))
+        _take(name, t, _I32)
     _take("table", table, _WORD)
     if cu_q.numel() != n + 1 or table_indptr.numel() != n + 1:
         raise ValueError("cu_q and table_indptr must have one element more than q_pos0")
-    guard, st = _on((q_raw, cu_q, q_pos0, table, table_indptr, pool.k_codes, out, workspace, d_status), stream)
-    with guard:
-        _check("lazy_prefill_attn_q8", _lib.lazy_prefill_attn_q8(
+    _launch("lazy_prefill_attn_q8", _lib.lazy_prefill_attn_q8,
+            (q_raw, cu_q, q_pos0, table, table_indptr, pool.k_codes, out, workspace, d_status), stream,
             ctypes.byref(c), _ptr(q_raw), _ptr(cu_q), _ptr(q_pos0), n, total_q, int(max_q), _ptr(table),
             _ptr(table_indptr), int(max_words), ctypes.byref(q), _ptr(out), _ptr(workspace), _nbytes(workspace),
-            _ptr(d_status), st))
+            _ptr(d_status))
 
 
 def evict_blocks(table, table_indptr, max_words: int, block_mass, keep, n_first: int, n_last: int, table_out,
@@ -535,20 +534,19 @@ def evict_blocks(table, table_indptr, max_words: int, block_mass, keep, n_first:
         if t is not None:
             _take(name, t, _WORD)
     for name, t in (("block_mass", block_mass), ("mass_out", mass_out)):
-        _take(name, t, ("float32",))
+        _take(name, t, _F32)
     for name, t in (("table_indptr", table_indptr), ("indptr_out", indptr_out), ("keep", keep)):
-        _take(name, t, ("int32",))
+        _take(name, t, _I32)
     if table_indptr.numel() != n + 1 or indptr_out.numel() < n + 1:
         raise ValueError("table_indptr and indptr_out must have one element more than keep")
     if block_mass.numel() != words:
         raise ValueError("block_mass must have one element per table word")
     if min([words] + [t.numel() for t in (table_out, mass_out, evicted) if t is not None]) < words:
         raise ValueError("table_out, mass_out and evicted need room for every table word")
-    guard, st = _on((table, table_indptr, block_mass, keep, table_out, indptr_out, mass_out, evicted, d_status), stream)
-    with guard:
-        _check("lazy_evict_blocks", _lib.lazy_evict_blocks(
+    _launch("lazy_evict_blocks", _lib.lazy_evict_blocks,
+            (table, table_indptr, block_mass, keep, table_out, indptr_out, mass_out, evicted, d_status), stream,
             _ptr(table), _ptr(table_indptr), n, int(max_words), _ptr(block_mass), _ptr(keep), int(n_first),
-            int(n_last), _ptr(table_out), _ptr(indptr_out), _ptr(mass_out), _ptr(evicted), _ptr(d_status), st))
+            int(n_last), _ptr(table_out), _ptr(indptr_out), _ptr(mass_out), _ptr(evicted), _ptr(d_status))
 
 
 class BlockCache:
