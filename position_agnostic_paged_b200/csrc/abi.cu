@@ -229,7 +229,8 @@ int64_t prefill_units(const lazy_attn_cfg *cfg, int num_req, int max_q) {
 // mass one log2 weight sum per (request, word, query head).
 size_t lane_ws(const lazy_attn_cfg *cfg, int num_req, int max_words, bool q8, bool mass, LanePlan &pl) {
     const int G = cfg->num_q_heads / cfg->num_kv_heads;
-    pl = lane_plan(num_req, cfg->num_kv_heads, max_words, G, q8, mass, sm_count());
+    pl = q8 ? decode_q8_plan(num_req, cfg->num_kv_heads, max_words, G, mass, sm_count())
+            : lane_plan(num_req, cfg->num_kv_heads, max_words, G, q8, mass, sm_count());
     size_t n = static_cast<size_t>(pl.slots) * G * (128 * sizeof(float) + sizeof(float4));
     if (mass) n += static_cast<size_t>(num_req) * max_words * cfg->num_q_heads * sizeof(float);
     return n;
@@ -245,7 +246,7 @@ int lane_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_
     if (rc) return rc;
     if (num_req == 0) return LAZY_OK;
     if (!q_raw || !q_pos || (num_blocks > 0 && !k)) return LAZY_EINVAL;
-    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q_raw, 4)) return LAZY_EINVAL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q_raw, q8 ? 8 : 4)) return LAZY_EINVAL;
     if (max_words == 0 || num_blocks == 0)
         // nothing can be visible: every output row is zero
         return launch_rc(cudaMemsetAsync(out, 0, static_cast<size_t>(num_req) * p.a.hq * 128 * 2,
@@ -271,7 +272,8 @@ int lane_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_
     if (q8 ? !make_codes_map(&tk, k, pool_rows) || !make_codes_map(&tv, v, pool_rows)
            : !make_rows_map(&tk, k, pool_rows) || !make_rows_map(&tv, v, pool_rows))
         return LAZY_ECUDA;
-    return launch_rc(launch_decode_lane(tk, tv, p, q8, static_cast<cudaStream_t>(stream)));
+    return launch_rc(q8 ? launch_decode_q8(tk, tv, p, static_cast<cudaStream_t>(stream))
+                        : launch_decode_lane(tk, tv, p, q8, static_cast<cudaStream_t>(stream)));
 }
 
 int prefill_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *cu_q, const int32_t *q_pos0,

@@ -127,6 +127,10 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
     const int G = a.group, hkv = a.hkv, B = a.num_req;
     const int gw = blockIdx.x * kWarps + warp;
     const int kvh = gw % hkv, wi = gw / hkv;
+    // the rotation frequencies: a per-lane read of the parameter table takes 32 turns
+    __shared__ double theta[kHalfDim];
+    for (int i = threadIdx.x; i < kHalfDim; i += kWarps * 32) theta[i] = a.rope.theta[i];
+    __syncthreads();
     if (wi >= p.warps_per_head) return;
     const int base = a.table_indptr[0];
     const int total = a.table_indptr[B] - base;
@@ -172,31 +176,27 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
     meta_at(lane, w_cur, m_cur, ks_cur, vs_cur);
     meta_at(32 + lane, w_nxt, m_nxt, ks_nxt, vs_nxt);
 
-    // copies of word k (of this warp) into stage k % S; `kb` is the batch that w_cur holds.  A word without
-    // tokens, or without a block, completes its phase with no data.
-    auto issue = [&](int k, int kb) {
-        if (k < cnt) {
-            const bool nx = (k >> 5) != kb;
-            const uint32_t w = __shfl_sync(0xffffffffu, nx ? w_nxt : w_cur, k & 31);
-            const uint32_t m = __shfl_sync(0xffffffffu, nx ? m_nxt : m_cur, k & 31);
-            if (lane == 0) {
-                uint64_t *bar = &bars[k % S];
-                if (meta_valid(m) > 0) {
-                    uint8_t *d = stages + (k % S) * C::kStageBytes;
-                    const int row = (static_cast<int>(word_block(w)) * hkv + kvh) * kBlockTokens;
-                    mbar_arrive_expect_tx(bar, C::kStageBytes);
-                    tma_load_2d(d, &tmK, 0, row, bar);
-                    if (!Q8) tma_load_2d(d + kBoxBytes, &tmK, kHalfDim, row, bar);
-                    tma_load_2d(d + C::kTile, &tmV, 0, row, bar);
-                    if (!Q8) tma_load_2d(d + C::kTile + kBoxBytes, &tmV, kHalfDim, row, bar);
-                } else {
-                    mbar_arrive(bar);
-                }
+    // copies of word k (of this warp) into stage sg, by the lane that holds the word.  A word without tokens, or
+    // without a block, completes its phase with no data.
+    auto issue = [&](int k, bool next_batch, int sg) {
+        if (k < cnt && lane == (k & 31)) {
+            const uint32_t w = next_batch ? w_nxt : w_cur, m = next_batch ? m_nxt : m_cur;
+            uint64_t *bar = &bars[sg];
+            if (meta_valid(m) > 0) {
+                uint8_t *d = stages + sg * C::kStageBytes;
+                const int row = (static_cast<int>(word_block(w)) * hkv + kvh) * kBlockTokens;
+                mbar_arrive_expect_tx(bar, C::kStageBytes);
+                tma_load_2d(d, &tmK, 0, row, bar);
+                if (!Q8) tma_load_2d(d + kBoxBytes, &tmK, kHalfDim, row, bar);
+                tma_load_2d(d + C::kTile, &tmV, 0, row, bar);
+                if (!Q8) tma_load_2d(d + C::kTile + kBoxBytes, &tmV, kHalfDim, row, bar);
+            } else {
+                mbar_arrive(bar);
             }
         }
     };
 #pragma unroll
-    for (int k = 0; k < S - 1; ++k) issue(k, 0);
+    for (int k = 0; k < S - 1; ++k) issue(k, false, k);
 
     // ---- the request of the first word: the largest r with table_indptr[r] <= its index
     int r = 0;
@@ -211,18 +211,14 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             hi = min(hi, r + step);
         }
     }
-    // kept in registers: a per-lane read of the parameter table takes 32 turns
-    double th0 = a.rope.theta[lane], th1 = a.rope.theta[lane + 32];
-    asm volatile("" : "+d"(th0), "+d"(th1));
-
     int r_beg = a.table_indptr[r] - base, r_end = a.table_indptr[r + 1] - base;
     int qpos = 0, cur_off = -1;
-    uint32_t qraw[C::kRegQ ? 8 : 1][2];
     uint32_t qb[C::kRegQ ? QP : 1][C::kRegQ ? 8 : 1][2];
     float qn[NT];            // 2^-e of this lane's fragment head (8 n + rr)
     float hm[NT][2];         // score factor of heads 8 n + 2c, + 1: softmax scale * log2(e) * 2^e
-    float sl[NT][2];         // ALiBi slopes of those heads (log2 units)
-    float m_run[NT][2], l_run[NT][2], mo[NT][2];
+    // per head, in log2 units: reference mu of the row sum l_run; dm = mu - mo, mo the reference of
+    // score + log2 of the V scale (+inf before the first visible key); dv = 2^(dm - 20)
+    float mu[NT][2], l_run[NT][2], dm[NT][2], dv[NT][2];
     float oacc[NT][8][4];
 
     auto begin_request = [&]() {
@@ -244,10 +240,6 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
                     w0 = q[d >> 1];
                     w1 = q[(d >> 1) + 1];
                 }
-                if (C::kRegQ) {
-                    qraw[s][0] = w0;
-                    qraw[s][1] = w1;
-                }
                 am = fmaxf(am, fmaxf(fmaxf(fabsf(bf16_lo(w0)), fabsf(bf16_hi(w0))),
                                      fmaxf(fabsf(bf16_lo(w1)), fabsf(bf16_hi(w1)))));
             }
@@ -262,10 +254,8 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             hm[n][1] = __shfl_sync(0xffffffffu, q2, 8 * c + 4);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const int h = 8 * n + 2 * c + j;
-                sl[n][j] = (a.alibi && h < G) ? a.alibi_log2[kvh * G + h] : 0.f;
-                m_run[n][j] = mo[n][j] = -INFINITY;
-                l_run[n][j] = 0.f;
+                mu[n][j] = l_run[n][j] = dv[n][j] = 0.f;
+                dm[n][j] = INFINITY;
             }
 #pragma unroll
             for (int t = 0; t < 8; ++t) oacc[n][t][0] = oacc[n][t][1] = oacc[n][t][2] = oacc[n][t][3] = 0.f;
@@ -276,8 +266,8 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
         cur_off = off;
         const int delta = a.alibi ? 0 : qpos - off;
         float2 z0, z1;
-        rope_cos_sin(delta, th0, z0.x, z0.y);
-        rope_cos_sin(delta, th1, z1.x, z1.y);
+        rope_cos_sin(delta, theta[lane], z0.x, z0.y);
+        rope_cos_sin(delta, theta[lane + 32], z1.x, z1.y);
         __syncwarp();
         cs[lane] = z0;
         cs[lane + 32] = z1;
@@ -297,11 +287,7 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     const int st = y < 2 ? s : t, d = qdim<Q8>(st, c) + 2 * (y & 1);
-                    uint32_t w;
-                    if (C::kRegQ)
-                        w = qraw[C::kRegQ ? st : 0][y & 1];
-                    else
-                        w = g < G ? q[d >> 1] : 0u;
+                    const uint32_t w = g < G ? q[d >> 1] : 0u;
                     const float4 z = *reinterpret_cast<const float4 *>(&cs[d & 63]);   // (cos, sin) of two pairs
                     const float o0 = bf16_lo(w) * qn[n], o1 = bf16_hi(w) * qn[n];
                     if (Q8) {
@@ -373,13 +359,21 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
                         *reinterpret_cast<float4 *>(o + odim<Q8>(t, rr)) =
                             make_float4(oacc[n][t][j], oacc[n][t][j + 2], oacc[n][t + 1][j], oacc[n][t + 1][j + 2]);
                     }
-                    if (rr == 0) p.ws_ml[slot * G + g] = make_float4(m_run[n][j], l, mo[n][j], 0.f);
+                    if (rr == 0) p.ws_ml[slot * G + g] = dm[n][j] == INFINITY && l == l ? make_float4(-INFINITY, 0.f, -INFINITY, 0.f)
+                                                                                 : make_float4(mu[n][j], l, mu[n][j] - dm[n][j], 0.f);
                 }
             }
     };
     begin_request();
 
+    int sg = S - 1, before = S - 2;   // stages of words k and k - 1
+    uint32_t phase = 1;               // of stage sg
     for (int k = 0; k < cnt; ++k) {
+        before = sg;
+        if (++sg == S) {
+            sg = 0;
+            phase ^= 1;
+        }
         if (k > 0 && (k & 31) == 0) {
             w_cur = w_nxt;
             m_cur = m_nxt;
@@ -390,8 +384,8 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             meta_at(k + 32 + lane, w_nxt, m_nxt, ks_nxt, vs_nxt);
         }
         __syncwarp();   // every lane has read the stage that is loaded next
-        issue(k + S - 1, k >> 5);
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars[k % S], (k / S) & 1))) {
+        issue(k + S - 1, (k & 31) + S - 1 >= 32, before);
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars[sg], phase))) {
             set_status(a.d_status, LAZY_DSTATUS_TIMEOUT);
             for (int i = k; i < min(cnt, k + S); ++i) mbar_wait(&bars[i % S], (i / S) & 1);   // copies in flight
             break;
@@ -408,7 +402,8 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
         const uint32_t w = __shfl_sync(0xffffffffu, w_cur, k & 31);
         const uint32_t meta = __shfl_sync(0xffffffffu, m_cur, k & 31);
         const float ksc = Q8 ? __shfl_sync(0xffffffffu, ks_cur, k & 31) : 1.f;
-        const float lv = Q8 ? fast_log2(__shfl_sync(0xffffffffu, vs_cur, k & 31)) : 0.f;
+        const float vsc = Q8 ? __shfl_sync(0xffffffffu, vs_cur, k & 31) : 1.f;
+        const float lv = Q8 ? fast_log2(vsc) : 0.f;
         const int i_req = lo + k - r_beg;                       // index of the word in its request
         const int off = word_offset(w);
         const int pos0 = off + meta_j0(meta);
@@ -421,7 +416,7 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
         }
         if (cur_off < 0 || (off != cur_off && !a.alibi)) rotate(off);
 
-        const uint32_t st = smem_u32(stages) + (k % S) * C::kStageBytes;
+        const uint32_t st = smem_u32(stages) + sg * C::kStageBytes;
         // ---- S^T [16 keys][8 heads] = K q^T
         float sa[NT][4];
 #pragma unroll
@@ -458,65 +453,79 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
                     }
             }
         }
-        // ---- softmax over the word's keys (rr and rr + 8 in this lane).  References (m_run for the row sums, mo
-        // for score + log2 of the V scale) move only when some score passes them by kSlack: weights stay
+        // ---- softmax over the word's keys (rr and rr + 8 in this lane).  References (mu for the row sums, mo for
+        // score + log2 of the V scale) move only when some score passes them by kSlack: weights stay
         // below 2^8 and most words need neither the maxima nor rescaling.
-        const bool vis0 = rr < lim, vis1 = rr + 8 < lim;
         uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            bool past = false;
+            // scores relative to mu
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const float f = hm[n][j] * ksc;
-                float s0 = sa[n][j] * f, s1 = sa[n][j + 2] * f;
-                if (a.alibi) {
-                    const float d0 = static_cast<float>(pos0 + rr - qpos);
-                    s0 = fmaf(sl[n][j], d0, s0);
-                    s1 = fmaf(sl[n][j], d0 + 8.f, s1);
-                }
-                sa[n][j] = vis0 ? s0 : -INFINITY;
-                sa[n][j + 2] = vis1 ? s1 : -INFINITY;
-                const float top = fmaxf(sa[n][j], sa[n][j + 2]);
-                past |= top > m_run[n][j] + kSlack || (Q8 && top + lv > mo[n][j] + kSlack);
+                sa[n][j] = fmaf(sa[n][j], f, -mu[n][j]);
+                sa[n][j + 2] = fmaf(sa[n][j + 2], f, -mu[n][j]);
             }
+            if (a.alibi) {
+                const float d0 = static_cast<float>(pos0 + rr - qpos);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float sl = 8 * n + 2 * c + j < G ? a.alibi_log2[kvh * G + 8 * n + 2 * c + j] : 0.f;
+                    sa[n][j] = fmaf(sl, d0, sa[n][j]);
+                    sa[n][j + 2] = fmaf(sl, d0 + 8.f, sa[n][j + 2]);
+                }
+            }
+            if (lim < kBlockTokens) {
+                if (rr >= lim) sa[n][0] = sa[n][1] = -INFINITY;
+                if (rr + 8 >= lim) sa[n][2] = sa[n][3] = -INFINITY;
+            }
+            bool past = false;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                past |= fmaxf(sa[n][j], sa[n][j + 2]) + fmaxf(Q8 || dm[n][j] == INFINITY ? lv + dm[n][j] : 0.f, 0.f) > kSlack;
             if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float bm = fmaxf(sa[n][j], sa[n][j + 2]);
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
-                    const float mn = fmaxf(m_run[n][j], bm), mon = Q8 ? fmaxf(mo[n][j], bm + lv) : mn;
-                    if (mn != m_run[n][j]) l_run[n][j] *= fast_exp2(m_run[n][j] - mn);
-                    if (mon != mo[n][j]) {
-                        const float sc = fast_exp2(mo[n][j] - mon);
+                    if (bm == -INFINITY) continue;   // this head sees no key of the word
+                    // up: the references' steps
+                    const bool first = dm[n][j] == INFINITY;
+                    const float up = first ? bm : fmaxf(bm, 0.f);
+                    const float mo_old = mu[n][j] - dm[n][j], top = mu[n][j] + bm + lv;
+                    const float mo = Q8 ? (first ? top : fmaxf(mo_old, top)) : mu[n][j] + up;
+                    if (!first) {
+                        l_run[n][j] *= fast_exp2(-up);
+                        const float sc = fast_exp2(mo_old - mo);
 #pragma unroll
                         for (int t = 0; t < 8; ++t) {
                             oacc[n][t][j] *= sc;
                             oacc[n][t][j + 2] *= sc;
                         }
                     }
-                    m_run[n][j] = mn;
-                    mo[n][j] = mon;
+                    mu[n][j] += up;
+                    sa[n][j] -= up;
+                    sa[n][j + 2] -= up;
+                    dm[n][j] = mu[n][j] - mo;
+                    dv[n][j] = fast_exp2(fminf(dm[n][j] - 20.f, 126.f));
                 }
             }
             float pr[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float mu = m_run[n][j] == -INFINITY ? 0.f : m_run[n][j];
-                float p0 = fast_exp2(sa[n][j] - mu), p1 = fast_exp2(sa[n][j + 2] - mu);
+                float p0 = fast_exp2(sa[n][j]), p1 = fast_exp2(sa[n][j + 2]);
                 float ps = p0 + p1;
                 if (MASS) {
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, x);
                     const int g = 8 * n + 2 * c + j;
-                    if (rr == 0 && g < G) lse[g] = mu + fast_log2(ps);
+                    if (rr == 0 && g < G) lse[g] = mu[n][j] + fast_log2(ps);
                 }
                 l_run[n][j] += ps;
                 if (Q8) {
-                    // weights for the V product: w 2^(log2 s_v) against 2^mo
-                    const float mou = mo[n][j] == -INFINITY ? 0.f : mo[n][j];
-                    const float f = fast_exp2(fminf(mu + lv - mou, 126.f));
+                    // weights for the V product: w s_v against 2^mo (two factors: s_v spans the range of a float)
+                    const float f = vsc * dv[n][j] * 0x1p20f;
                     p0 *= f;
                     p1 *= f;
                 }
@@ -573,7 +582,7 @@ constexpr int kMassWords = 32;   // words per CTA of the mass part
 
 // CTAs 0 .. num_req * Hq - 1: out[r][h] from the request's partials.  The CTAs behind them: the
 // word accumulators, mass[w] += sum_h 2^(lse[w][h] - z_h), z_h = M_h + log2 L_h, one warp per word.
-__global__ void __launch_bounds__(128) lane_combine_kernel(const LaneParams p) {
+__global__ void __launch_bounds__(128) lane_combine_kernel(const __grid_constant__ LaneParams p, int min_words) {
     const AttnParams &a = p.a;
     const int B = a.num_req, G = a.group, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool for_out = static_cast<int>(blockIdx.x) < B * a.hq;
@@ -584,7 +593,7 @@ __global__ void __launch_bounds__(128) lane_combine_kernel(const LaneParams p) {
     const int total = a.table_indptr[B] - base;
     const int beg = a.table_indptr[r] - base;
     const int n = min(a.table_indptr[r + 1] - base - beg, a.max_words);
-    const int per = words_per_warp(total, p.warps_per_head);
+    const int per = max(min_words, (total + p.warps_per_head - 1) / p.warps_per_head);
     const int w0 = n > 0 ? beg / per : 0, nw = n > 0 ? (beg + n - 1) / per - w0 + 1 : 0;
     if (for_out) {
         __shared__ float red[4][2], wgt[128], lsum[4];
@@ -621,7 +630,8 @@ __global__ void __launch_bounds__(128) lane_combine_kernel(const LaneParams p) {
             const int m = min(128, nw - i0);
             const float *acc = a.ws_acc + ((s0 + i0) * G + g) * kHeadDim + tid;
 #pragma unroll 8
-            for (int i = 0; i < m; ++i) A += wgt[i] * acc[static_cast<size_t>(i) * G * kHeadDim];
+            for (int i = 0; i < m; ++i)
+                if (wgt[i] != 0.f) A += wgt[i] * acc[static_cast<size_t>(i) * G * kHeadDim];   // (a partial without keys has no acc)
         }
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
@@ -670,9 +680,7 @@ cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const LanePar
     kern<<<ctas, C::kWarps * 32, C::kSmem, s>>>(tk, tv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int chunks = (p.a.max_words + kMassWords - 1) / kMassWords;
-    lane_combine_kernel<<<p.a.num_req * (p.a.hq + (p.mass ? chunks : 0)), 128, p.mass ? p.a.hq * sizeof(float) : 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_lane_combine(p, kMinWords, s);
 }
 
 template <bool Q8, bool MASS>
@@ -701,6 +709,12 @@ LanePlan lane_plan(int num_req, int hkv, int max_words, int group, bool q8, bool
     if (pl.warps_per_head < 1) pl.warps_per_head = 1;
     pl.slots = static_cast<int64_t>(hkv) * (pl.warps_per_head + num_req);
     return pl;
+}
+
+cudaError_t launch_lane_combine(const LaneParams &p, int min_words, cudaStream_t s) {
+    const int chunks = (p.a.max_words + kMassWords - 1) / kMassWords;
+    lane_combine_kernel<<<p.a.num_req * (p.a.hq + (p.mass ? chunks : 0)), 128, p.mass ? p.a.hq * sizeof(float) : 0, s>>>(p, min_words);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_decode_lane(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, bool q8, cudaStream_t s) {

@@ -1,0 +1,753 @@
+// decode_q8.cu -- decode attention over the 8-bit pool on tcgen05 tensor cores, codes used as they are.
+//
+// Per request, query head h on KV head k, key t (code k_t, v_t) of a block with scales s_k, s_v, table
+// offset o, local index j and position o + j <= p (the query's):
+//   s_t = scale s_k q_h^T R(-(p - o)) k_t,   w_t = 2^(s_t - M) / L,   out = sum_t w_t s_v v_t,
+//   block_mass[word] += sum_h sum_{t in word} w_t.
+//
+// Both products take e4m3 operands (kind::f8f6f4), so no code is ever converted.  The other operand, a
+// rotated query or a weight x <= 448, becomes a sum of e4m3 parts with steps of 2^-4 (e4m3 rounds to 2^-4 of
+// a value, so 2^4 times the rest is at most 256):
+//   x = x_0 + 2^-4 x_1 + 2^-8 x_2,   x_0 = e4m3(x), x_1 = e4m3(2^4 (x - x_0)), x_2 = e4m3(2^4 (...)):
+// three parts are off by 2^-5 at most (2^-12 of 128, f16 would keep 2^-11) and reach down to 2^-18.  Each
+// part is a row group of the B operand with accumulator columns of its own; the sum is taken in fp32
+// when they are read.  With block mass the query has five parts (2^-13).
+//
+//   S^T [128 keys][parts x heads] = K [128 keys][128] Q^T      A: the K codes of 8 words as they lie in the pool
+//   O^T [128 dims][parts x heads] += V^T [128 dims][keys] P^T  A: the V codes, keys as rows (MN-major)
+//
+// A block's K scale multiplies the scores of its 16 lanes of S^T; its V scale joins the weights.
+//
+// Work split.  The words of all requests lie one after the other in `table`, so for one KV head they
+// form one line; it is cut into equal pieces, one per resident CTA: ragged batches balance by
+// themselves and no request waits for the longest.  Where a request ends inside a piece the CTA writes a
+// partial result (m, l, acc) to workspace slot (piece + request), unique because each new partial moves
+// on to the next piece or the next request.  A second kernel joins a request's partials in order.
+//
+// Warps: four per group of 8 query heads (or 4) for the softmax (thread t of a group: key t of the tile, later
+// head dim t), one for the table walk and the TMA loads, one for MMA issue.  A tile is up to 8 words of one request with one offset; K and V of a tile (32 KiB)
+// share a stage.  Scores are double-buffered and a tile ahead of the softmax.
+#include <climits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "q8.cuh"
+#include "tc.cuh"
+
+namespace lazy {
+
+namespace {
+
+constexpr int kTileWords = 8;
+constexpr int kCodeBlock = kBlockTokens * kHeadDim;              // codes of one block of one head
+constexpr int kHalfStage = kTileWords * kCodeBlock, kStageBytes = 2 * kHalfStage;
+constexpr int kRecords = 4;
+constexpr float kSlack = 1.75f;       // log2 units by which a score may pass its reference: weights times 2^7 stay below 448
+constexpr float kPartStep = 16.f;     // between parts
+
+// One tile of the walk; n = 0 ends it.
+struct Tile {
+    int n, off, req, word;            // words, offset, request, index of the first word in the request
+    int lim[kTileWords];              // visible slots of each word
+    int pos[kTileWords];              // position of its slot 0
+    float ks[kTileWords], vs[kTileWords];
+};
+
+// NG: query heads per KV head, rounded up to 4, 8, 16 or 32.  QP: parts of the query.
+template <int NG, int QP>
+struct Cfg {
+    static constexpr int kHT = NG < 8 ? NG : 8, kGroups = NG / kHT;          // heads per softmax thread, groups of 128 threads
+    static constexpr int kSoft = 128 * kGroups, kThreads = kSoft + 64;
+    static constexpr int kQRows = QP * NG, kQN = (kQRows + 15) / 16 * 16;    // rows of the Q operand, N of the S product
+    static constexpr int kPRows = 3 * NG, kPN = (kPRows + 15) / 16 * 16;
+    static constexpr int kQBytes = (kQN + 7) / 8 * 1024, kPBytes = (kPN + 7) / 8 * 1024;
+    static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 4096 + 1024;   // buffers, small state, alignment
+    static constexpr int kOcc = 2 * (kFixed + 2 * kStageBytes + 1024) <= 227 * 1024 ? 2 : 1;
+    static constexpr int kStages0 = (227 * 1024 / kOcc - 1024 - kFixed) / kStageBytes;
+    static constexpr int kStages = kStages0 > 4 ? 4 : kStages0;
+    static constexpr int kSmem = kFixed + kStages * kStageBytes;
+    static constexpr int kCols0 = 2 * kQN + kPN;
+    static constexpr int kCols = kCols0 <= 64 ? 64 : kCols0 <= 128 ? 128 : kCols0 <= 256 ? 256 : 512;   // tensor memory
+    static_assert(kStages >= 2 && kOcc * kCols <= 512, "resources");
+    // shared memory, from a 1 KiB boundary
+    static constexpr int kOffQ = kStages * kStageBytes, kOffP = kOffQ + 2 * kQBytes, kOffState = kOffP + 2 * kPBytes;
+};
+// small state, from kOffState
+constexpr int kOffTile = 0;                                      // records
+constexpr int kOffBars = kOffTile + kRecords * static_cast<int>(sizeof(Tile));
+constexpr int kOffHead = kOffBars + 256;                         // mu, dm, dv, step of O, hm of two Q buffers, slope: [32] each
+constexpr int kOffRed = kOffHead + 7 * 128;                      // [4][32] reductions
+constexpr int kOffAngle = kOffRed + 512;                         // [64] float2
+constexpr int kOffMisc = kOffAngle + 512;
+static_assert(kOffMisc + 16 <= 4096, "state");
+
+// kind::f8f6f4 with e4m3 A/B and fp32 accumulation, M = 128.
+constexpr uint32_t idesc_e4m3(int n, bool a_mn_major) {
+    return (1u << 4) | (a_mn_major ? (1u << 15) : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate));
+}
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t *r) {
+    static_assert(N == 4 || N == 8, "columns");
+    if constexpr (N == 8)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_store4(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *d_status) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, d_status));
+}
+__device__ __forceinline__ float log2_of(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// the softmax warps
+template <int N>
+__device__ __forceinline__ void sync_softmax() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory"); }
+template <int N>
+__device__ __forceinline__ bool any_softmax(bool x) {
+    uint32_t y;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(y)
+                 : "r"(x ? 1u : 0u), "n"(N)
+                 : "memory");
+    return y != 0;
+}
+// Four values as the codes of their next part, each value replaced by 2^4 times what is left of it.
+__device__ __forceinline__ uint32_t take_part(float (&x)[4]) {
+    const uint32_t w = f32_to_codes(x[0], x[1], x[2], x[3]);
+    uint32_t h0, h1;
+    float y[4];
+    codes_to_f16(w, h0, h1);
+    f16x2_to_f32(h0, y[0], y[1]);
+    f16x2_to_f32(h1, y[2], y[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = (x[i] - y[i]) * kPartStep;
+    return w;
+}
+// byte offset of column `col` of row `row` in an operand of 128-byte rows, 128-byte swizzled
+__device__ __forceinline__ uint32_t swz8(int row, int col) {
+    return row * 128 + (((col >> 4) ^ (row & 7)) << 4) + (col & 15);
+}
+// Words per piece: the same on both kernels.
+__device__ __forceinline__ int words_per_piece(int total, int pieces) {
+    return max(kLineMinWordsQ8, (total + pieces - 1) / pieces);
+}
+
+template <int NG, int QP, bool MASS>
+__global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) decode_q8_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                                                  const __grid_constant__ CUtensorMap tmV,
+                                                                                  const __grid_constant__ LaneParams p) {
+    using C = Cfg<NG, QP>;
+    constexpr int S = C::kStages, HT = C::kHT, kWalk = C::kSoft / 32, kIssue = kWalk + 1;   // warps
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *state = sm + C::kOffState;
+    Tile *tiles = reinterpret_cast<Tile *>(state + kOffTile);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(state + kOffBars);
+    uint64_t *full = bars, *empty = bars + 4, *ifull = bars + 8, *iempty = bars + 12, *qready = bars + 16, *sfull = bars + 18,
+             *pready = bars + 20, *odone = bars + 22, *drain = bars + 24;
+    float *h_mu = reinterpret_cast<float *>(state + kOffHead), *h_dm = h_mu + 32, *h_dv = h_mu + 64, *h_step = h_mu + 96,
+          *h_hm = h_mu + 128, *h_slope = h_mu + 192;
+    float(*red)[32] = reinterpret_cast<float(*)[32]>(state + kOffRed);
+    float2 *angle = reinterpret_cast<float2 *>(state + kOffAngle);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(state + kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(state + kOffMisc + 4);
+
+    const AttnParams &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.group, hkv = a.hkv, B = a.num_req;
+    const int kvh = blockIdx.x % hkv, wi = blockIdx.x / hkv;
+    const int base = a.table_indptr[0];
+    const int total = a.table_indptr[B] - base;
+    if (total <= 0) return;
+    const int per = words_per_piece(total, p.warps_per_head);
+    if (wi > (total - 1) / per) return;
+    const int lo = wi * per, cnt = min(total - lo, per);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < kRecords; ++i) {
+            mbar_init(&ifull[i], 1);
+            mbar_init(&iempty[i], kWalk + 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&qready[i], kWalk);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pready[i], kWalk);
+            mbar_init(&odone[i], 1);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    // rows of the operands that hold no head stay zero
+    for (int i = threadIdx.x; i < (2 * C::kQBytes + 2 * C::kPBytes) / 16; i += C::kThreads)
+        reinterpret_cast<uint4 *>(sm + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
+    if (a.alibi && threadIdx.x < 32) h_slope[threadIdx.x] = threadIdx.x < G ? a.alibi_log2[kvh * G + threadIdx.x] : 0.f;
+    if (warp == kIssue) {
+        tc::tmem_alloc(tmem_slot, C::kCols);
+        tc::tmem_relinquish();
+    }
+    fence_proxy_async_smem();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tbase = *tmem_slot;
+    const uint32_t tO = tbase + 2 * C::kQN;
+
+    if (warp == kWalk) {
+        // ============================================================ table walk and loads
+        const bool leader = tc::elect_one();
+        if (leader) {
+            tma_prefetch_desc(&tmK);
+            tma_prefetch_desc(&tmV);
+        }
+        // the request of the first word: the largest r with table_indptr[r] <= its index
+        int r = 0, hi = B;
+        while (hi - r > 1) {
+            const int step = (hi - r + 31) >> 5, x = r + step * lane;
+            const bool below = x < hi && a.table_indptr[x] - base <= lo;
+            const int k = __popc(__ballot_sync(0xffffffffu, below)) - 1;
+            r += step * k;
+            hi = min(hi, r + step);
+        }
+        int r_beg = a.table_indptr[r] - base, r_end = a.table_indptr[r + 1] - base, qpos = a.q_pos[r];
+        int j = 0, first = 0;     // tiles; the first tile of the request
+        bool ok = true;
+        auto enter = [&]() {
+            if (lo <= r_beg && r_end - r_beg > a.max_words && kvh == 0 && lane == 0) set_status(a.d_status, LAZY_DSTATUS_BAD_TABLE);
+        };
+        // a request none of whose words here is visible has no tile to write its partial result
+        auto leave = [&]() {
+            if (j == first && lane < G)
+                p.ws_ml[((static_cast<size_t>(kvh) * (p.warps_per_head + B)) + wi + r) * G + lane] =
+                    make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+            first = j;
+        };
+        enter();
+        uint32_t wl = 0u, ml = 0u;
+        float ksl = 1.f, vsl = 1.f;
+        int b0 = INT_MIN / 2;
+        for (int k = 0; k < cnt;) {
+            if (lo + k >= r_end) {
+                leave();
+                do {
+                    ++r;
+                    r_beg = r_end;
+                    r_end = a.table_indptr[r + 1] - base;
+                } while (lo + k >= r_end);
+                qpos = a.q_pos[r];
+                enter();
+            }
+            if (k - b0 + kTileWords > 32 && b0 + 32 < cnt) {
+                // 32 words, one per lane, with their blocks' metadata and scales
+                b0 = k;
+                wl = ml = 0u;
+                if (k + lane < cnt) {
+                    wl = a.table[base + lo + k + lane];
+                    const uint32_t b = word_block(wl);
+                    if (b < static_cast<uint32_t>(a.num_blocks)) {
+                        const size_t bh = static_cast<size_t>(b) * hkv + kvh;
+                        ml = a.blk_meta[b];
+                        ksl = p.k_scale[bh];
+                        vsl = p.v_scale[bh];
+                    } else {
+                        set_status(a.d_status, LAZY_DSTATUS_BAD_BLOCK);
+                    }
+                }
+            }
+            const int i = k - b0, x = b0 + lane;             // lane `lane` holds word x
+            const int pos = word_offset(wl) + meta_j0(ml);
+            const bool mine = x >= k && x < cnt && lo + x < r_end;
+            const int lim = mine && lo + x - r_beg < a.max_words ? min(meta_valid(ml), qpos - pos + 1) : 0;
+            const uint32_t seen = __ballot_sync(0xffffffffu, lim > 0);
+            const int here = __popc(__ballot_sync(0xffffffffu, mine));      // words of the request from k on, in this batch
+            if (!((seen >> i) & 1u)) {
+                const int skip = min(here, seen ? __ffs(seen) - 1 - i : 32);
+                if (MASS)
+                    for (int y = k; y < k + skip; ++y)
+                        if (lo + y - r_beg < a.max_words && lane < G)
+                            p.ws_lse[(static_cast<size_t>(r) * a.max_words + lo + y - r_beg) * a.hq + kvh * G + lane] = -INFINITY;
+                k += skip;
+                continue;
+            }
+            const int src = (i + lane) & 31;
+            const uint32_t wk = __shfl_sync(0xffffffffu, wl, src);
+            const int lim_k = __shfl_sync(0xffffffffu, lim, src), pos_k = __shfl_sync(0xffffffffu, pos, src);
+            const float ks = __shfl_sync(0xffffffffu, ksl, src), vs = __shfl_sync(0xffffffffu, vsl, src);
+            const int off = word_offset(__shfl_sync(0xffffffffu, wl, i));
+            const bool same = lane < kTileWords && i + lane < 32 && lim_k > 0 && (a.alibi || word_offset(wk) == off);
+            const int n = __ffs(~__ballot_sync(0xffffffffu, same)) - 1;
+            const int is = j % kRecords, st = j % S;
+            ok = warp_wait(&iempty[is], ((j / kRecords) & 1) ^ 1, abort_flag, a.d_status);
+            if (!ok) break;
+            Tile &t = tiles[is];
+            if (lane < kTileWords) {
+                t.lim[lane] = lane < n ? lim_k : 0;
+                t.pos[lane] = lane < n ? pos_k : 0;
+                t.ks[lane] = lane < n ? ks : 1.f;
+                t.vs[lane] = lane < n ? vs : 1.f;
+            }
+            if (leader) {
+                t.n = n;
+                t.off = off;
+                t.req = r;
+                t.word = lo + k - r_beg;
+            }
+            __syncwarp();
+            if (leader) mbar_arrive(&ifull[is]);
+            ok = warp_wait(&empty[st], ((j / S) & 1) ^ 1, abort_flag, a.d_status);
+            if (!ok) break;
+            if (leader) mbar_arrive_expect_tx(&full[st], n * 2 * kCodeBlock);
+            __syncwarp();
+            if (lane < n) {
+                const int row = (static_cast<int>(word_block(wk)) * hkv + kvh) * kBlockTokens;
+                uint8_t *d = sm + st * kStageBytes + lane * kCodeBlock;
+                tma_load_2d(d, &tmK, 0, row, &full[st]);
+                tma_load_2d(d + kHalfStage, &tmV, 0, row, &full[st]);
+            }
+            __syncwarp();
+            ++j;
+            k += n;
+        }
+        if (ok) {
+            leave();
+            const int is = j % kRecords;
+            if (warp_wait(&iempty[is], ((j / kRecords) & 1) ^ 1, abort_flag, a.d_status)) {
+                if (leader) {
+                    tiles[is].n = 0;
+                    mbar_arrive(&ifull[is]);
+                }
+                __syncwarp();
+            }
+        }
+        // every copy lands before the kernel can end, whatever stopped the walk
+        for (int i = max(0, j - S); i < j; ++i) mbar_wait(&full[i % S], (i / S) & 1);
+    } else if (warp == kIssue) {
+        // ============================================================ MMA issue
+        //   QK(0) | QK(1) PV(0) | QK(2) PV(1) | ...; PV(i) goes first where tile i + 1 has not landed
+        const bool leader = tc::elect_one();
+        constexpr uint32_t idq = idesc_e4m3(C::kQN, false), idp = idesc_e4m3(C::kPN, true);
+        const uint64_t dA = tc::smem_desc(smem_u32(sm), 16, 1024);
+        const uint64_t dQ = tc::smem_desc(smem_u32(sm + C::kOffQ), 16, 1024), dP = tc::smem_desc(smem_u32(sm + C::kOffP), 16, 1024);
+        bool ok = true;
+        int off = 0, req = -1, qbuf = 1;       // of the tile whose QK was issued last
+        // record of tile i: words, and whether it opens a request
+        auto read = [&](int i, int &n, bool &opens) {
+            const int is = i % kRecords;
+            ok = warp_wait(&ifull[is], (i / kRecords) & 1, abort_flag, a.d_status);
+            n = ok ? tiles[is].n : 0;
+            if (n > 0) {
+                const int o = tiles[is].off, q = tiles[is].req;
+                opens = q != req;
+                if (opens || (o != off && !a.alibi)) qbuf ^= 1;   // the softmax warps count the same changes
+                off = o;
+                req = q;
+            }
+            __syncwarp();
+            if (leader) mbar_arrive(&iempty[is]);
+        };
+        auto qk = [&](int i) {
+            const int st = i % S;
+            if (!warp_wait(&full[st], (i / S) & 1, abort_flag, a.d_status) ||
+                !warp_wait(&qready[i & 1], (i >> 1) & 1, abort_flag, a.d_status)) {
+                ok = false;
+                return;
+            }
+            tc::fence_after_sync();
+            if (leader) {
+                const uint64_t ka = dA + static_cast<uint64_t>((st * kStageBytes) >> 4);
+                const uint64_t qb = dQ + static_cast<uint64_t>((qbuf * C::kQBytes) >> 4);
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    mma_e4m3(tbase + (i & 1) * C::kQN, ka + 2 * s, qb + 2 * s, idq, s > 0 ? 1u : 0u);
+                tc::commit(&sfull[i & 1]);
+            }
+            __syncwarp();
+        };
+        int n = 0, n1 = 0;
+        bool opens = true, opens1 = true;
+        read(0, n, opens);
+        if (n > 0) qk(0);
+        for (int i = 0; ok && n > 0; ++i) {
+            read(i + 1, n1, opens1);
+            if (!ok) break;
+            const bool early = n1 > 0 && __all_sync(0xffffffffu, mbar_test_wait(&full[(i + 1) % S], ((i + 1) / S) & 1));
+            if (early) {
+                qk(i + 1);
+                if (!ok) break;
+            }
+            if (!warp_wait(&pready[i & 1], (i >> 1) & 1, abort_flag, a.d_status)) break;
+            tc::fence_after_sync();
+            if (leader) {
+                const int st = i % S;
+                const uint64_t va = dA + static_cast<uint64_t>((st * kStageBytes + kHalfStage) >> 4);
+                const uint64_t pb = dP + static_cast<uint64_t>(((i & 1) * C::kPBytes) >> 4);
+                for (int s = 0; 2 * s < n; ++s)
+                    mma_e4m3(tO, va + static_cast<uint64_t>((s * 32 * 128) >> 4), pb + 2 * s, idp, (opens && s == 0) ? 0u : 1u);
+                tc::commit(&empty[st]);
+                tc::commit(&odone[i & 1]);
+            }
+            __syncwarp();
+            if (n1 > 0 && !early) qk(i + 1);
+            n = n1;
+            opens = opens1;
+        }
+        if (leader) tc::commit(drain);
+        __syncwarp();
+        mbar_wait(drain, 0);
+    } else {
+        // ============================================================ softmax
+        const int t = threadIdx.x & 127, wq = warp & 3;   // key of the tile, later head dim; warp of the group
+        const int g0 = (threadIdx.x >> 7) * HT;           // first head of this thread
+        const uint32_t lane_off = static_cast<uint32_t>(32 * wq) << 16;
+        float l[HT];
+        int qbuf = 1, cur_req = -1, cur_off = 0;   // of the Q operand made last
+        // the query of tile `tl` as e4m3 parts, if it is not the one made last
+        auto query = [&](const Tile &tl) {
+            const int off = tl.off, r = tl.req;
+            if (r == cur_req && (off == cur_off || a.alibi)) return;
+            qbuf ^= 1;
+            cur_req = r;
+            cur_off = off;
+            if (threadIdx.x < kHalfDim)
+                rope_cos_sin(a.alibi ? 0 : a.q_pos[r] - off, a.rope.theta[threadIdx.x], angle[threadIdx.x].x, angle[threadIdx.x].y);
+            sync_softmax<C::kSoft>();
+            uint8_t *qd = sm + C::kOffQ + qbuf * C::kQBytes;
+            // 16 threads per head: dims 4c .. + 3 and 64 above
+            const int c = threadIdx.x & 15;
+            for (int h0 = 0; h0 < G; h0 += C::kSoft / 16) {
+                const int h = h0 + (threadIdx.x >> 4);
+                uint2 lo2 = make_uint2(0u, 0u), hi2 = lo2;
+                if (h < G) {
+                    const uint2 *q = reinterpret_cast<const uint2 *>(a.q_raw + (static_cast<size_t>(r) * a.hq + kvh * G + h) * kHeadDim);
+                    lo2 = __ldg(q + c);
+                    hi2 = __ldg(q + 16 + c);
+                }
+                const float av[4] = {bf16_lo(lo2.x), bf16_hi(lo2.x), bf16_lo(lo2.y), bf16_hi(lo2.y)};
+                const float bv[4] = {bf16_lo(hi2.x), bf16_hi(hi2.x), bf16_lo(hi2.y), bf16_hi(hi2.y)};
+                float am = 0.f;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) am = fmaxf(am, fmaxf(fabsf(av[u]), fabsf(bv[u])));
+#pragma unroll
+                for (int x = 1; x < 16; x <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, x));
+                // largest element in [128, 256): a rotation keeps it below 363; e = 0 for an all-zero or non-finite head
+                int e = static_cast<int>(__float_as_uint(am) >> 23) - 127;
+                e = (am == 0.f || e == 128) ? 0 : max(-119, e);
+                const float dn = __uint_as_float(static_cast<uint32_t>(134 - e) << 23);   // 2^(7 - e)
+                float x[4], y[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float2 z = angle[4 * c + u];
+                    const float xa = av[u] * dn, xb = bv[u] * dn;
+                    x[u] = xa * z.x - xb * z.y;
+                    y[u] = xb * z.x + xa * z.y;
+                }
+                if (h < G) {
+#pragma unroll
+                    for (int part = 0; part < QP; ++part) {
+                        const int row = part * NG + h;
+                        *reinterpret_cast<uint32_t *>(qd + swz8(row, 4 * c)) = take_part(x);
+                        *reinterpret_cast<uint32_t *>(qd + swz8(row, 64 + 4 * c)) = take_part(y);
+                    }
+                    if (c == 0) h_hm[32 * qbuf + h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.scale_log2 * 0x1p-7f);
+                }
+            }
+            if (threadIdx.x >= G && threadIdx.x < 32) h_hm[32 * qbuf + threadIdx.x] = 0.f;
+            fence_proxy_async_smem();
+            sync_softmax<C::kSoft>();   // hm and the angles' next use
+        };
+        bool ok = warp_wait(&ifull[0], 0, abort_flag, a.d_status);
+        // (one decision for all four warps, which meet at barriers from here on)
+        ok = !any_softmax<C::kSoft>(!ok);
+        int n = ok ? tiles[0].n : 0;
+        if (n > 0) {
+            query(tiles[0]);
+            if (lane == 0) mbar_arrive(&qready[0]);
+        }
+        bool opens = true;
+        for (int i = 0; ok && n > 0; ++i) {
+            const Tile &tl = tiles[i % kRecords];
+            const int buf = i & 1, my_q = qbuf;
+            // ---- the next tile's record, and its query
+            const Tile &nx = tiles[(i + 1) % kRecords];
+            ok = !any_softmax<C::kSoft>(!warp_wait(&ifull[(i + 1) % kRecords], ((i + 1) / kRecords) & 1, abort_flag, a.d_status));
+            if (!ok) break;
+            const int n_next = nx.n;
+            const int r = tl.req;
+            const bool closes = n_next == 0 || nx.req != r;
+            if (n_next > 0) {
+                query(nx);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&qready[(i + 1) & 1]);
+            }
+            if (opens) {
+#pragma unroll
+                for (int h = 0; h < HT; ++h) l[h] = 0.f;
+                if (threadIdx.x < 32) {
+                    h_mu[threadIdx.x] = 0.f;
+                    h_dm[threadIdx.x] = INFINITY;
+                    h_dv[threadIdx.x] = 0.f;
+                }
+                sync_softmax<C::kSoft>();
+            }
+            // ---- scores
+            const int blk = t >> 4, slot = t & 15;
+            const int lim = tl.lim[blk];
+            const bool vis = slot < lim;
+            const float ks = tl.ks[blk], vs = tl.vs[blk], lv = log2_of(vs);
+            const float dpos = a.alibi ? static_cast<float>(tl.pos[blk] + slot - a.q_pos[r]) : 0.f;
+            ok = !any_softmax<C::kSoft>(!warp_wait(&sfull[buf], (i >> 1) & 1, abort_flag, a.d_status));
+            if (!ok) break;
+            tc::fence_after_sync();
+            float x[HT];
+            {
+                uint32_t sv[QP][HT];
+#pragma unroll
+                for (int part = 0; part < QP; ++part) tmem_load<HT>(tbase + lane_off + buf * C::kQN + part * NG + g0, sv[part]);
+                tc::wait_ld();
+#pragma unroll
+                for (int h = 0; h < HT; ++h) {
+                    float s = __uint_as_float(sv[QP - 1][h]);
+#pragma unroll
+                    for (int part = QP - 2; part >= 0; --part) s = fmaf(s, 1.f / kPartStep, __uint_as_float(sv[part][h]));
+                    x[h] = fmaf(s, ks * h_hm[32 * my_q + g0 + h], -h_mu[g0 + h]);
+                    if (a.alibi) x[h] = fmaf(h_slope[g0 + h], dpos, x[h]);
+                    if (!vis) x[h] = -INFINITY;
+                }
+            }
+            bool past = false;
+#pragma unroll
+            for (int h = 0; h < HT; ++h) past |= x[h] + fmaxf(lv + h_dm[g0 + h], 0.f) > kSlack;
+            if (any_softmax<C::kSoft>(past)) {
+                // ---- references (mu for the row sums, mo for score + log2 of the V scale) move to the new maxima
+                float top[HT];
+#pragma unroll
+                for (int pass = 0; pass < 2; ++pass) {
+                    // pass 0: of the scores; pass 1: of score + log2 of the V scale
+#pragma unroll
+                    for (int h = 0; h < HT; ++h) {
+                        float m = pass ? x[h] + lv : x[h];
+#pragma unroll
+                        for (int y = 16; y > 0; y >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
+                        if (lane == 0) red[wq][g0 + h] = m;
+                    }
+                    sync_softmax<C::kSoft>();
+#pragma unroll
+                    for (int h = 0; h < HT; ++h) {
+                        const int gh = g0 + h;
+                        const float m = fmaxf(fmaxf(red[0][gh], red[1][gh]), fmaxf(red[2][gh], red[3][gh]));
+                        if (pass == 0) {
+                            // how far mu moves: to the first maximum, or up
+                            top[h] = m == -INFINITY ? 0.f : h_dm[gh] == INFINITY ? m : fmaxf(m, 0.f);
+                        } else if (t == h) {
+                            const bool none = m == -INFINITY, fresh = h_dm[gh] == INFINITY;
+                            const float mo_old = h_mu[gh] - h_dm[gh], mo_new = h_mu[gh] + m;
+                            const float mo = fresh ? mo_new : fmaxf(mo_old, mo_new);
+                            h_step[gh] = none || fresh ? 1.f : fast_exp2(mo_old - mo);
+                            if (!none) {
+                                h_mu[gh] += top[h];
+                                h_dm[gh] = h_mu[gh] - mo;
+                                // weights times 2^7; 2^-20 of it later, as s_v spans the range of a float
+                                h_dv[gh] = fast_exp2(fminf(h_dm[gh] - 13.f, 126.f));
+                            }
+                        }
+                    }
+                    sync_softmax<C::kSoft>();
+                }
+#pragma unroll
+                for (int h = 0; h < HT; ++h) {
+                    x[h] -= top[h];
+                    if (top[h] > 0.f) l[h] *= fast_exp2(-top[h]);   // (at the first maximum l is 0)
+                }
+                if (!opens) {
+                    // O of the tiles before, once the last product is done
+                    ok = !any_softmax<C::kSoft>(!warp_wait(&odone[buf ^ 1], ((i - 1) >> 1) & 1, abort_flag, a.d_status));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int part = 0; part < 3; ++part)
+#pragma unroll
+                        for (int h = 0; h < HT; h += 4) {
+                            const uint32_t col = tO + lane_off + part * NG + g0 + h;
+                            uint32_t o[4];
+                            tmem_load<4>(col, o);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * h_step[g0 + h + y]);
+                            tmem_store4(col, o);
+                        }
+                    tc::wait_st();
+                    tc::fence_before_sync();
+                }
+            }
+            // ---- weights, their sums, and their parts as the P operand
+#pragma unroll
+            for (int h = 0; h < HT; ++h) {
+                x[h] = fast_exp2(x[h]);
+                l[h] += x[h];
+            }
+            uint8_t *pd = sm + C::kOffP + buf * C::kPBytes;
+#pragma unroll
+            for (int h = 0; h < HT; h += 4) {
+                float w[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) w[y] = vis ? x[h + y] * (vs * h_dv[g0 + h + y] * 0x1p20f) : 0.f;
+#pragma unroll
+                for (int part = 0; part < 3; ++part) {
+                    const uint32_t codes = take_part(w);
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) pd[swz8(part * NG + g0 + h + y, t)] = static_cast<uint8_t>(codes >> (8 * y));
+                }
+            }
+            // a weight of 0 does not undo a NaN in a slot that the query does not see
+            if (!vis && g0 == 0 && t < ((n + 1) & ~1) * kBlockTokens) {
+                mbar_wait(&full[i % S], (i / S) & 1);
+                uint4 *row = reinterpret_cast<uint4 *>(sm + (i % S) * kStageBytes + kHalfStage + t * 128);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) row[y] = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pready[buf]);
+            if (MASS) {
+                // sum over the 16 lanes of a word, the heads spread over the lanes on the way
+                float v[HT];
+#pragma unroll
+                for (int h = 0; h < HT; ++h) v[h] = x[h];
+                int head = 0, left = HT;
+#pragma unroll
+                for (int bit = 8; bit > 0; bit >>= 1) {
+                    if (left > 1) {
+                        left >>= 1;
+                        const bool up = (lane & bit) != 0;
+                        if (up) head += left;
+#pragma unroll
+                        for (int h = 0; h < HT / 2; ++h)
+                            if (h < left) {
+                                const float keep = up ? v[h + left] : v[h], send = up ? v[h] : v[h + left];
+                                v[h] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+                            }
+                    } else {
+                        v[0] += __shfl_xor_sync(0xffffffffu, v[0], bit);
+                    }
+                }
+                // HT lanes of the word hold a head each
+                if (blk < n && (slot & (16 / HT - 1)) == 0 && g0 + head < G)
+                    p.ws_lse[(static_cast<size_t>(r) * a.max_words + tl.word + blk) * a.hq + kvh * G + g0 + head] =
+                        h_mu[g0 + head] + log2_of(v[0]);
+            }
+            if (closes) {
+                // ---- the request's partial result
+                ok = !any_softmax<C::kSoft>(!warp_wait(&odone[buf], (i >> 1) & 1, abort_flag, a.d_status));
+                if (!ok) break;
+                tc::fence_after_sync();
+                const size_t slot_g = (static_cast<size_t>(kvh) * (p.warps_per_head + B) + wi + r) * G;
+#pragma unroll
+                for (int h = 0; h < HT; ++h) {
+                    float s = l[h];
+#pragma unroll
+                    for (int y = 16; y > 0; y >>= 1) s += __shfl_xor_sync(0xffffffffu, s, y);
+                    if (lane == 0) red[wq][g0 + h] = s;
+                }
+                sync_softmax<C::kSoft>();
+                if (threadIdx.x < G) {
+                    const int h = threadIdx.x;
+                    const float s = (red[0][h] + red[1][h]) + (red[2][h] + red[3][h]);
+                    const bool none = h_dm[h] == INFINITY && s == s;
+                    p.ws_ml[slot_g + h] = none ? make_float4(-INFINITY, 0.f, -INFINITY, 0.f)
+                                               : make_float4(h_mu[h], s, h_mu[h] - h_dm[h], 0.f);
+                }
+#pragma unroll
+                for (int h = 0; h < HT; h += 4) {
+                    uint32_t o[3][4];
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) tmem_load<4>(tO + lane_off + part * NG + g0 + h, o[part]);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        if (g0 + h + y < G) {
+                            float v = fmaf(__uint_as_float(o[2][y]), 1.f / kPartStep, __uint_as_float(o[1][y]));
+                            v = fmaf(v, 1.f / kPartStep, __uint_as_float(o[0][y]));
+                            a.ws_acc[(slot_g + g0 + h + y) * kHeadDim + t] = v * 0x1p-7f;
+                        }
+                }
+                tc::fence_before_sync();
+                sync_softmax<C::kSoft>();   // red and the heads' state before the next request writes them
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&iempty[i % kRecords]);
+            opens = closes;
+            n = n_next;
+        }
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == kIssue) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tbase, C::kCols);
+    }
+}
+
+template <int NG, int QP, bool MASS>
+cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
+    using C = Cfg<NG, QP>;
+    auto kern = decode_q8_kernel<NG, QP, MASS>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<p.warps_per_head * p.a.hkv, C::kThreads, C::kSmem, s>>>(tk, tv, p);
+    return cudaGetLastError();
+}
+template <int NG>
+cudaError_t launch_g(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
+    return p.mass ? launch_t<NG, 5, true>(tk, tv, p, s) : launch_t<NG, 3, false>(tk, tv, p, s);
+}
+template <int QP>
+int occupancy(int group) {
+    return group <= 4 ? Cfg<4, QP>::kOcc : group <= 8 ? Cfg<8, QP>::kOcc : group <= 16 ? Cfg<16, QP>::kOcc : Cfg<32, QP>::kOcc;
+}
+
+}  // namespace
+
+LanePlan decode_q8_plan(int num_req, int hkv, int max_words, int group, bool mass, int sms) {
+    // one wave of resident CTAs, at least one tile of words each
+    const int64_t words = static_cast<int64_t>(num_req) * max_words;
+    const int64_t most = (words + kLineMinWordsQ8 - 1) / kLineMinWordsQ8;
+    const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * (mass ? occupancy<5>(group) : occupancy<3>(group)) / hkv;
+    LanePlan pl;
+    pl.warps_per_head = static_cast<int>(most < resident ? most : resident);
+    if (pl.warps_per_head < 1) pl.warps_per_head = 1;
+    pl.slots = static_cast<int64_t>(hkv) * (pl.warps_per_head + num_req);
+    return pl;
+}
+
+cudaError_t launch_decode_q8(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
+    const int g = p.a.group;
+    const cudaError_t e = g <= 4    ? launch_g<4>(tk, tv, p, s)
+                          : g <= 8  ? launch_g<8>(tk, tv, p, s)
+                          : g <= 16 ? launch_g<16>(tk, tv, p, s)
+                                    : launch_g<32>(tk, tv, p, s);
+    return e == cudaSuccess ? launch_lane_combine(p, kLineMinWordsQ8, s) : e;
+}
+
+}  // namespace lazy

@@ -154,6 +154,12 @@ struct LanePlan {
 LanePlan lane_plan(int num_req, int hkv, int max_words, int group, bool q8, bool mass, int sms);
 // tk, tv: the codes as rows of 128 bytes (one box = one block of one head), or the bf16 pools as rows of 128
 // elements (one box = half of one).
+// Joins the partials of every request; min_words: the least words of a piece of the line.
+cudaError_t launch_lane_combine(const LaneParams &p, int min_words, cudaStream_t s);
+// Decode over the 8-bit pool (decode_q8.cu): warps_per_head is the number of pieces, one CTA each.
+constexpr int kLineMinWordsQ8 = 8;
+LanePlan decode_q8_plan(int num_req, int hkv, int max_words, int group, bool mass, int sms);
+cudaError_t launch_decode_q8(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s);
 cudaError_t launch_decode_lane(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, bool q8, cudaStream_t s);
 
 // Prefill over the 8-bit pool (prefill_q8.cu).  a.q_prep: prepared query tiles; row_scale: their row
