@@ -42,7 +42,9 @@ constexpr int kTileWords = 8;
 constexpr int kCodeBlock = kBlockTokens * kHeadDim;              // codes of one block of one head
 constexpr int kHalfStage = kTileWords * kCodeBlock, kStageBytes = 2 * kHalfStage;
 constexpr int kRecords = 4;
-constexpr float kSlack = 1.75f;       // log2 units by which a score may pass its reference: weights times 2^7 stay below 448
+// A reference is set kMargin above the largest score seen, and moves when a score passes it by kSlack (log2
+// units): weights times 2^7 stay below 448, the largest is 2^4 or more, and few tiles move a reference.
+constexpr float kSlack = 1.75f, kMargin = 3.f;
 constexpr float kPartStep = 16.f;     // between parts
 
 // One tile of the walk; n = 0 ends it.
@@ -475,9 +477,18 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             fence_proxy_async_smem();
             sync_softmax<C::kSoft>();   // hm and the angles' next use
         };
-        bool ok = warp_wait(&ifull[0], 0, abort_flag, a.d_status);
-        // (one decision for all four warps, which meet at barriers from here on)
-        ok = !any_softmax<C::kSoft>(!ok);
+        auto open = [&]() {
+#pragma unroll
+            for (int h = 0; h < HT; ++h) l[h] = 0.f;
+            if (threadIdx.x < 32) {
+                h_mu[threadIdx.x] = 0.f;
+                h_dm[threadIdx.x] = INFINITY;
+                h_dv[threadIdx.x] = 0.f;
+            }
+        };
+        open();
+        // (the softmax warps take one decision on waits, as they meet at barriers)
+        bool ok = !any_softmax<C::kSoft>(!warp_wait(&ifull[0], 0, abort_flag, a.d_status));
         int n = ok ? tiles[0].n : 0;
         if (n > 0) {
             query(tiles[0]);
@@ -485,38 +496,16 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
         }
         bool opens = true;
         for (int i = 0; ok && n > 0; ++i) {
-            const Tile &tl = tiles[i % kRecords];
-            const int buf = i & 1, my_q = qbuf;
-            // ---- the next tile's record, and its query
-            const Tile &nx = tiles[(i + 1) % kRecords];
-            ok = !any_softmax<C::kSoft>(!warp_wait(&ifull[(i + 1) % kRecords], ((i + 1) / kRecords) & 1, abort_flag, a.d_status));
-            if (!ok) break;
-            const int n_next = nx.n;
-            const int r = tl.req;
-            const bool closes = n_next == 0 || nx.req != r;
-            if (n_next > 0) {
-                query(nx);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&qready[(i + 1) & 1]);
-            }
-            if (opens) {
-#pragma unroll
-                for (int h = 0; h < HT; ++h) l[h] = 0.f;
-                if (threadIdx.x < 32) {
-                    h_mu[threadIdx.x] = 0.f;
-                    h_dm[threadIdx.x] = INFINITY;
-                    h_dv[threadIdx.x] = 0.f;
-                }
-                sync_softmax<C::kSoft>();
-            }
+            const Tile &tl = tiles[i % kRecords], &nx = tiles[(i + 1) % kRecords];
+            const int buf = i & 1, my_q = qbuf, r = tl.req;
             // ---- scores
             const int blk = t >> 4, slot = t & 15;
             const int lim = tl.lim[blk];
             const bool vis = slot < lim;
             const float ks = tl.ks[blk], vs = tl.vs[blk], lv = log2_of(vs);
             const float dpos = a.alibi ? static_cast<float>(tl.pos[blk] + slot - a.q_pos[r]) : 0.f;
-            ok = !any_softmax<C::kSoft>(!warp_wait(&sfull[buf], (i >> 1) & 1, abort_flag, a.d_status));
-            if (!ok) break;
+            const bool got = warp_wait(&sfull[buf], (i >> 1) & 1, abort_flag, a.d_status) &&
+                             warp_wait(&ifull[(i + 1) % kRecords], ((i + 1) / kRecords) & 1, abort_flag, a.d_status);
             tc::fence_after_sync();
             float x[HT];
             {
@@ -525,19 +514,32 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 for (int part = 0; part < QP; ++part) tmem_load<HT>(tbase + lane_off + buf * C::kQN + part * NG + g0, sv[part]);
                 tc::wait_ld();
 #pragma unroll
-                for (int h = 0; h < HT; ++h) {
-                    float s = __uint_as_float(sv[QP - 1][h]);
+                for (int h = 0; h < HT; h += 4) {
+                    const float4 hm = *reinterpret_cast<const float4 *>(&h_hm[32 * my_q + g0 + h]);
+                    const float4 mu = *reinterpret_cast<const float4 *>(&h_mu[g0 + h]);
+                    const float hm4[4] = {hm.x, hm.y, hm.z, hm.w}, mu4[4] = {mu.x, mu.y, mu.z, mu.w};
 #pragma unroll
-                    for (int part = QP - 2; part >= 0; --part) s = fmaf(s, 1.f / kPartStep, __uint_as_float(sv[part][h]));
-                    x[h] = fmaf(s, ks * h_hm[32 * my_q + g0 + h], -h_mu[g0 + h]);
-                    if (a.alibi) x[h] = fmaf(h_slope[g0 + h], dpos, x[h]);
-                    if (!vis) x[h] = -INFINITY;
+                    for (int y = 0; y < 4; ++y) {
+                        float s = __uint_as_float(sv[QP - 1][h + y]);
+#pragma unroll
+                        for (int part = QP - 2; part >= 0; --part)
+                            s = fmaf(s, 1.f / kPartStep, __uint_as_float(sv[part][h + y]));
+                        x[h + y] = fmaf(s, ks * hm4[y], -mu4[y]);
+                        if (a.alibi) x[h + y] = fmaf(h_slope[g0 + h + y], dpos, x[h + y]);
+                        if (!vis) x[h + y] = -INFINITY;
+                    }
                 }
             }
-            bool past = false;
+            bool past = !got;
 #pragma unroll
-            for (int h = 0; h < HT; ++h) past |= x[h] + fmaxf(lv + h_dm[g0 + h], 0.f) > kSlack;
+            for (int h = 0; h < HT; h += 4) {
+                const float4 dm = *reinterpret_cast<const float4 *>(&h_dm[g0 + h]);
+                past |= x[h] + fmaxf(lv + dm.x, 0.f) > kSlack || x[h + 1] + fmaxf(lv + dm.y, 0.f) > kSlack ||
+                        x[h + 2] + fmaxf(lv + dm.z, 0.f) > kSlack || x[h + 3] + fmaxf(lv + dm.w, 0.f) > kSlack;
+            }
             if (any_softmax<C::kSoft>(past)) {
+                ok = !any_softmax<C::kSoft>(!got);
+                if (!ok) break;
                 // ---- references (mu for the row sums, mo for score + log2 of the V scale) move to the new maxima
                 float top[HT];
 #pragma unroll
@@ -556,12 +558,12 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                         const int gh = g0 + h;
                         const float m = fmaxf(fmaxf(red[0][gh], red[1][gh]), fmaxf(red[2][gh], red[3][gh]));
                         if (pass == 0) {
-                            // how far mu moves: to the first maximum, or up
-                            top[h] = m == -INFINITY ? 0.f : h_dm[gh] == INFINITY ? m : fmaxf(m, 0.f);
+                            // how far mu moves
+                            top[h] = m != -INFINITY && (h_dm[gh] == INFINITY || m > kSlack) ? m + kMargin : 0.f;
                         } else if (t == h) {
                             const bool none = m == -INFINITY, fresh = h_dm[gh] == INFINITY;
                             const float mo_old = h_mu[gh] - h_dm[gh], mo_new = h_mu[gh] + m;
-                            const float mo = fresh ? mo_new : fmaxf(mo_old, mo_new);
+                            const float mo = fresh || mo_new > mo_old + kSlack ? mo_new + kMargin : mo_old;
                             h_step[gh] = none || fresh ? 1.f : fast_exp2(mo_old - mo);
                             if (!none) {
                                 h_mu[gh] += top[h];
@@ -599,6 +601,14 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                     tc::fence_before_sync();
                 }
             }
+            // ---- the next tile's query, so that its scores are computed meanwhile
+            const int n_next = nx.n;
+            const bool closes = n_next == 0 || nx.req != r;
+            if (n_next > 0) {
+                query(nx);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&qready[buf ^ 1]);
+            }
             // ---- weights, their sums, and their parts as the P operand
 #pragma unroll
             for (int h = 0; h < HT; ++h) {
@@ -608,9 +618,11 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             uint8_t *pd = sm + C::kOffP + buf * C::kPBytes;
 #pragma unroll
             for (int h = 0; h < HT; h += 4) {
+                const float4 dv = *reinterpret_cast<const float4 *>(&h_dv[g0 + h]);
+                const float dv4[4] = {dv.x, dv.y, dv.z, dv.w};
                 float w[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) w[y] = vis ? x[h + y] * (vs * h_dv[g0 + h + y] * 0x1p20f) : 0.f;
+                for (int y = 0; y < 4; ++y) w[y] = vis ? x[h + y] * (vs * dv4[y] * 0x1p20f) : 0.f;
 #pragma unroll
                 for (int part = 0; part < 3; ++part) {
                     const uint32_t codes = take_part(w);
@@ -692,7 +704,9 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                         }
                 }
                 tc::fence_before_sync();
-                sync_softmax<C::kSoft>();   // red and the heads' state before the next request writes them
+                sync_softmax<C::kSoft>();
+                open();
+                sync_softmax<C::kSoft>();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&iempty[i % kRecords]);
