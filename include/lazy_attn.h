@@ -315,7 +315,8 @@ size_t lazy_decode_q8_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, int
  * (so a request's accumulators grow by Hq in all per call, or by nothing if its query sees no
  * key).  Sums are taken in a fixed order: the same inputs give the same bits.  Words past
  * max_words of a request (LAZY_DSTATUS_BAD_TABLE) are ignored.  NaN or garbage in slots that
- * the query does not see has no influence. */
+ * the query does not see has no influence.  q_raw, out: 8-byte aligned (LAZY_EINVAL).
+ * num_req <= 2^24, and with block_mass max_words <= 2^20 (LAZY_ERANGE). */
 int lazy_decode_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_pos, int num_req,
                         const uint32_t *table, const int32_t *table_indptr, int max_words,
                         const lazy_q8_pool *pool, uint16_t *out, float *block_mass, void *workspace,

@@ -246,13 +246,13 @@ int lane_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_
     if (rc) return rc;
     if (num_req == 0) return LAZY_OK;
     if (!q_raw || !q_pos || (num_blocks > 0 && !k)) return LAZY_EINVAL;
-    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q_raw, q8 ? 8 : 4)) return LAZY_EINVAL;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q_raw, 8) || !aligned(out, 8)) return LAZY_EINVAL;
     if (max_words == 0 || num_blocks == 0)
         // nothing can be visible: every output row is zero
         return launch_rc(cudaMemsetAsync(out, 0, static_cast<size_t>(num_req) * p.a.hq * 128 * 2,
                                          static_cast<cudaStream_t>(stream)));
-    // one CTA per output row, and with block mass one per 32 words of a request
-    if (static_cast<int64_t>(num_req) * (p.a.hq + (mass ? max_words / 32 + 1 : 0)) > INT32_MAX) return LAZY_ERANGE;
+    // the joining grid is (requests, heads, and with block mass 32 words of a request each)
+    if (num_req > (1 << 24) || (mass && max_words > (1 << 20))) return LAZY_ERANGE;
     LanePlan pl;
     const size_t need = lane_ws(cfg, num_req, max_words, q8, mass != nullptr, pl);
     if (!workspace || ws_bytes < need) return LAZY_EWORKSPACE;

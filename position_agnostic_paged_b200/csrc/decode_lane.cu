@@ -34,6 +34,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pdl.cuh"
 #include "q8.cuh"
 
 namespace lazy {
@@ -118,6 +119,7 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
     decode_lane_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ LaneParams p) {
     using C = Cfg<Q8, NT, MASS>;
+    pdl_trigger();
     constexpr int QP = C::QP, S = C::kStages, kWarps = C::kWarps;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -580,89 +582,115 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
 // ---------------------------------------------------------------------------- joining the partials
 constexpr int kMassWords = 32;   // words per CTA of the mass part
 
-// CTAs 0 .. num_req * Hq - 1: out[r][h] from the request's partials.  The CTAs behind them: the
-// word accumulators, mass[w] += sum_h 2^(lse[w][h] - z_h), z_h = M_h + log2 L_h, one warp per word.
-__global__ void __launch_bounds__(128) lane_combine_kernel(const __grid_constant__ LaneParams p, int min_words) {
+// Maximum and sum of a head's partials: M = max m_i, L = sum l_i 2^(m_i - M), and the largest output reference; the
+// whole warp, partials over its lanes.
+__device__ __forceinline__ void join_head(const float4 *ml, int nw, int G, int lane, float &M, float &L, float &MO) {
+    M = MO = -INFINITY;
+    L = 0.f;
+    for (int i = lane; i < nw; i += 32) {
+        const float4 v = ml[static_cast<size_t>(i) * G];
+        M = fmaxf(M, v.x);
+        MO = fmaxf(MO, v.z);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) {
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, x));
+    }
+    const float mu = M == -INFINITY ? 0.f : M;
+    for (int i = lane; i < nw; i += 32) {
+        const float4 v = ml[static_cast<size_t>(i) * G];
+        L += v.y * fast_exp2(v.x - mu);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+}
+
+// Grid (request, y).  y < heads / heads per CTA: out[r][h] from the request's partials, four head dims per lane; one
+// head per warp, or (JOIN warps, where a request has many partials) one per CTA with every JOIN-th partial
+// per warp.  y behind them: the word accumulators, mass[w] += sum_h 2^(lse[w][h] - z_h), z_h = M_h + log2 L_h.
+// One warp per word.
+template <int JOIN>
+__global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kernel(const __grid_constant__ LaneParams p, int min_words) {
+    constexpr int kWarps = JOIN > 1 ? JOIN : 4;
+    pdl_wait();
     const AttnParams &a = p.a;
-    const int B = a.num_req, G = a.group, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const bool for_out = static_cast<int>(blockIdx.x) < B * a.hq;
-    const int chunks = (a.max_words + kMassWords - 1) / kMassWords;
-    const int mi = blockIdx.x - B * a.hq;
-    const int r = for_out ? blockIdx.x / a.hq : mi / chunks;
+    const unsigned B = a.num_req, G = a.group, hq = a.hq;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned r = blockIdx.x, out_ctas = JOIN > 1 ? hq : (hq + 3) / 4;
     const int base = a.table_indptr[0];
-    const int total = a.table_indptr[B] - base;
-    const int beg = a.table_indptr[r] - base;
-    const int n = min(a.table_indptr[r + 1] - base - beg, a.max_words);
-    const int per = max(min_words, (total + p.warps_per_head - 1) / p.warps_per_head);
-    const int w0 = n > 0 ? beg / per : 0, nw = n > 0 ? (beg + n - 1) / per - w0 + 1 : 0;
-    if (for_out) {
-        __shared__ float red[4][2], wgt[128], lsum[4];
-        const int h = blockIdx.x % a.hq, kvh = h / G, g = h % G;
+    const unsigned total = a.table_indptr[B] - base;
+    const unsigned beg = a.table_indptr[r] - base;
+    const int n = min(a.table_indptr[r + 1] - base - static_cast<int>(beg), a.max_words);
+    const unsigned per = max(static_cast<unsigned>(min_words), (total + p.warps_per_head - 1) / static_cast<unsigned>(p.warps_per_head));
+    const unsigned w0 = n > 0 ? beg / per : 0;
+    const int nw = n > 0 ? static_cast<int>((beg + n - 1) / per - w0 + 1) : 0;
+    if (blockIdx.y < out_ctas) {
+        const unsigned h = JOIN > 1 ? blockIdx.y : blockIdx.y * 4 + warp;
+        if (h >= hq) return;
+        const unsigned kvh = h / G, g = h - kvh * G;
         const size_t s0 = static_cast<size_t>(kvh) * (p.warps_per_head + B) + w0 + r;
-        float M = -INFINITY, MO = -INFINITY;
-        for (int i = tid; i < nw; i += 128) {
-            const float4 ml = p.ws_ml[(s0 + i) * G + g];
-            M = fmaxf(M, ml.x);
-            MO = fmaxf(MO, ml.z);
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) {
-            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-            MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, x));
-        }
-        if (lane == 0) {
-            red[warp][0] = M;
-            red[warp][1] = MO;
-        }
-        __syncthreads();
-        M = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
-        MO = fmaxf(fmaxf(red[0][1], red[1][1]), fmaxf(red[2][1], red[3][1]));
+        const float4 *ml = p.ws_ml + s0 * G + g;
+        float M, L, MO;
+        join_head(ml, nw, G, lane, M, L, MO);
         const float mu = M == -INFINITY ? 0.f : M, mou = MO == -INFINITY ? 0.f : MO;
-        float L = 0.f, A = 0.f;
-        for (int i0 = 0; i0 < nw; i0 += 128) {
-            if (i0 > 0) __syncthreads();
-            if (i0 + tid < nw) {
-                const float4 ml = p.ws_ml[(s0 + i0 + tid) * G + g];
-                L += ml.y * fast_exp2(ml.x - mu);
-                wgt[tid] = fast_exp2(ml.z - mou);
+        const float4 *acc = reinterpret_cast<const float4 *>(a.ws_acc + (s0 * G + g) * kHeadDim) + lane;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll (JOIN > 1 ? 8 : 2)
+        for (int i = JOIN > 1 ? warp : 0; i < nw; i += JOIN) {
+            const float w = fast_exp2(ml[static_cast<size_t>(i) * G].z - mou);
+            if (w != 0.f) {   // (a partial without keys has no acc)
+                const float4 v = acc[static_cast<size_t>(i) * G * (kHeadDim / 4)];
+                A.x += w * v.x;
+                A.y += w * v.y;
+                A.z += w * v.z;
+                A.w += w * v.w;
             }
-            __syncthreads();
-            const int m = min(128, nw - i0);
-            const float *acc = a.ws_acc + ((s0 + i0) * G + g) * kHeadDim + tid;
-#pragma unroll 8
-            for (int i = 0; i < m; ++i)
-                if (wgt[i] != 0.f) A += wgt[i] * acc[static_cast<size_t>(i) * G * kHeadDim];   // (a partial without keys has no acc)
         }
+        if constexpr (JOIN > 1) {
+            __shared__ float4 part[JOIN][32];
+            part[warp][lane] = A;
+            __syncthreads();
+            if (warp != 0) return;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
-        if (lane == 0) lsum[warp] = L;
-        __syncthreads();
-        L = (lsum[0] + lsum[1]) + (lsum[2] + lsum[3]);
+            for (int x = 1; x < JOIN; ++x) {
+                const float4 v = part[x][lane];
+                A.x += v.x;
+                A.y += v.y;
+                A.z += v.z;
+                A.w += v.w;
+            }
+        }
         // A is relative to 2^MO, L to 2^M (fminf only keeps an overflow of the factor from making 0 * inf)
-        const float o = L > 0.f || L != L ? A / L * fast_exp2(fminf(mou - mu, 126.f)) : 0.f;
-        const __nv_bfloat16 ob = __float2bfloat16_rn(o);
-        a.out[(static_cast<size_t>(r) * a.hq + h) * kHeadDim + tid] = *reinterpret_cast<const uint16_t *>(&ob);
+        const float f = fast_exp2(fminf(mou - mu, 126.f)), inv = L > 0.f || L != L ? 1.f / L : 0.f;
+        reinterpret_cast<uint2 *>(a.out + (static_cast<size_t>(r) * hq + h) * kHeadDim)[lane] =
+            make_uint2(pack_bf16(A.x * inv * f, A.y * inv * f), pack_bf16(A.z * inv * f, A.w * inv * f));
     } else {
         extern __shared__ float z[];   // [Hq]
-        const int c0 = (mi % chunks) * kMassWords;
+        const int c0 = (blockIdx.y - out_ctas) * kMassWords;
         if (c0 >= n) return;
-        for (int h = tid; h < a.hq; h += 128) {
-            const int kvh = h / G, g = h % G;
+        for (unsigned h = JOIN > 1 ? warp : threadIdx.x; h < hq; h += JOIN > 1 ? kWarps : 128) {
+            const unsigned kvh = h / G, g = h - kvh * G;
             const float4 *ml = p.ws_ml + (static_cast<size_t>(kvh) * (p.warps_per_head + B) + w0 + r) * G + g;
-            float M = -INFINITY, L = 0.f;
-            for (int i = 0; i < nw; ++i) M = fmaxf(M, ml[static_cast<size_t>(i) * G].x);
-            const float mu = M == -INFINITY ? 0.f : M;
-            for (int i = 0; i < nw; ++i) {
-                const float4 v = ml[static_cast<size_t>(i) * G];
-                L += v.y * fast_exp2(v.x - mu);
+            float M = -INFINITY, L = 0.f, MO;
+            if (JOIN > 1) {
+                join_head(ml, nw, G, lane, M, L, MO);
+            } else {
+                // a few partials: one thread per head
+                for (int i = 0; i < nw; ++i) M = fmaxf(M, ml[static_cast<size_t>(i) * G].x);
+                for (int i = 0; i < nw; ++i) {
+                    const float4 v = ml[static_cast<size_t>(i) * G];
+                    L += v.y * fast_exp2(v.x - (M == -INFINITY ? 0.f : M));
+                }
             }
-            z[h] = L > 0.f || L != L ? mu + fast_log2(L) : INFINITY;
+            if (JOIN == 1 || lane == 0) z[h] = L > 0.f || L != L ? (M == -INFINITY ? 0.f : M) + fast_log2(L) : INFINITY;
         }
         __syncthreads();
-        for (int i = c0 + warp; i < min(n, c0 + kMassWords); i += 4) {
-            const float *lse = p.ws_lse + (static_cast<size_t>(r) * a.max_words + i) * a.hq;
+#pragma unroll 4
+        for (int i = c0 + warp; i < min(n, c0 + kMassWords); i += kWarps) {
+            const float *lse = p.ws_lse + (static_cast<size_t>(r) * a.max_words + i) * hq;
             float s = 0.f;
-            for (int h = lane; h < a.hq; h += 32) s += fast_exp2(lse[h] - z[h]);
+            for (unsigned h = lane; h < hq; h += 32) s += fast_exp2(lse[h] - z[h]);
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
             if (lane == 0) p.mass[base + beg + i] += s;
@@ -712,9 +740,12 @@ LanePlan lane_plan(int num_req, int hkv, int max_words, int group, bool q8, bool
 }
 
 cudaError_t launch_lane_combine(const LaneParams &p, int min_words, cudaStream_t s) {
-    const int chunks = (p.a.max_words + kMassWords - 1) / kMassWords;
-    lane_combine_kernel<<<p.a.num_req * (p.a.hq + (p.mass ? chunks : 0)), 128, p.mass ? p.a.hq * sizeof(float) : 0, s>>>(p, min_words);
-    return cudaGetLastError();
+    const int chunks = p.mass ? (p.a.max_words + kMassWords - 1) / kMassWords : 0;
+    const size_t smem = p.mass ? p.a.hq * sizeof(float) : 0;
+    // a request has about pieces / requests partials
+    if (p.warps_per_head > 8 * p.a.num_req)
+        return launch_dependent(lane_combine_kernel<8>, dim3(p.a.num_req, p.a.hq + chunks), 256, smem, s, p, min_words);
+    return launch_dependent(lane_combine_kernel<1>, dim3(p.a.num_req, (p.a.hq + 3) / 4 + chunks), 128, smem, s, p, min_words);
 }
 
 cudaError_t launch_decode_lane(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, bool q8, cudaStream_t s) {

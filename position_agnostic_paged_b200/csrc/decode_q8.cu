@@ -9,7 +9,8 @@
 // rotated query or a weight x <= 448, becomes a sum of e4m3 parts with steps of 2^-4 (e4m3 rounds to 2^-4 of
 // a value, so 2^4 times the rest is at most 256):
 //   x = x_0 + 2^-4 x_1 + 2^-8 x_2,   x_0 = e4m3(x), x_1 = e4m3(2^4 (x - x_0)), x_2 = e4m3(2^4 (...)):
-// three parts are off by 2^-5 at most (2^-12 of 128, f16 would keep 2^-11) and reach down to 2^-18.  Each
+// three parts (the query) are off by 2^-5 at most, 2^-12 of 128 (f16 would keep 2^-11); four (the weights)
+// reach down to 2^-21.  Each
 // part is a row group of the B operand with accumulator columns of its own; the sum is taken in fp32
 // when they are read.  With block mass the query has five parts (2^-13).
 //
@@ -31,6 +32,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pdl.cuh"
 #include "q8.cuh"
 #include "tc.cuh"
 
@@ -43,9 +45,12 @@ constexpr int kCodeBlock = kBlockTokens * kHeadDim;              // codes of one
 constexpr int kHalfStage = kTileWords * kCodeBlock, kStageBytes = 2 * kHalfStage;
 constexpr int kRecords = 4;
 // A reference is set kMargin above the largest score seen, and moves when a score passes it by kSlack (log2
-// units): weights times 2^7 stay below 448, the largest is 2^4 or more, and few tiles move a reference.
-constexpr float kSlack = 1.75f, kMargin = 3.f;
+// units): weights times 2^7 stay below 448, the largest is 2^2 or more, and few tiles move a reference
+// (32 heads, margin 3 against 5: up to 15 against 4 of 38 tiles, 3 us each).  Four parts of the weights reach
+// down to 2^-23 of the largest.
+constexpr float kSlack = 1.75f, kMargin = 5.f;
 constexpr float kPartStep = 16.f;     // between parts
+constexpr int kPP = 4;                // parts of the weights
 
 // One tile of the walk; n = 0 ends it.
 struct Tile {
@@ -61,7 +66,7 @@ struct Cfg {
     static constexpr int kHT = NG < 8 ? NG : 8, kGroups = NG / kHT;          // heads per softmax thread, groups of 128 threads
     static constexpr int kSoft = 128 * kGroups, kThreads = kSoft + 64;
     static constexpr int kQRows = QP * NG, kQN = (kQRows + 15) / 16 * 16;    // rows of the Q operand, N of the S product
-    static constexpr int kPRows = 3 * NG, kPN = (kPRows + 15) / 16 * 16;
+    static constexpr int kPRows = kPP * NG, kPN = (kPRows + 15) / 16 * 16;
     static constexpr int kQBytes = (kQN + 7) / 8 * 1024, kPBytes = (kPN + 7) / 8 * 1024;
     static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 4096 + 1024;   // buffers, small state, alignment
     static constexpr int kOcc = 2 * (kFixed + 2 * kStageBytes + 1024) <= 227 * 1024 ? 2 : 1;
@@ -155,6 +160,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                                                                                   const __grid_constant__ CUtensorMap tmV,
                                                                                   const __grid_constant__ LaneParams p) {
     using C = Cfg<NG, QP>;
+    pdl_trigger();   // (one wave of CTAs: the join's do not take places from this kernel's)
     constexpr int S = C::kStages, HT = C::kHT, kWalk = C::kSoft / 32, kIssue = kWalk + 1;   // warps
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -586,7 +592,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                     if (!ok) break;
                     tc::fence_after_sync();
 #pragma unroll 1
-                    for (int part = 0; part < 3; ++part)
+                    for (int part = 0; part < kPP; ++part)
 #pragma unroll
                         for (int h = 0; h < HT; h += 4) {
                             const uint32_t col = tO + lane_off + part * NG + g0 + h;
@@ -624,7 +630,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
 #pragma unroll
                 for (int y = 0; y < 4; ++y) w[y] = vis ? x[h + y] * (vs * dv4[y] * 0x1p20f) : 0.f;
 #pragma unroll
-                for (int part = 0; part < 3; ++part) {
+                for (int part = 0; part < kPP; ++part) {
                     const uint32_t codes = take_part(w);
 #pragma unroll
                     for (int y = 0; y < 4; ++y) pd[swz8(part * NG + g0 + h + y, t)] = static_cast<uint8_t>(codes >> (8 * y));
@@ -691,15 +697,16 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 }
 #pragma unroll
                 for (int h = 0; h < HT; h += 4) {
-                    uint32_t o[3][4];
+                    uint32_t o[kPP][4];
 #pragma unroll
-                    for (int part = 0; part < 3; ++part) tmem_load<4>(tO + lane_off + part * NG + g0 + h, o[part]);
+                    for (int part = 0; part < kPP; ++part) tmem_load<4>(tO + lane_off + part * NG + g0 + h, o[part]);
                     tc::wait_ld();
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
                         if (g0 + h + y < G) {
-                            float v = fmaf(__uint_as_float(o[2][y]), 1.f / kPartStep, __uint_as_float(o[1][y]));
-                            v = fmaf(v, 1.f / kPartStep, __uint_as_float(o[0][y]));
+                            float v = __uint_as_float(o[kPP - 1][y]);
+#pragma unroll
+                            for (int part = kPP - 2; part >= 0; --part) v = fmaf(v, 1.f / kPartStep, __uint_as_float(o[part][y]));
                             a.ws_acc[(slot_g + g0 + h + y) * kHeadDim + t] = v * 0x1p-7f;
                         }
                 }

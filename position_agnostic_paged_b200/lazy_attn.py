@@ -189,8 +189,14 @@ def _ptr(t) -> int | None:
     return int(t.data_ptr())
 
 
+# the current stream's handle without making a Stream object (0.2 us against 3 us), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return int(_raw_stream(torch.cuda.current_device())) or None
         return int(torch.cuda.current_stream().cuda_stream) or None
     return int(getattr(stream, "cuda_stream", stream)) or None
 

@@ -102,6 +102,8 @@ def test_decode_refusals():
         assert _mass(**{f: None}) == la.LAZY_EINVAL
     assert _mass(k=P + 8) == la.LAZY_EINVAL
     assert _mass(nb=(1 << 17) + 1) == la.LAZY_ERANGE
+    for call in (_decode, _mass):
+        assert call(q=P + 4) == la.LAZY_EINVAL and call(out=P + 4) == la.LAZY_EINVAL
     assert _decode(mw=-1) == la.LAZY_EINVAL
     assert _decode(ws=None) == la.LAZY_EWORKSPACE
     assert _decode(ws=P + 8) == la.LAZY_EINVAL
@@ -111,6 +113,7 @@ def test_decode_refusals():
     assert _decode(mass=P, wsb=la.decode_q8_workspace_bytes(OK, 2, 4)) == la.LAZY_EWORKSPACE
     assert _mass(wsb=la.decode_mass_workspace_bytes(OK, 2, 4) - 1) == la.LAZY_EWORKSPACE
     assert _decode(n=1 << 28) == la.LAZY_ERANGE
+    assert _mass(mw=(1 << 20) + 1) == la.LAZY_ERANGE and _decode(mass=P, mw=(1 << 20) + 1) == la.LAZY_ERANGE
 
 
 def test_prefill_refusals():
