@@ -83,8 +83,8 @@ struct Cfg {
 constexpr int kOffTile = 0;                                      // records
 constexpr int kOffBars = kOffTile + kRecords * static_cast<int>(sizeof(Tile));
 constexpr int kOffHead = kOffBars + 256;                         // mu, dm, dv, step of O, hm of two Q buffers, slope: [32] each
-constexpr int kOffRed = kOffHead + 7 * 128;                      // [4][32] reductions
-constexpr int kOffAngle = kOffRed + 512;                         // [64] float2
+constexpr int kOffRed = kOffHead + 7 * 128;                      // [2][4][32] reductions
+constexpr int kOffAngle = kOffRed + 1024;                        // [64] float2
 constexpr int kOffMisc = kOffAngle + 512;
 static_assert(kOffMisc + 16 <= 4096, "state");
 
@@ -134,6 +134,12 @@ __device__ __forceinline__ bool any_softmax(bool x) {
                  : "memory");
     return y != 0;
 }
+// maximum over the warp (NaN ignored)
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
 // Four values as the codes of their next part, each value replaced by 2^4 times what is left of it.
 __device__ __forceinline__ uint32_t take_part(float (&x)[4]) {
     const uint32_t w = f32_to_codes(x[0], x[1], x[2], x[3]);
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
              *pready = bars + 20, *odone = bars + 22, *drain = bars + 24;
     float *h_mu = reinterpret_cast<float *>(state + kOffHead), *h_dm = h_mu + 32, *h_dv = h_mu + 64, *h_step = h_mu + 96,
           *h_hm = h_mu + 128, *h_slope = h_mu + 192;
-    float(*red)[32] = reinterpret_cast<float(*)[32]>(state + kOffRed);
+    float(*red)[32] = reinterpret_cast<float(*)[32]>(state + kOffRed), (*red_o)[32] = red + 4;
     float2 *angle = reinterpret_cast<float2 *>(state + kOffAngle);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(state + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(state + kOffMisc + 4);
@@ -537,11 +543,16 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 }
             }
             bool past = !got;
+            float dm[HT];
 #pragma unroll
             for (int h = 0; h < HT; h += 4) {
-                const float4 dm = *reinterpret_cast<const float4 *>(&h_dm[g0 + h]);
-                past |= x[h] + fmaxf(lv + dm.x, 0.f) > kSlack || x[h + 1] + fmaxf(lv + dm.y, 0.f) > kSlack ||
-                        x[h + 2] + fmaxf(lv + dm.z, 0.f) > kSlack || x[h + 3] + fmaxf(lv + dm.w, 0.f) > kSlack;
+                const float4 d = *reinterpret_cast<const float4 *>(&h_dm[g0 + h]);
+                dm[h] = d.x;
+                dm[h + 1] = d.y;
+                dm[h + 2] = d.z;
+                dm[h + 3] = d.w;
+#pragma unroll
+                for (int y = h; y < h + 4; ++y) past |= x[y] + fmaxf(lv + dm[y], 0.f) > kSlack;
             }
             if (any_softmax<C::kSoft>(past)) {
                 ok = !any_softmax<C::kSoft>(!got);
@@ -549,38 +560,34 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 // ---- references (mu for the row sums, mo for score + log2 of the V scale) move to the new maxima
                 float top[HT];
 #pragma unroll
-                for (int pass = 0; pass < 2; ++pass) {
-                    // pass 0: of the scores; pass 1: of score + log2 of the V scale
-#pragma unroll
-                    for (int h = 0; h < HT; ++h) {
-                        float m = pass ? x[h] + lv : x[h];
-#pragma unroll
-                        for (int y = 16; y > 0; y >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
-                        if (lane == 0) red[wq][g0 + h] = m;
+                for (int h = 0; h < HT; ++h) {
+                    const float m = warp_max(x[h]), m_o = warp_max(x[h] + lv);
+                    if (lane == 0) {
+                        red[wq][g0 + h] = m;
+                        red_o[wq][g0 + h] = m_o;
                     }
-                    sync_softmax<C::kSoft>();
+                }
+                sync_softmax<C::kSoft>();
 #pragma unroll
-                    for (int h = 0; h < HT; ++h) {
-                        const int gh = g0 + h;
-                        const float m = fmaxf(fmaxf(red[0][gh], red[1][gh]), fmaxf(red[2][gh], red[3][gh]));
-                        if (pass == 0) {
-                            // how far mu moves
-                            top[h] = m != -INFINITY && (h_dm[gh] == INFINITY || m > kSlack) ? m + kMargin : 0.f;
-                        } else if (t == h) {
-                            const bool none = m == -INFINITY, fresh = h_dm[gh] == INFINITY;
-                            const float mo_old = h_mu[gh] - h_dm[gh], mo_new = h_mu[gh] + m;
-                            const float mo = fresh || mo_new > mo_old + kSlack ? mo_new + kMargin : mo_old;
-                            h_step[gh] = none || fresh ? 1.f : fast_exp2(mo_old - mo);
-                            if (!none) {
-                                h_mu[gh] += top[h];
-                                h_dm[gh] = h_mu[gh] - mo;
-                                // weights times 2^7; 2^-20 of it later, as s_v spans the range of a float
-                                h_dv[gh] = fast_exp2(fminf(h_dm[gh] - 13.f, 126.f));
-                            }
+                for (int h = 0; h < HT; ++h) {
+                    const int gh = g0 + h;
+                    const float m = fmaxf(fmaxf(red[0][gh], red[1][gh]), fmaxf(red[2][gh], red[3][gh]));
+                    const bool none = m == -INFINITY, fresh = dm[h] == INFINITY;
+                    top[h] = !none && (fresh || m > kSlack) ? m + kMargin : 0.f;   // how far mu moves
+                    if (t == h) {
+                        const float m_o = fmaxf(fmaxf(red_o[0][gh], red_o[1][gh]), fmaxf(red_o[2][gh], red_o[3][gh]));
+                        const float mu = h_mu[gh], mo_old = mu - dm[h], mo_new = mu + m_o;
+                        const float mo = fresh || mo_new > mo_old + kSlack ? mo_new + kMargin : mo_old;
+                        h_step[gh] = none || fresh ? 1.f : fast_exp2(mo_old - mo);
+                        if (!none) {
+                            h_mu[gh] = mu + top[h];
+                            h_dm[gh] = mu + top[h] - mo;
+                            // weights times 2^7; 2^-20 of it later, as s_v spans the range of a float
+                            h_dv[gh] = fast_exp2(fminf(mu + top[h] - mo - 13.f, 126.f));
                         }
                     }
-                    sync_softmax<C::kSoft>();
                 }
+                sync_softmax<C::kSoft>();
 #pragma unroll
                 for (int h = 0; h < HT; ++h) {
                     x[h] -= top[h];
@@ -591,17 +598,17 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                     ok = !any_softmax<C::kSoft>(!warp_wait(&odone[buf ^ 1], ((i - 1) >> 1) & 1, abort_flag, a.d_status));
                     if (!ok) break;
                     tc::fence_after_sync();
-#pragma unroll 1
+                    uint32_t o[kPP][HT];
+#pragma unroll
+                    for (int part = 0; part < kPP; ++part) tmem_load<HT>(tO + lane_off + part * NG + g0, o[part]);
+                    tc::wait_ld();
+#pragma unroll
                     for (int part = 0; part < kPP; ++part)
 #pragma unroll
                         for (int h = 0; h < HT; h += 4) {
-                            const uint32_t col = tO + lane_off + part * NG + g0 + h;
-                            uint32_t o[4];
-                            tmem_load<4>(col, o);
-                            tc::wait_ld();
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * h_step[g0 + h + y]);
-                            tmem_store4(col, o);
+                            for (int y = h; y < h + 4; ++y) o[part][y] = __float_as_uint(__uint_as_float(o[part][y]) * h_step[g0 + y]);
+                            tmem_store4(tO + lane_off + part * NG + g0 + h, &o[part][h]);
                         }
                     tc::wait_st();
                     tc::fence_before_sync();
