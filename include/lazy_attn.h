@@ -282,8 +282,8 @@ typedef struct lazy_q8_pool {
     int num_blocks;
 } lazy_q8_pool;
 
-/* Workspace for lazy_kv_write_q8: 0 up to 1024 tokens, else one row of 16 token indices and a
- * metadata word per block of the pool.  The workspaces of this section are 16-byte aligned
+/* Workspace for lazy_kv_write_q8: 0 up to 1024 tokens, else 68 bytes per block of the pool (a row
+ * of token indices and a metadata word) and 16 KiB.  The workspaces of this section are 16-byte aligned
  * (LAZY_EINVAL), and calls that may overlap on the GPU need one each. */
 size_t lazy_kv_write_q8_workspace_bytes(const lazy_attn_cfg *cfg, int n_tok, int num_blocks);
 
@@ -298,7 +298,7 @@ size_t lazy_kv_write_q8_workspace_bytes(const lazy_attn_cfg *cfg, int n_tok, int
  * NaN as NaN; neither counts for the scale.  Tokens may come in any order; of two tokens with
  * the same slot the later one in the call is stored.  Bad slots and misaligned indices are
  * reported and skipped as by lazy_kv_write, and blk_meta is maintained the same way.  The result
- * depends on the inputs alone (no order of execution enters it).  k_raw, v_raw: 8-byte
+ * depends on the inputs alone (no order of execution enters it).  k_raw, v_raw: 16-byte
  * aligned (LAZY_EINVAL).  A call must not overlap on the GPU with another that reads or writes
  * the same blocks. */
 int lazy_kv_write_q8(const lazy_attn_cfg *cfg, const uint16_t *k_raw, const uint16_t *v_raw, int n_tok,

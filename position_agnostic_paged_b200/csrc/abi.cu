@@ -472,7 +472,7 @@ int lazy_kv_write_q8(const lazy_attn_cfg *cfg, const uint16_t *k_raw, const uint
     rc = check_q8_pool(pool);
     if (rc) return rc;
     if (n_tok == 0) return LAZY_OK;
-    if (!k_raw || !v_raw || !slot || !local_j || !aligned(k_raw, 8) || !aligned(v_raw, 8)) return LAZY_EINVAL;
+    if (!k_raw || !v_raw || !slot || !local_j || !aligned(k_raw, 16) || !aligned(v_raw, 16)) return LAZY_EINVAL;
     const size_t need = lazy_kv_write_q8_workspace_bytes(cfg, n_tok, pool->num_blocks);
     if (need > 0 && (!workspace || ws_bytes < need)) return LAZY_EWORKSPACE;
     if (need > 0 && !aligned(workspace, 16)) return LAZY_EINVAL;

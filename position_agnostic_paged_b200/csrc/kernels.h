@@ -127,13 +127,15 @@ struct Q8WriteParams {
     uint8_t *k_codes, *v_codes;
     float *k_scale, *v_scale;
     uint32_t *blk_meta;
-    uint32_t *rows;              // large calls: [num_blocks][16] token index + 1 per slot, [num_blocks] metadata; or null
+    uint32_t *rows;              // large calls: the workspace (token index + 1 per slot, metadata, angles); or null
     int n_tok, hkv, num_blocks;
     int *d_status;
     RopeTableHost rope;
 };
 constexpr int kQ8ScanTokens = 1024;   // up to this many tokens a write finds each block's tokens by scanning the call
-inline size_t q8_write_ws_bytes(int num_blocks) { return static_cast<size_t>(num_blocks) * (16 + 1) * 4; }
+inline size_t q8_write_ws_bytes(int num_blocks) {
+    return (static_cast<size_t>(num_blocks) * 16 + (static_cast<size_t>(num_blocks) + 3) / 4 * 4 + 16 * 64 * 4) * 4;
+}
 cudaError_t launch_kv_write_q8(const Q8WriteParams &p, cudaStream_t s);
 
 // Streaming decode (decode_lane.cu) over the 8-bit pool, or over the bf16 pool with block mass.

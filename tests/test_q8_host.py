@@ -87,7 +87,7 @@ def test_write_refusals():
     assert _write(cfg=None) == la.LAZY_EINVAL
     for f in ("k", "v", "slot", "j"):
         assert _write(**{f: None}) == la.LAZY_EINVAL
-    assert _write(k=P + 2) == la.LAZY_EINVAL
+    assert _write(k=P + 8) == la.LAZY_EINVAL and _write(v=P + 2) == la.LAZY_EINVAL
     assert _write(n=5000, ws=None) == la.LAZY_EWORKSPACE
     assert _write(n=5000, wsb=la.kv_write_q8_workspace_bytes(OK, 5000, 8) - 1) == la.LAZY_EWORKSPACE
     assert _write(n=5000, ws=P + 4) == la.LAZY_EINVAL
