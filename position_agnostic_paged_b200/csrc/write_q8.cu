@@ -90,23 +90,48 @@ __device__ __forceinline__ void unpack_row(uint2 lo, uint2 hi, float (&x)[8]) {
     x[0] = bf16_lo(lo.x), x[1] = bf16_hi(lo.x), x[2] = bf16_lo(lo.y), x[3] = bf16_hi(lo.y);
     x[4] = bf16_lo(hi.x), x[5] = bf16_hi(hi.x), x[6] = bf16_lo(hi.y), x[7] = bf16_hi(hi.y);
 }
-// x (four pairs: u and u + 4) turned by the angles with cosines c and sines s
-__device__ __forceinline__ void turn(float (&x)[8], const float (&c)[4], const float (&s)[4]) {
+// x (four pairs: u and u + 4) turned by the angles with cosines c and sines s.  (Scalar: negations and absolute values
+// are free there, and paired fp32 instructions would spend more on moves.)
+__device__ __forceinline__ void turn(float (&x)[8], const float4 c, const float4 s) {
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-    for (int u = 0; u < 4; u += 2) {
-        float ac0, ac1, bc0, bc1;
-        const float a0 = x[u], a1 = x[u + 1], b0 = x[u + 4], b1 = x[u + 5];
-        mul2(ac0, ac1, a0, a1, c[u], c[u + 1]);
-        mul2(bc0, bc1, b0, b1, c[u], c[u + 1]);
-        fma2v(x[u], x[u + 1], -b0, -b1, s[u], s[u + 1], ac0, ac1);
-        fma2v(x[u + 4], x[u + 5], a0, a1, s[u], s[u + 1], bc0, bc1);
+    for (int u = 0; u < 4; ++u) {
+        const float a = x[u], b = x[u + 4];
+        x[u] = fmaf(-b, ss[u], a * cc[u]);
+        x[u + 4] = fmaf(a, ss[u], b * cc[u]);
     }
 }
 // largest |x| so far; NaN does not enter
 __device__ __forceinline__ float max_abs(float am, const float (&x)[8]) {
 #pragma unroll
-    for (int u = 0; u < 8; u += 2) am = max3(am, fabsf(x[u]), fabsf(x[u + 1]));
+    for (int u = 0; u < 8; ++u) am = fmaxf(am, fabsf(x[u]));
     return am;
+}
+
+// The codes of the elements x (0 .. 3 of row t at dims 4 c, 4 .. 7 64 above) for the scale 1 / inv.
+template <bool KEY>
+__device__ __forceinline__ uint2 code_row(const Q8WriteParams &p, const float (&x)[8], float inv, float err, float scale, int t, int j,
+                                          int h, int c) {
+    float y[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) y[u] = x[u] * inv;
+    uint2 code;
+    if (KEY || err != 0.f) {
+        // codes of both ends of the error interval: they differ where it holds a rounding border
+        float e[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) e[u] = (fabsf(y[u]) + fabsf(y[u + 4])) * err;
+        code.x = f32_to_codes(y[0] + e[0], y[1] + e[1], y[2] + e[2], y[3] + e[3]);
+        code.y = f32_to_codes(y[4] + e[0], y[5] + e[1], y[6] + e[2], y[7] + e[3]);
+        if (code.x != f32_to_codes(y[0] - e[0], y[1] - e[1], y[2] - e[2], y[3] - e[3]))
+            code.x = codes_f64<KEY>(p, t, j, h, c, 0, scale);
+        if (code.y != f32_to_codes(y[4] - e[0], y[5] - e[1], y[6] - e[2], y[7] - e[3]))
+            code.y = codes_f64<KEY>(p, t, j, h, c, 1, scale);
+    } else {
+        code.x = f32_to_codes(y[0], y[1], y[2], y[3]);
+        code.y = f32_to_codes(y[4], y[5], y[6], y[7]);
+    }
+    return code;
 }
 
 // One head's scale from max |x| in fp32 over the lanes, and its rows' codes; row(r, x) gives row r (x in fp32) to its
@@ -130,49 +155,38 @@ __device__ __forceinline__ void code_head(const Q8WriteParams &p, int blk, int h
     const bool grew = nv > 0 && scale != before;
     const float err = (KEY ? key_err : 0.f) + (pow2 ? 0.f : 0x1p-22f);   // of x * inv, relative to |x0| + |x1|
     uint8_t *codes = (KEY ? p.k_codes : p.v_codes) + (static_cast<size_t>(blk) * p.hkv + h) * kBlockTokens * kHeadDim;
-    const float ratio = before / scale;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(codes + hl * kHeadDim) + c;
+    if (have == 0xFFFFu) {
 #pragma unroll 2
-    for (int i = 0; i < 8; ++i) {
-        const int r = 2 * i + hl;
-        if (!((have >> (2 * i)) & 3u) && !(grew && 2 * i < nv)) continue;   // neither row of the pair
-        uint32_t *dst = reinterpret_cast<uint32_t *>(codes + r * kHeadDim) + c;
-        if ((have >> r) & 1u) {
-            float y[8];
-            row(r, y);
-#pragma unroll
-            for (int u = 0; u < 8; u += 2) mul2(y[u], y[u + 1], y[u], y[u + 1], inv, inv);
-            if (KEY || !pow2) {
-                // codes of both ends of the error interval: they differ where it holds a rounding border
-                float e[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) e[u] = (fabsf(y[u]) + fabsf(y[u + 4])) * err;
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    float d[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) d[u] = y[4 * s + u];
-#pragma unroll
-                    for (int u = 0; u < 4; u += 2) {
-                        add2(y[4 * s + u], y[4 * s + u + 1], e[u], e[u + 1]);
-                        add2(d[u], d[u + 1], -e[u], -e[u + 1]);
-                    }
-                    uint32_t code = f32_to_codes(y[4 * s], y[4 * s + 1], y[4 * s + 2], y[4 * s + 3]);
-                    if (code != f32_to_codes(d[0], d[1], d[2], d[3])) code = codes_f64<KEY>(p, tok[r], pos[r], h, c, s, scale);
-                    dst[16 * s] = code;
-                }
-            } else {
-                dst[0] = f32_to_codes(y[0], y[1], y[2], y[3]);
-                dst[16] = f32_to_codes(y[4], y[5], y[6], y[7]);
-            }
-        } else if (r < nv && grew) {
+        for (int i = 0; i < 8; ++i, dst += 2 * kHeadDim / 4) {
+            float x[8];
+            row(2 * i + hl, x);
+            const uint2 code = code_row<KEY>(p, x, inv, err, scale, tok[2 * i + hl], pos[2 * i + hl], h, c);
+            dst[0] = code.x;
+            dst[16] = code.y;
+        }
+    } else {
+        const float ratio = before / scale;
 #pragma unroll 1
-            for (int s = 0; s < 2; ++s) {
-                uint32_t h0, h1;
-                float y[4];
-                codes_to_f16(dst[16 * s], h0, h1);
-                f16x2_to_f32(h0, y[0], y[1]);
-                f16x2_to_f32(h1, y[2], y[3]);
-                dst[16 * s] = f32_to_codes(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio);
+        for (int i = 0; i < 8; ++i, dst += 2 * kHeadDim / 4) {
+            const int r = 2 * i + hl;
+            if (!((have >> (2 * i)) & 3u) && !(grew && 2 * i < nv)) continue;   // neither row of the pair
+            if ((have >> r) & 1u) {
+                float x[8];
+                row(r, x);
+                const uint2 code = code_row<KEY>(p, x, inv, err, scale, tok[r], pos[r], h, c);
+                dst[0] = code.x;
+                dst[16] = code.y;
+            } else if (r < nv && grew) {
+#pragma unroll 1
+                for (int s = 0; s < 2; ++s) {
+                    uint32_t h0, h1;
+                    float y[4];
+                    codes_to_f16(dst[16 * s], h0, h1);
+                    f16x2_to_f32(h0, y[0], y[1]);
+                    f16x2_to_f32(h1, y[2], y[3]);
+                    dst[16 * s] = f32_to_codes(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio);
+                }
             }
         }
     }
@@ -314,22 +328,27 @@ __global__ void __launch_bounds__(kBulkWarps * 32, 5) kv_write_q8_bulk_kernel(co
             auto key_row = [&](int r, float(&x)[8]) {
                 const uint2 *q = reinterpret_cast<const uint2 *>(raw[0] + r * 256);
                 unpack_row(q[c], q[16 + c], x);
-                const float4 z = *reinterpret_cast<const float4 *>(&cs[r][0][4 * c]);
-                const float4 y = *reinterpret_cast<const float4 *>(&cs[r][1][4 * c]);
-                const float zc[4] = {z.x, z.y, z.z, z.w}, zs[4] = {y.x, y.y, y.z, y.w};
-                turn(x, zc, zs);
+                turn(x, *reinterpret_cast<const float4 *>(&cs[r][0][4 * c]), *reinterpret_cast<const float4 *>(&cs[r][1][4 * c]));
             };
             auto val_row = [&](int r, float(&x)[8]) {
                 const uint2 *q = reinterpret_cast<const uint2 *>(raw[1] + r * 256);
                 unpack_row(q[c], q[16 + c], x);
             };
             ok = landed(0);
-            float am = 0.f, vm = 0.f;
+            float am = 0.f;
+            if (have == 0xFFFFu) {
 #pragma unroll 2
-            for (int i = 0; i < 8; ++i) {
-                float x[8];
-                if ((have >> (2 * i + hl)) & 1u) {
-                    key_row(2 * i + hl, x);
+                for (int r = hl; r < kBlockTokens; r += 2) {
+                    float x[8];
+                    key_row(r, x);
+                    am = max_abs(am, x);
+                }
+            } else {
+#pragma unroll 1
+                for (int r = hl; r < kBlockTokens; r += 2) {
+                    float x[8];
+                    if (!((have >> r) & 1u)) continue;
+                    key_row(r, x);
                     am = max_abs(am, x);
                 }
             }
@@ -337,14 +356,18 @@ __global__ void __launch_bounds__(kBulkWarps * 32, 5) kv_write_q8_bulk_kernel(co
             code_head<true>(p, blk, h, nv, tok, pos, have, lane, am, kErrLarge, key_row);
             if (h + kBulkWarps < p.hkv) fetch(0, h + kBulkWarps);
             ok &= landed(1);
+            // max |v| as bf16 pairs (a NaN does not enter)
+            __nv_bfloat162 v2 = __float2bfloat162_rn(0.f);
 #pragma unroll 2
-            for (int i = 0; i < 8; ++i) {
-                float x[8];
-                if ((have >> (2 * i + hl)) & 1u) {
-                    val_row(2 * i + hl, x);
-                    vm = max_abs(vm, x);
-                }
+            for (int r = hl; r < kBlockTokens; r += 2) {
+                const uint4 *q = reinterpret_cast<const uint4 *>(raw[1] + r * 256);
+                const uint4 w = q[c];
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                if ((have >> r) & 1u)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) v2 = __hmax2(v2, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&ws[u])));
             }
+            const float vm = fmaxf(__low2float(v2), __high2float(v2));
             __syncwarp();
             code_head<false>(p, blk, h, nv, tok, pos, have, lane, vm, 0.f, val_row);
             if (h + kBulkWarps < p.hkv) fetch(1, h + kBulkWarps);
@@ -399,10 +422,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_q8_kernel(const __grid_cons
         };
         auto key_row = [&](int r, float(&x)[8]) {
             val_row(p.k_raw, r, x);
-            const float4 z = *reinterpret_cast<const float4 *>(&cs[r][0][4 * c]);
-            const float4 y = *reinterpret_cast<const float4 *>(&cs[r][1][4 * c]);
-            const float zc[4] = {z.x, z.y, z.z, z.w}, zs[4] = {y.x, y.y, y.z, y.w};
-            turn(x, zc, zs);
+            turn(x, *reinterpret_cast<const float4 *>(&cs[r][0][4 * c]), *reinterpret_cast<const float4 *>(&cs[r][1][4 * c]));
         };
         float am = 0.f, vm = 0.f;
 #pragma unroll 2
