@@ -4,8 +4,15 @@
 // others, then by weight, then by index; the first k = min(n, max(keep, 0)) stay, in table order.
 // Weights become 32-bit keys of the same order; the k-th key is found by radix selection (8 bits a
 // pass, stopping as soon as the bin that holds it is taken whole), ties at that key go to the lowest
-// indices, and one ordered compaction writes survivors and evicted words.  A CTA takes one request:
-// keys are read once and stay in shared memory.
+// indices, and one ordered compaction writes survivors and evicted words.
+//
+// A cluster of CTAs takes one request, each a run of its words with the keys in shared memory; the CTAs add up
+// their histograms and counts over distributed shared memory.  Latency is the bound: 8 requests of 32768
+// words move 2.5 MB (0.4 us at the copy rate) in 15 us, most of it the four passes' barriers and the atomics
+// of the histograms; one CTA per request took 48 us for them.  About 16 clusters of such CTAs run at once, so
+// that many requests are better off with a CTA each (64 of 8192 words: 15 us, in clusters 48 us; 32 of 32768: 48 us, in clusters 39 us).
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -13,8 +20,15 @@ namespace lazy {
 
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kSmemKeys = 49152;   // words of a request whose keys stay in shared memory
+constexpr int kSmemKeys = 49152;     // words of a CTA whose keys stay in shared memory
+constexpr int kCluster = 8;          // CTAs of a cluster
+// In clusters where tables of more than kLongWords words (measured for 8 requests: 4096 words 9.4 us in one CTA
+// each, 4100 in clusters 9.4, 8192 in one 15.7, in clusters 11.6) and the calls' waves of clusters are few:
+// each wave costs about what kWaveWords words cost one CTA.
+constexpr int kLongWords = 4096, kWaveWords = 16384, kWave = 16;
 
 __device__ __forceinline__ uint32_t key_of(float m) {
     if (m != m) m = INFINITY;
@@ -23,39 +37,58 @@ __device__ __forceinline__ uint32_t key_of(float m) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// CL: CTAs per request (a cluster).
+template <int CL>
 __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, int smem_keys) {
     extern __shared__ uint32_t keys[];
-    __shared__ int hist[256];
-    __shared__ int red[kWarps], cnt_gt[kWarps], cnt_eq[kWarps];
+    __shared__ int total[CL > 1 ? 256 : 1];
+    __shared__ int hist[2][256];          // of this CTA; two, so that a pass need not wait for readers of the last one
+    __shared__ int red[kWarps], cnt_gt[kWarps], cnt_eq[kWarps], cta_cnt[2];
     __shared__ int sel_bin, sel_above, sel_count;
-    const int r = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int r = blockIdx.x / CL, rank = blockIdx.x % CL;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto sync_request = [&]() {
+        if constexpr (CL > 1)
+            cg::this_cluster().sync();
+        else
+            __syncthreads();
+    };
+    // the same shared variable of CTA q of the request
+    auto of_rank = [&](int *x, int q) -> int * {
+        if constexpr (CL > 1)
+            return cg::this_cluster().map_shared_rank(x, q);
+        else
+            return x;
+    };
     const int base = p.table_indptr[0];
     const int beg = p.table_indptr[r], n_all = p.table_indptr[r + 1] - beg;
     const int n = max(0, min(n_all, p.max_words));
-    if (tid == 0 && n_all > p.max_words) set_status(p.d_status, LAZY_DSTATUS_BAD_TABLE);
+    if (tid == 0 && rank == 0 && n_all > p.max_words) set_status(p.d_status, LAZY_DSTATUS_BAD_TABLE);
     auto kept_of = [&](int q) {
         const int m = p.table_indptr[q + 1] - p.table_indptr[q];
         return max(0, min(min(m, p.max_words), p.keep[q]));
     };
     const int k = kept_of(r);
-    // ---- where this request's survivors go
+    // ---- this CTA's words; where the request's survivors go
+    const int run = ((n + CL - 1) / CL + 31) / 32 * 32;
+    const int lo = min(n, rank * run), hi = min(n, lo + run);
     int before = 0;
     for (int q = tid; q < r; q += kThreads) before += kept_of(q);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) before += __shfl_xor_sync(0xffffffffu, before, x);
     if (lane == 0) red[warp] = before;
-    // ---- keys
     const float *mass = p.mass + beg;
-    for (int i = tid; i < min(n, smem_keys); i += kThreads) keys[i] = key_of(mass[i]);
+    for (int i = lo + tid; i < min(hi, lo + smem_keys); i += kThreads) keys[i - lo] = key_of(mass[i]);
+    if (tid < 256) hist[0][tid] = 0;
     __syncthreads();
     int out = red[lane];
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) out += __shfl_xor_sync(0xffffffffu, out, x);
-    if (tid == 0) {
+    if (tid == 0 && rank == 0) {
         if (r == 0) p.indptr_out[0] = 0;
         p.indptr_out[r + 1] = out + k;
     }
-    auto key = [&](int i) { return i < smem_keys ? keys[i] : key_of(mass[i]); };
+    auto key = [&](int i) { return i - lo < smem_keys ? keys[i - lo] : key_of(mass[i]); };
     // ---- the class that the cut goes through: the protected words if they alone are too many, else the others
     const int nf = min(p.n_first, n), nl = min(p.n_last, n - nf), n_prot = nf + nl;
     auto is_prot = [&](int i) { return i < nf || i >= n - nl; };
@@ -65,20 +98,30 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
     const bool none = need == 0, all = need == n_class;
     uint32_t prefix = 0u, mask = 0u;
     bool whole = false;   // every key of the class with (key & mask) == prefix stays
-    if (!none && !all) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) hist[tid] = 0;
-            __syncthreads();
-            for (int i = tid; i < n; i += kThreads) {
+    if (!none && !all) {   // (the same for all CTAs of the request)
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass, buf = pass & 1;
+            for (int i = lo + tid; i < hi; i += kThreads) {
                 const uint32_t u = key(i);
-                if (is_prot(i) == cut_prot && (u & mask) == prefix) atomicAdd(&hist[(u >> shift) & 255u], 1);
+                if (is_prot(i) == cut_prot && (u & mask) == prefix) atomicAdd(&hist[buf][(u >> shift) & 255u], 1);
             }
-            __syncthreads();
+            sync_request();
+            if (tid < 256) {
+                hist[buf ^ 1][tid] = 0;   // read last before the sync
+                if constexpr (CL > 1) {
+                    int c = 0;
+#pragma unroll
+                    for (int q = 0; q < CL; ++q) c += of_rank(hist[buf], q)[tid];
+                    total[tid] = c;
+                }
+            }
+            if constexpr (CL > 1) __syncthreads();
             if (warp == 0) {
                 // lane l: bins 255 - 8 l downwards
+                const int *h = CL > 1 ? total : hist[buf];
                 int c[8], s = 0;
 #pragma unroll
-                for (int x = 0; x < 8; ++x) s += c[x] = hist[255 - 8 * lane - x];
+                for (int x = 0; x < 8; ++x) s += c[x] = h[255 - 8 * lane - x];
                 int inc = s;
 #pragma unroll
                 for (int x = 1; x < 32; x <<= 1) {
@@ -102,11 +145,9 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
             prefix |= static_cast<uint32_t>(sel_bin) << shift;
             mask |= 255u << shift;
             need -= sel_above;
-            if (need == sel_count) {
-                whole = true;
-                break;
-            }
-            __syncthreads();
+            whole = need == sel_count;
+            if (whole) break;
+            __syncthreads();   // sel_* are read before the next pass writes them
         }
     }
     // 2: stays, 1: stays if among the first `need` of its kind, 0: goes
@@ -117,8 +158,8 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
         return u > prefix ? 2 : u < prefix ? 0 : whole ? 2 : 1;
     };
     // ---- ordered compaction: a warp takes a run of words
-    const int seg = ((n + kThreads - 1) / kThreads) * 32;
-    const int w0 = min(n, warp * seg), w1 = min(n, w0 + seg);
+    const int seg = ((hi - lo + kThreads - 1) / kThreads) * 32;
+    const int w0 = min(hi, lo + warp * seg), w1 = min(hi, w0 + seg);
     int gt = 0, eq = 0;
     for (int i0 = w0; i0 < w1; i0 += 32) {
         const int v = i0 + lane < w1 ? verdict(i0 + lane) : 0;
@@ -135,6 +176,18 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
     for (int x = 16; x > 0; x >>= 1) {
         gt_before += __shfl_xor_sync(0xffffffffu, gt_before, x);
         eq_before += __shfl_xor_sync(0xffffffffu, eq_before, x);
+    }
+    if constexpr (CL > 1) {
+        if (tid == kThreads - 32) {   // the last warp's totals include all warps
+            cta_cnt[0] = gt_before + gt;
+            cta_cnt[1] = eq_before + eq;
+        }
+        sync_request();
+        for (int q = 0; q < rank; ++q) {
+            const int *c = of_rank(cta_cnt, q);
+            gt_before += c[0];
+            eq_before += c[1];
+        }
     }
     int stay = gt_before + min(eq_before, need);   // survivors before this position
     const uint32_t lower = (1u << lane) - 1u;
@@ -160,17 +213,32 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
         eq_before += __popc(em);
     }
     if (p.evicted)
-        for (int i = n + tid; i < n_all; i += kThreads) p.evicted[gone0 + i - k] = p.table[beg + i];
+        for (int i = n + rank * kThreads + tid; i < n_all; i += CL * kThreads) p.evicted[gone0 + i - k] = p.table[beg + i];
+    if constexpr (CL > 1) sync_request();   // shared memory lives until the other CTAs have read it
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t s) {
-    const int smem_keys = p.max_words < kSmemKeys ? p.max_words : kSmemKeys;
-    cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKeys * 4);
+    const long long waves = (p.num_req + kWave - 1) / kWave;
+    const bool cluster = p.max_words > kLongWords + kWaveWords * (waves - 1);
+    const int per_cta = cluster ? (p.max_words + kCluster - 1) / kCluster + 32 : p.max_words;
+    const int smem_keys = per_cta < kSmemKeys ? per_cta : kSmemKeys;
+    auto kern = cluster ? evict_kernel<kCluster> : evict_kernel<1>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKeys * 4);
     if (e != cudaSuccess) return e;
-    evict_kernel<<<p.num_req, kThreads, smem_keys * 4, s>>>(p, smem_keys);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster ? kCluster : 1;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.num_req * (cluster ? kCluster : 1));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_keys * 4;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, smem_keys);
 }
 
 }  // namespace lazy

@@ -446,6 +446,19 @@ def test_evict_long(n):
     _check_evict(words, ind, n, np.zeros(n, np.float32), [77, 1500], 4, 64)
 
 
+@pytest.mark.parametrize("n", [4095, 4097, 5000, 400003])
+def test_evict_cluster(n):
+    """Requests of one CTA and of a cluster, empty ones among them; more keys than a cluster's shared memory holds."""
+    rng = np.random.default_rng(n)
+    lens = [n, 0, 1, 31, 4097, 300]
+    ind = np.concatenate([[0], np.cumsum(lens)])
+    mass = np.round(rng.random(ind[-1]) * 5000).astype(np.float32) / 5000
+    words = rng.integers(0, 1 << 32, ind[-1], dtype=np.uint32)
+    for keep in ([n - 7, 3, 1, 30, 2048, 150], [n // 2, 0, 0, 5, 33, 299]):
+        want = la.DSTATUS_BAD_TABLE if max(lens) > n else 0
+        assert _check_evict(words, ind, n, mass, keep, 4, 64) == want
+
+
 def test_evict_request_longer_than_max_words():
     mass = np.arange(20, dtype=np.float32)
     assert _check_evict(np.arange(20, dtype=np.uint32), [0, 12, 20], 9, mass, [5, 6], 1, 2) == la.DSTATUS_BAD_TABLE
