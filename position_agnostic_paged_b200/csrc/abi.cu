@@ -230,7 +230,7 @@ int64_t prefill_units(const lazy_attn_cfg *cfg, int num_req, int max_q) {
 size_t lane_ws(const lazy_attn_cfg *cfg, int num_req, int max_words, bool q8, bool mass, LanePlan &pl) {
     const int G = cfg->num_q_heads / cfg->num_kv_heads;
     pl = q8 ? decode_q8_plan(num_req, cfg->num_kv_heads, max_words, G, mass, sm_count())
-            : lane_plan(num_req, cfg->num_kv_heads, max_words, G, q8, mass, sm_count());
+            : decode_mass_plan(num_req, cfg->num_kv_heads, max_words, G, sm_count());
     size_t n = static_cast<size_t>(pl.slots) * G * (128 * sizeof(float) + sizeof(float4));
     if (mass) n += static_cast<size_t>(num_req) * max_words * cfg->num_q_heads * sizeof(float);
     return n;
@@ -266,14 +266,14 @@ int lane_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_
     p.mass = mass;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    p.warps_per_head = pl.warps_per_head;
+    p.pieces = pl.pieces;
     CUtensorMap tk, tv;
     const int64_t pool_rows = static_cast<int64_t>(num_blocks) * p.a.hkv * 16;
     if (q8 ? !make_codes_map(&tk, k, pool_rows) || !make_codes_map(&tv, v, pool_rows)
            : !make_rows_map(&tk, k, pool_rows) || !make_rows_map(&tv, v, pool_rows))
         return LAZY_ECUDA;
     return launch_rc(q8 ? launch_decode_q8(tk, tv, p, static_cast<cudaStream_t>(stream))
-                        : launch_decode_lane(tk, tv, p, q8, static_cast<cudaStream_t>(stream)));
+                        : launch_decode_mass(tk, tv, p, static_cast<cudaStream_t>(stream)));
 }
 
 int prefill_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *cu_q, const int32_t *q_pos0,

@@ -1,5 +1,5 @@
-// decode_lane.cu -- decode attention that also accumulates each table word's attention weight,
-// and decode attention over the 8-bit pool.
+// decode_lane.cu -- decode attention over the bf16 pool that also accumulates each table word's
+// attention weight.
 //
 // Per request, query head h on KV head k, key t with table offset o, local index j and position
 // o + j <= p (the query's), as in decode.cu:
@@ -15,27 +15,24 @@
 //
 // Data path.  Each warp is its own producer: lane 0 loads the warp's next words by TMA (128-byte
 // swizzle) into the warp's stages, so there are no barriers between warps.  (With cp.async the
-// loads of table words, and spilled registers, waited in the L1's queue behind all copies in flight:
-// 213 us for the 8B step below.)  The K index order of an MMA is free as long as both operands use
-// the same one, and so is the order of output rows; both are chosen to make a lane's share
-// contiguous, and a quarter warp's 16-byte reads cover all banks:
-//   K (rows = keys as the A operand): lane (rr, c) takes 16-byte pieces 2c, 2c + 1 of each 128-byte
-//     row, key rows rr and rr + 8;
+// loads of table words, and spilled registers, waited in the L1's queue behind all copies in flight.)
+// The K index order of an MMA is free as long as both operands use the same one, and so is the order
+// of output rows; both are chosen to make a lane's share contiguous, and a quarter warp's 16-byte
+// reads cover all banks:
+//   K (rows = keys as the A operand): lane (rr, c) takes 16-byte pieces 2c, 2c + 1 of each half
+//     row of 64 dims, key rows rr and rr + 8;
 //   V^T (rows = head dims as the A operand): lane (rr, c) takes piece rr of key rows 2c, 2c+1,
 //     2c+8, 2c+9 and pairs keys with byte permutes.
-// e4m3 codes become f16 (exact); the query is scaled by a power of two to [1, 2) and rounded to f16
-// (2^-12 of its largest element); weights are f16 against a running reference that includes the
-// block's V scale, so they neither overflow nor lose the small blocks.  Scores, sums, maxima and
-// outputs are fp32.  With block mass the query is split into two f16 (8-bit pool) or three bf16
-// parts (bf16 pool), which keeps the fp32 weights to a few 2^-22.
-#include <cuda_fp16.h>
-
+// The query is scaled by a power of two to [1, 2) and split into three bf16 parts, so that the
+// accumulated fp32 weights are good to a few 2^-22; the weights of the V product are rounded to bf16.
+// Scores, sums, maxima and outputs are fp32.
+//
+// What bounds it: HBM.  64 requests of 4161 tokens with 8 KV heads: MASS8B_FIG.
 #include <climits>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "pdl.cuh"
-#include "q8.cuh"
 
 namespace lazy {
 
@@ -49,25 +46,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-template <bool Q8>
-__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                      uint32_t b1) {
-    if (Q8)
-        mma_f16(d, a0, a1, a2, a3, b0, b1);
-    else
-        mma_bf16(d, a0, a1, a2, a3, b0, b1);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
 __device__ __forceinline__ float fast_log2(float x) {
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -79,19 +57,20 @@ __device__ __forceinline__ int words_per_warp(int total, int warps) {
     return max(kMinWords, (total + warps - 1) / warps);
 }
 
-// NT: groups of 8 query heads per KV head.  QP: parts the query is split into.
-template <bool Q8, int NT, bool MASS>
+constexpr int kQParts = 3;
+constexpr int kTileBytes = 2 * kBoxBytes;        // K (or V) of one word and head
+constexpr int kStageBytes = 2 * kTileBytes;
+
+// NT: groups of 8 query heads per KV head.
+template <int NT>
 struct Cfg {
-    static constexpr int QP = Q8 ? (MASS ? 2 : 1) : 3;
     static constexpr bool kRegQ = NT == 1;                     // query fragments in registers, else in shared memory
-    static constexpr int kTile = Q8 ? 2048 : 4096;             // bytes of K (and of V) per word
-    static constexpr int kStageBytes = 2 * kTile;
-    static constexpr int kQBytes = kRegQ ? 0 : NT * QP * 8 * 32 * 8;      // query fragments per warp
+    static constexpr int kQBytes = kRegQ ? 0 : NT * kQParts * 8 * 32 * 8;      // query fragments per warp
     static constexpr int kExtra = kQBytes + 512 + 64;                     // query fragments, angles, barriers
     static constexpr int kLeast = 2 * kStageBytes + kExtra;               // shared memory per warp, two stages
     // CTAs per SM by registers (4 warps each); where the query fragments leave no room for two stages of so
-    // many warps (bf16 with block mass, G > 8): one CTA of as many warps as fit
-    static constexpr int kOcc0 = NT == 4 ? 2 : (NT == 2 || !Q8) ? 3 : 4;
+    // many warps (G > 8): one CTA of as many warps as fit
+    static constexpr int kOcc0 = NT == 4 ? 2 : 3;
     static constexpr bool kFits = kOcc0 * (4 * kLeast + 2048) <= 227 * 1024;
     static constexpr int kOcc = kFits ? kOcc0 : 1;
     static constexpr int kWarps = kFits ? 4 : 225 * 1024 / kLeast;
@@ -101,26 +80,19 @@ struct Cfg {
     static_assert(kStages >= 2 && kWarps <= 8, "pipeline depth");
 };
 
-// First of the four head dims of the query fragment's registers for k-step s: codes hold 16 dims per piece,
-// so lane c has dims 32c .. + 31 and its rotation pairs lie in lane c ^ 2; bf16 rows are two halves of 64
-// dims, 16c .. + 15 of each, and pairs lie in k-steps s and s + 4.
-template <bool Q8>
-__device__ __forceinline__ int qdim(int s, int c) {
-    return Q8 ? 32 * c + 4 * s : 16 * c + 4 * (s & 3) + 64 * (s >> 2);
-}
+// First of the four head dims of the query fragment's registers for k-step s: rows are two halves of 64 dims,
+// lane c has dims 16c .. + 15 of each, and rotation pairs lie in k-steps s and s + 4.
+__device__ __forceinline__ int qdim(int s, int c) { return 16 * c + 4 * (s & 3) + 64 * (s >> 2); }
 // First head dim of output tile t's row pair (rows rr and rr + 8 hold odim and odim + 1).
-template <bool Q8>
-__device__ __forceinline__ int odim(int t, int rr) {
-    return Q8 ? 16 * rr + 2 * t : 64 * (t >> 2) + 8 * rr + 2 * (t & 3);
-}
+__device__ __forceinline__ int odim(int t, int rr) { return 64 * (t >> 2) + 8 * rr + 2 * (t & 3); }
 
-template <bool Q8, int NT, bool MASS>
-__global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT, MASS>::kOcc))
+template <int NT>
+__global__ void __launch_bounds__((Cfg<NT>::kWarps * 32), (Cfg<NT>::kOcc))
     decode_lane_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ LaneParams p) {
-    using C = Cfg<Q8, NT, MASS>;
+    using C = Cfg<NT>;
     pdl_trigger();
-    constexpr int QP = C::QP, S = C::kStages, kWarps = C::kWarps;
+    constexpr int QP = kQParts, S = C::kStages, kWarps = C::kWarps;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -133,16 +105,16 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
     __shared__ double theta[kHalfDim];
     for (int i = threadIdx.x; i < kHalfDim; i += kWarps * 32) theta[i] = a.rope.theta[i];
     __syncthreads();
-    if (wi >= p.warps_per_head) return;
+    if (wi >= p.pieces) return;
     const int base = a.table_indptr[0];
     const int total = a.table_indptr[B] - base;
     if (total <= 0) return;
-    const int per = words_per_warp(total, p.warps_per_head);
+    const int per = words_per_warp(total, p.pieces);
     if (wi > (total - 1) / per) return;
     const int lo = wi * per, cnt = min(total - lo, per);
 
-    uint8_t *stages = sm + warp * S * C::kStageBytes;
-    uint8_t *extra = sm + kWarps * S * C::kStageBytes + warp * C::kExtra;
+    uint8_t *stages = sm + warp * S * kStageBytes;
+    uint8_t *extra = sm + kWarps * S * kStageBytes + warp * C::kExtra;
     uint2 *qs = reinterpret_cast<uint2 *>(extra);                              // [NT][QP][8][32]
     float2 *cs = reinterpret_cast<float2 *>(extra + C::kQBytes);               // [64]
     uint64_t *bars = reinterpret_cast<uint64_t *>(extra + C::kQBytes + 512);   // [S]
@@ -151,32 +123,22 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
     fence_proxy_async_smem();
     __syncwarp();
 
-    // ---- the words of this warp, 32 at a time, one per lane; metadata and scales are loaded a batch
+    // ---- the words of this warp, 32 at a time, one per lane; metadata is loaded a batch
     // ahead of their use and words two, so that no load is waited for
     uint32_t w_cur, m_cur, w_nxt, m_nxt, w_2nd;
-    float ks_cur, vs_cur, ks_nxt, vs_nxt;
     auto word_at = [&](int k) { return k < cnt ? a.table[base + lo + k] : 0u; };
-    auto meta_at = [&](int k, uint32_t w, uint32_t &m, float &ks, float &vs) {
-        m = 0u;
-        ks = vs = 1.f;
-        if (k < cnt) {
-            const uint32_t b = word_block(w);
-            if (b < static_cast<uint32_t>(a.num_blocks)) {
-                m = a.blk_meta[b];
-                if (Q8) {
-                    ks = p.k_scale[static_cast<size_t>(b) * hkv + kvh];
-                    vs = p.v_scale[static_cast<size_t>(b) * hkv + kvh];
-                }
-            } else {
-                set_status(a.d_status, LAZY_DSTATUS_BAD_BLOCK);
-            }
-        }
+    auto meta_at = [&](int k, uint32_t w) {
+        if (k >= cnt) return 0u;
+        const uint32_t b = word_block(w);
+        if (b < static_cast<uint32_t>(a.num_blocks)) return a.blk_meta[b];
+        set_status(a.d_status, LAZY_DSTATUS_BAD_BLOCK);
+        return 0u;
     };
     w_cur = word_at(lane);
     w_nxt = word_at(32 + lane);
     w_2nd = word_at(64 + lane);
-    meta_at(lane, w_cur, m_cur, ks_cur, vs_cur);
-    meta_at(32 + lane, w_nxt, m_nxt, ks_nxt, vs_nxt);
+    m_cur = meta_at(lane, w_cur);
+    m_nxt = meta_at(32 + lane, w_nxt);
 
     // copies of word k (of this warp) into stage sg, by the lane that holds the word.  A word without tokens, or
     // without a block, completes its phase with no data.
@@ -185,13 +147,13 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             const uint32_t w = next_batch ? w_nxt : w_cur, m = next_batch ? m_nxt : m_cur;
             uint64_t *bar = &bars[sg];
             if (meta_valid(m) > 0) {
-                uint8_t *d = stages + sg * C::kStageBytes;
+                uint8_t *d = stages + sg * kStageBytes;
                 const int row = (static_cast<int>(word_block(w)) * hkv + kvh) * kBlockTokens;
-                mbar_arrive_expect_tx(bar, C::kStageBytes);
+                mbar_arrive_expect_tx(bar, kStageBytes);
                 tma_load_2d(d, &tmK, 0, row, bar);
-                if (!Q8) tma_load_2d(d + kBoxBytes, &tmK, kHalfDim, row, bar);
-                tma_load_2d(d + C::kTile, &tmV, 0, row, bar);
-                if (!Q8) tma_load_2d(d + C::kTile + kBoxBytes, &tmV, kHalfDim, row, bar);
+                tma_load_2d(d + kBoxBytes, &tmK, kHalfDim, row, bar);
+                tma_load_2d(d + kTileBytes, &tmV, 0, row, bar);
+                tma_load_2d(d + kTileBytes + kBoxBytes, &tmV, kHalfDim, row, bar);
             } else {
                 mbar_arrive(bar);
             }
@@ -218,9 +180,8 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
     uint32_t qb[C::kRegQ ? QP : 1][C::kRegQ ? 8 : 1][2];
     float qn[NT];            // 2^-e of this lane's fragment head (8 n + rr)
     float hm[NT][2];         // score factor of heads 8 n + 2c, + 1: softmax scale * log2(e) * 2^e
-    // per head, in log2 units: reference mu of the row sum l_run; dm = mu - mo, mo the reference of
-    // score + log2 of the V scale (+inf before the first visible key); dv = 2^(dm - 20)
-    float mu[NT][2], l_run[NT][2], dm[NT][2], dv[NT][2];
+    // per head, in log2 units: reference mu of the weights (0 and l_run 0 before the first visible key)
+    float mu[NT][2], l_run[NT][2];
     float oacc[NT][8][4];
 
     auto begin_request = [&]() {
@@ -236,7 +197,7 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             float am = 0.f;
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
-                const int d = qdim<Q8>(s, c);
+                const int d = qdim(s, c);
                 uint32_t w0 = 0u, w1 = 0u;
                 if (g < G) {
                     w0 = q[d >> 1];
@@ -255,10 +216,7 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             hm[n][0] = __shfl_sync(0xffffffffu, q2, 8 * c);
             hm[n][1] = __shfl_sync(0xffffffffu, q2, 8 * c + 4);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                mu[n][j] = l_run[n][j] = dv[n][j] = 0.f;
-                dm[n][j] = INFINITY;
-            }
+            for (int j = 0; j < 2; ++j) mu[n][j] = l_run[n][j] = 0.f;
 #pragma unroll
             for (int t = 0; t < 8; ++t) oacc[n][t][0] = oacc[n][t][1] = oacc[n][t][2] = oacc[n][t][3] = 0.f;
         }
@@ -279,90 +237,62 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             const int g = 8 * n + rr;
             const uint32_t *q = reinterpret_cast<const uint32_t *>(
                 a.q_raw + (static_cast<size_t>(r) * a.hq + kvh * G + min(g, G - 1)) * kHeadDim);
-            const float sg = c < 2 ? -1.f : 1.f;   // codes: of the partner's sine
 #pragma unroll
-            for (int s = 0; s < 8; s += Q8 ? 2 : 1) {
-                if (!Q8 && s >= 4) break;
-                // two k-steps: codes s, s + 1; bf16 s, s + 4
-                const int t = Q8 ? s + 1 : s + 4;
+            for (int s = 0; s < 4; ++s) {
+                // k-steps s and s + 4: dims d .. d + 3 and their pairs
+                const int d = qdim(s, c);
                 float x[8];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int st = y < 2 ? s : t, d = qdim<Q8>(st, c) + 2 * (y & 1);
-                    const uint32_t w = g < G ? q[d >> 1] : 0u;
-                    const float4 z = *reinterpret_cast<const float4 *>(&cs[d & 63]);   // (cos, sin) of two pairs
-                    const float o0 = bf16_lo(w) * qn[n], o1 = bf16_hi(w) * qn[n];
-                    if (Q8) {
-                        const float p0 = __shfl_xor_sync(0xffffffffu, o0, 2), p1 = __shfl_xor_sync(0xffffffffu, o1, 2);
-                        x[2 * y] = o0 * z.x + sg * p0 * z.y;
-                        x[2 * y + 1] = o1 * z.z + sg * p1 * z.w;
-                    } else {
-                        x[2 * y] = o0;
-                        x[2 * y + 1] = o1;
-                    }
-                }
-                if (!Q8) {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float4 z = *reinterpret_cast<const float4 *>(&cs[qdim<Q8>(s, c) + 2 * y]);
-                        const float a0 = x[2 * y], a1 = x[2 * y + 1], b0 = x[4 + 2 * y], b1 = x[5 + 2 * y];
-                        x[2 * y] = a0 * z.x - b0 * z.y;
-                        x[2 * y + 1] = a1 * z.z - b1 * z.w;
-                        x[4 + 2 * y] = b0 * z.x + a0 * z.y;
-                        x[5 + 2 * y] = b1 * z.z + a1 * z.w;
-                    }
+                for (int y = 0; y < 2; ++y) {
+                    const uint32_t wa = g < G ? q[(d >> 1) + y] : 0u, wb = g < G ? q[(d >> 1) + 32 + y] : 0u;
+                    const float4 z = *reinterpret_cast<const float4 *>(&cs[d + 2 * y]);   // (cos, sin) of two pairs
+                    const float a0 = bf16_lo(wa) * qn[n], a1 = bf16_hi(wa) * qn[n];
+                    const float b0 = bf16_lo(wb) * qn[n], b1 = bf16_hi(wb) * qn[n];
+                    x[2 * y] = a0 * z.x - b0 * z.y;
+                    x[2 * y + 1] = a1 * z.z - b1 * z.w;
+                    x[4 + 2 * y] = b0 * z.x + a0 * z.y;
+                    x[5 + 2 * y] = b1 * z.z + a1 * z.w;
                 }
 #pragma unroll
                 for (int part = 0; part < QP; ++part) {
                     uint32_t w[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        if (Q8) {
-                            w[y] = pack_f16(x[2 * y], x[2 * y + 1]);
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[y]));
-                            x[2 * y] -= f.x;
-                            x[2 * y + 1] -= f.y;
-                        } else {
-                            w[y] = pack_bf16(x[2 * y], x[2 * y + 1]);
-                            x[2 * y] -= bf16_lo(w[y]);
-                            x[2 * y + 1] -= bf16_hi(w[y]);
-                        }
+                        w[y] = pack_bf16(x[2 * y], x[2 * y + 1]);
+                        x[2 * y] -= bf16_lo(w[y]);
+                        x[2 * y + 1] -= bf16_hi(w[y]);
                     }
                     if (C::kRegQ) {
                         qb[part][C::kRegQ ? s : 0][0] = w[0];
                         qb[part][C::kRegQ ? s : 0][1] = w[1];
-                        qb[part][C::kRegQ ? t : 0][0] = w[2];
-                        qb[part][C::kRegQ ? t : 0][1] = w[3];
+                        qb[part][C::kRegQ ? s + 4 : 0][0] = w[2];
+                        qb[part][C::kRegQ ? s + 4 : 0][1] = w[3];
                     } else {
                         qs[((n * QP + part) * 8 + s) * 32 + lane] = make_uint2(w[0], w[1]);
-                        qs[((n * QP + part) * 8 + t) * 32 + lane] = make_uint2(w[2], w[3]);
+                        qs[((n * QP + part) * 8 + s + 4) * 32 + lane] = make_uint2(w[2], w[3]);
                     }
                 }
             }
         }
     };
     auto end_request = [&]() {
-        const size_t slot = static_cast<size_t>(kvh) * (p.warps_per_head + B) + wi + r;
+        const size_t slot = static_cast<size_t>(kvh) * (p.pieces + B) + wi + r;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float l = l_run[n][j];
-                if (!MASS) {
-#pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-                }
                 const int g = 8 * n + 2 * c + j;
                 if (g < G) {
                     float *o = a.ws_acc + (slot * G + g) * kHeadDim;
 #pragma unroll
                     for (int t = 0; t < 8; t += 2) {
                         // tiles t and t + 1: four consecutive head dims
-                        *reinterpret_cast<float4 *>(o + odim<Q8>(t, rr)) =
+                        *reinterpret_cast<float4 *>(o + odim(t, rr)) =
                             make_float4(oacc[n][t][j], oacc[n][t][j + 2], oacc[n][t + 1][j], oacc[n][t + 1][j + 2]);
                     }
-                    if (rr == 0) p.ws_ml[slot * G + g] = dm[n][j] == INFINITY && l == l ? make_float4(-INFINITY, 0.f, -INFINITY, 0.f)
-                                                                                 : make_float4(mu[n][j], l, mu[n][j] - dm[n][j], 0.f);
+                    if (rr == 0)
+                        p.ws_ml[slot * G + g] = l_run[n][j] == 0.f ? make_float4(-INFINITY, 0.f, -INFINITY, 0.f)
+                                                                   : make_float4(mu[n][j], l_run[n][j], mu[n][j], 0.f);
                 }
             }
     };
@@ -379,11 +309,9 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
         if (k > 0 && (k & 31) == 0) {
             w_cur = w_nxt;
             m_cur = m_nxt;
-            ks_cur = ks_nxt;
-            vs_cur = vs_nxt;
             w_nxt = w_2nd;
             w_2nd = word_at(k + 64 + lane);
-            meta_at(k + 32 + lane, w_nxt, m_nxt, ks_nxt, vs_nxt);
+            m_nxt = meta_at(k + 32 + lane, w_nxt);
         }
         __syncwarp();   // every lane has read the stage that is loaded next
         issue(k + S - 1, (k & 31) + S - 1 >= 32, before);
@@ -403,45 +331,33 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
         }
         const uint32_t w = __shfl_sync(0xffffffffu, w_cur, k & 31);
         const uint32_t meta = __shfl_sync(0xffffffffu, m_cur, k & 31);
-        const float ksc = Q8 ? __shfl_sync(0xffffffffu, ks_cur, k & 31) : 1.f;
-        const float vsc = Q8 ? __shfl_sync(0xffffffffu, vs_cur, k & 31) : 1.f;
-        const float lv = Q8 ? fast_log2(vsc) : 0.f;
         const int i_req = lo + k - r_beg;                       // index of the word in its request
         const int off = word_offset(w);
         const int pos0 = off + meta_j0(meta);
         // keys of this word that the query sees: slots 0 .. lim - 1
         const int lim = i_req < a.max_words ? min(meta_valid(meta), qpos - pos0 + 1) : 0;
-        float *lse = MASS ? p.ws_lse + (static_cast<size_t>(r) * a.max_words + i_req) * a.hq + kvh * G : nullptr;
+        float *lse = p.ws_lse + (static_cast<size_t>(r) * a.max_words + i_req) * a.hq + kvh * G;
         if (lim <= 0) {
-            if (MASS && i_req < a.max_words && lane < G) lse[lane] = -INFINITY;
+            if (i_req < a.max_words && lane < G) lse[lane] = -INFINITY;
             continue;
         }
         if (cur_off < 0 || (off != cur_off && !a.alibi)) rotate(off);
 
-        const uint32_t st = smem_u32(stages) + sg * C::kStageBytes;
+        const uint32_t st = smem_u32(stages) + sg * kStageBytes;
         // ---- S^T [16 keys][8 heads] = K q^T
         float sa[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) sa[n][0] = sa[n][1] = sa[n][2] = sa[n][3] = 0.f;
 #pragma unroll
-        for (int m = 0; m < (Q8 ? 2 : 4); ++m) {
-            // piece 2c + (m & 1) of key rows rr and rr + 8 (bf16: of half m >> 1): four or two k-steps
+        for (int m = 0; m < 4; ++m) {
+            // piece 2c + (m & 1) of half m >> 1 of key rows rr and rr + 8: two k-steps
             const uint32_t ka = st + (m >> 1) * kBoxBytes + rr * 128 + (((2 * c + (m & 1)) ^ rr) << 4);
             const uint4 ra = lds16(ka), rb = lds16(ka + 1024);
             const uint32_t aw[4] = {ra.x, ra.y, ra.z, ra.w}, bw[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
-            for (int u = 0; u < (Q8 ? 4 : 2); ++u) {
-                const int s = (Q8 ? 4 : 2) * m + u;
-                uint32_t a0, a1, a2, a3;
-                if (Q8) {
-                    codes_to_f16(aw[u], a0, a2);
-                    codes_to_f16(bw[u], a1, a3);
-                } else {
-                    a0 = aw[2 * (u & 1)];
-                    a2 = aw[2 * (u & 1) + 1];
-                    a1 = bw[2 * (u & 1)];
-                    a3 = bw[2 * (u & 1) + 1];
-                }
+            for (int u = 0; u < 2; ++u) {
+                const int s = 2 * m + u;
+                const uint32_t a0 = aw[2 * u], a1 = bw[2 * u], a2 = aw[2 * u + 1], a3 = bw[2 * u + 1];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -451,20 +367,20 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
                             b = make_uint2(qb[part][C::kRegQ ? s : 0][0], qb[part][C::kRegQ ? s : 0][1]);
                         else
                             b = qs[((n * QP + part) * 8 + s) * 32 + lane];
-                        mma16<Q8>(sa[n], a0, a1, a2, a3, b.x, b.y);
+                        mma_bf16(sa[n], a0, a1, a2, a3, b.x, b.y);
                     }
             }
         }
-        // ---- softmax over the word's keys (rr and rr + 8 in this lane).  References (mu for the row sums, mo for
-        // score + log2 of the V scale) move only when some score passes them by kSlack: weights stay
-        // below 2^8 and most words need neither the maxima nor rescaling.
+        // ---- softmax over the word's keys (rr and rr + 8 in this lane).  A reference moves
+        // only when some score passes it by kSlack: weights stay below 2^8 and most words need neither the
+        // maxima nor rescaling.
         uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             // scores relative to mu
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float f = hm[n][j] * ksc;
+                const float f = hm[n][j];
                 sa[n][j] = fmaf(sa[n][j], f, -mu[n][j]);
                 sa[n][j + 2] = fmaf(sa[n][j + 2], f, -mu[n][j]);
             }
@@ -483,8 +399,10 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             }
             bool past = false;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-                past |= fmaxf(sa[n][j], sa[n][j + 2]) + fmaxf(Q8 || dm[n][j] == INFINITY ? lv + dm[n][j] : 0.f, 0.f) > kSlack;
+            for (int j = 0; j < 2; ++j) {
+                const float top = fmaxf(sa[n][j], sa[n][j + 2]);
+                past |= top > (l_run[n][j] == 0.f ? -INFINITY : kSlack);
+            }
             if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -492,14 +410,10 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
                     if (bm == -INFINITY) continue;   // this head sees no key of the word
-                    // up: the references' steps
-                    const bool first = dm[n][j] == INFINITY;
-                    const float up = first ? bm : fmaxf(bm, 0.f);
-                    const float mo_old = mu[n][j] - dm[n][j], top = mu[n][j] + bm + lv;
-                    const float mo = Q8 ? (first ? top : fmaxf(mo_old, top)) : mu[n][j] + up;
-                    if (!first) {
-                        l_run[n][j] *= fast_exp2(-up);
-                        const float sc = fast_exp2(mo_old - mo);
+                    const float up = l_run[n][j] == 0.f ? bm : fmaxf(bm, 0.f);
+                    if (l_run[n][j] != 0.f) {
+                        const float sc = fast_exp2(-up);
+                        l_run[n][j] *= sc;
 #pragma unroll
                         for (int t = 0; t < 8; ++t) {
                             oacc[n][t][j] *= sc;
@@ -509,40 +423,30 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
                     mu[n][j] += up;
                     sa[n][j] -= up;
                     sa[n][j + 2] -= up;
-                    dm[n][j] = mu[n][j] - mo;
-                    dv[n][j] = fast_exp2(fminf(dm[n][j] - 20.f, 126.f));
                 }
             }
             float pr[4];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float p0 = fast_exp2(sa[n][j]), p1 = fast_exp2(sa[n][j + 2]);
+                const float p0 = fast_exp2(sa[n][j]), p1 = fast_exp2(sa[n][j + 2]);
                 float ps = p0 + p1;
-                if (MASS) {
 #pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, x);
-                    const int g = 8 * n + 2 * c + j;
-                    if (rr == 0 && g < G) lse[g] = mu[n][j] + fast_log2(ps);
-                }
+                for (int x = 4; x < 32; x <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, x);
+                const int g = 8 * n + 2 * c + j;
+                if (rr == 0 && g < G) lse[g] = mu[n][j] + fast_log2(ps);
                 l_run[n][j] += ps;
-                if (Q8) {
-                    // weights for the V product: w s_v against 2^mo (two factors: s_v spans the range of a float)
-                    const float f = vsc * dv[n][j] * 0x1p20f;
-                    p0 *= f;
-                    p1 *= f;
-                }
                 pr[j] = p0;
                 pr[j + 2] = p1;
             }
             // P^T (keys x heads) to the B fragment
-            pb[n][0] = movmatrix_t(Q8 ? pack_f16(pr[0], pr[1]) : pack_bf16(pr[0], pr[1]));
-            pb[n][1] = movmatrix_t(Q8 ? pack_f16(pr[2], pr[3]) : pack_bf16(pr[2], pr[3]));
+            pb[n][0] = movmatrix_t(pack_bf16(pr[0], pr[1]));
+            pb[n][1] = movmatrix_t(pack_bf16(pr[2], pr[3]));
         }
         // ---- O^T [128][8 heads] += V^T P^T
-        const uint32_t sv = st + C::kTile + 2 * c * 128;
+        const uint32_t sv = st + kTileBytes + 2 * c * 128;
         const uint32_t x0 = (rr ^ (2 * c)) << 4, x1 = (rr ^ (2 * c + 1)) << 4;
 #pragma unroll
-        for (int m = 0; m < (Q8 ? 1 : 2); ++m) {
+        for (int m = 0; m < 2; ++m) {
             uint4 v0 = lds16(sv + kBoxBytes * m + x0), v1 = lds16(sv + kBoxBytes * m + 128 + x1);
             uint4 v2 = lds16(sv + kBoxBytes * m + 1024 + x0), v3 = lds16(sv + kBoxBytes * m + 1152 + x1);
             if (lim < kBlockTokens) {
@@ -557,22 +461,10 @@ __global__ void __launch_bounds__((Cfg<Q8, NT, MASS>::kWarps * 32), (Cfg<Q8, NT,
             const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                if (Q8) {
-                    uint32_t a0, a1, a2, a3;
+                const uint32_t a0 = __byte_perm(w0[x], w1[x], 0x5410), a1 = __byte_perm(w0[x], w1[x], 0x7632);
+                const uint32_t a2 = __byte_perm(w2[x], w3[x], 0x5410), a3 = __byte_perm(w2[x], w3[x], 0x7632);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t sel = u ? 0x7362 : 0x5140;   // codes of keys 2c, 2c+1 side by side, two dims
-                        codes_to_f16(__byte_perm(w0[x], w1[x], sel), a0, a1);
-                        codes_to_f16(__byte_perm(w2[x], w3[x], sel), a2, a3);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16<Q8>(oacc[n][2 * x + u], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-                    }
-                } else {
-                    const uint32_t a0 = __byte_perm(w0[x], w1[x], 0x5410), a1 = __byte_perm(w0[x], w1[x], 0x7632);
-                    const uint32_t a2 = __byte_perm(w2[x], w3[x], 0x5410), a3 = __byte_perm(w2[x], w3[x], 0x7632);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16<Q8>(oacc[n][4 * m + x], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-                }
+                for (int n = 0; n < NT; ++n) mma_bf16(oacc[n][4 * m + x], a0, a1, a2, a3, pb[n][0], pb[n][1]);
             }
         }
     }
@@ -622,14 +514,14 @@ __global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kerne
     const unsigned total = a.table_indptr[B] - base;
     const unsigned beg = a.table_indptr[r] - base;
     const int n = min(a.table_indptr[r + 1] - base - static_cast<int>(beg), a.max_words);
-    const unsigned per = max(static_cast<unsigned>(min_words), (total + p.warps_per_head - 1) / static_cast<unsigned>(p.warps_per_head));
+    const unsigned per = max(static_cast<unsigned>(min_words), (total + p.pieces - 1) / static_cast<unsigned>(p.pieces));
     const unsigned w0 = n > 0 ? beg / per : 0;
     const int nw = n > 0 ? static_cast<int>((beg + n - 1) / per - w0 + 1) : 0;
     if (blockIdx.y < out_ctas) {
         const unsigned h = JOIN > 1 ? blockIdx.y : blockIdx.y * 4 + warp;
         if (h >= hq) return;
         const unsigned kvh = h / G, g = h - kvh * G;
-        const size_t s0 = static_cast<size_t>(kvh) * (p.warps_per_head + B) + w0 + r;
+        const size_t s0 = static_cast<size_t>(kvh) * (p.pieces + B) + w0 + r;
         const float4 *ml = p.ws_ml + s0 * G + g;
         float M, L, MO;
         join_head(ml, nw, G, lane, M, L, MO);
@@ -671,7 +563,7 @@ __global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kerne
         if (c0 >= n) return;
         for (unsigned h = JOIN > 1 ? warp : threadIdx.x; h < hq; h += JOIN > 1 ? kWarps : 128) {
             const unsigned kvh = h / G, g = h - kvh * G;
-            const float4 *ml = p.ws_ml + (static_cast<size_t>(kvh) * (p.warps_per_head + B) + w0 + r) * G + g;
+            const float4 *ml = p.ws_ml + (static_cast<size_t>(kvh) * (p.pieces + B) + w0 + r) * G + g;
             float M = -INFINITY, L = 0.f, MO;
             if (JOIN > 1) {
                 join_head(ml, nw, G, lane, M, L, MO);
@@ -698,44 +590,34 @@ __global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kerne
     }
 }
 
-template <bool Q8, int NT, bool MASS>
+template <int NT>
 cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
-    using C = Cfg<Q8, NT, MASS>;
-    auto kern = decode_lane_kernel<Q8, NT, MASS>;
+    using C = Cfg<NT>;
+    auto kern = decode_lane_kernel<NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    const int ctas = (p.warps_per_head * p.a.hkv + C::kWarps - 1) / C::kWarps;
+    const int ctas = (p.pieces * p.a.hkv + C::kWarps - 1) / C::kWarps;
     kern<<<ctas, C::kWarps * 32, C::kSmem, s>>>(tk, tv, p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_lane_combine(p, kMinWords, s);
 }
 
-template <bool Q8, bool MASS>
-cudaError_t launch_g(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
-    if (p.a.group <= 8) return launch_t<Q8, 1, MASS>(tk, tv, p, s);
-    return p.a.group <= 16 ? launch_t<Q8, 2, MASS>(tk, tv, p, s) : launch_t<Q8, 4, MASS>(tk, tv, p, s);
-}
+template <int NT>
+constexpr int kResident = Cfg<NT>::kOcc * Cfg<NT>::kWarps;
 
 }  // namespace
 
-template <bool Q8, bool MASS>
-static int resident_warps(int group) {
-    if (group <= 8) return Cfg<Q8, 1, MASS>::kOcc * Cfg<Q8, 1, MASS>::kWarps;
-    return group <= 16 ? Cfg<Q8, 2, MASS>::kOcc * Cfg<Q8, 2, MASS>::kWarps : Cfg<Q8, 4, MASS>::kOcc * Cfg<Q8, 4, MASS>::kWarps;
-}
-
-LanePlan lane_plan(int num_req, int hkv, int max_words, int group, bool q8, bool mass, int sms) {
+LanePlan decode_mass_plan(int num_req, int hkv, int max_words, int group, int sms) {
     // one wave of resident warps, but at least kMinWords words each
-    const int per_sm = !q8 ? resident_warps<false, true>(group)
-                           : mass ? resident_warps<true, true>(group) : resident_warps<true, false>(group);
+    const int per_sm = group <= 8 ? kResident<1> : group <= 16 ? kResident<2> : kResident<4>;
     const int64_t words = static_cast<int64_t>(num_req) * max_words;
     const int64_t most = (words + kMinWords - 1) / kMinWords;
     const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * per_sm / hkv;
     LanePlan pl;
-    pl.warps_per_head = static_cast<int>(most < resident ? most : resident);
-    if (pl.warps_per_head < 1) pl.warps_per_head = 1;
-    pl.slots = static_cast<int64_t>(hkv) * (pl.warps_per_head + num_req);
+    pl.pieces = static_cast<int>(most < resident ? most : resident);
+    if (pl.pieces < 1) pl.pieces = 1;
+    pl.slots = static_cast<int64_t>(hkv) * (pl.pieces + num_req);
     return pl;
 }
 
@@ -743,14 +625,14 @@ cudaError_t launch_lane_combine(const LaneParams &p, int min_words, cudaStream_t
     const int chunks = p.mass ? (p.a.max_words + kMassWords - 1) / kMassWords : 0;
     const size_t smem = p.mass ? p.a.hq * sizeof(float) : 0;
     // a request has about pieces / requests partials
-    if (p.warps_per_head > 8 * p.a.num_req)
+    if (p.pieces > 8 * p.a.num_req)
         return launch_dependent(lane_combine_kernel<8>, dim3(p.a.num_req, p.a.hq + chunks), 256, smem, s, p, min_words);
     return launch_dependent(lane_combine_kernel<1>, dim3(p.a.num_req, (p.a.hq + 3) / 4 + chunks), 128, smem, s, p, min_words);
 }
 
-cudaError_t launch_decode_lane(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, bool q8, cudaStream_t s) {
-    if (!q8) return launch_g<false, true>(tk, tv, p, s);
-    return p.mass ? launch_g<true, true>(tk, tv, p, s) : launch_g<true, false>(tk, tv, p, s);
+cudaError_t launch_decode_mass(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
+    if (p.a.group <= 8) return launch_t<1>(tk, tv, p, s);
+    return p.a.group <= 16 ? launch_t<2>(tk, tv, p, s) : launch_t<4>(tk, tv, p, s);
 }
 
 }  // namespace lazy

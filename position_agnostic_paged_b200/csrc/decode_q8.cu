@@ -189,7 +189,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
     const int base = a.table_indptr[0];
     const int total = a.table_indptr[B] - base;
     if (total <= 0) return;
-    const int per = words_per_piece(total, p.warps_per_head);
+    const int per = words_per_piece(total, p.pieces);
     if (wi > (total - 1) / per) return;
     const int lo = wi * per, cnt = min(total - lo, per);
 
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
         // a request none of whose words here is visible has no tile to write its partial result
         auto leave = [&]() {
             if (j == first && lane < G)
-                p.ws_ml[((static_cast<size_t>(kvh) * (p.warps_per_head + B)) + wi + r) * G + lane] =
+                p.ws_ml[((static_cast<size_t>(kvh) * (p.pieces + B)) + wi + r) * G + lane] =
                     make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
             first = j;
         };
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 ok = !any_softmax<C::kSoft>(!warp_wait(&odone[buf], (i >> 1) & 1, abort_flag, a.d_status));
                 if (!ok) break;
                 tc::fence_after_sync();
-                const size_t slot_g = (static_cast<size_t>(kvh) * (p.warps_per_head + B) + wi + r) * G;
+                const size_t slot_g = (static_cast<size_t>(kvh) * (p.pieces + B) + wi + r) * G;
 #pragma unroll
                 for (int h = 0; h < HT; ++h) {
                     float s = l[h];
@@ -743,7 +743,7 @@ cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const LanePar
     auto kern = decode_q8_kernel<NG, QP, MASS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<p.warps_per_head * p.a.hkv, C::kThreads, C::kSmem, s>>>(tk, tv, p);
+    kern<<<p.pieces * p.a.hkv, C::kThreads, C::kSmem, s>>>(tk, tv, p);
     return cudaGetLastError();
 }
 template <int NG>
@@ -763,9 +763,9 @@ LanePlan decode_q8_plan(int num_req, int hkv, int max_words, int group, bool mas
     const int64_t most = (words + kLineMinWordsQ8 - 1) / kLineMinWordsQ8;
     const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * (mass ? occupancy<5>(group) : occupancy<3>(group)) / hkv;
     LanePlan pl;
-    pl.warps_per_head = static_cast<int>(most < resident ? most : resident);
-    if (pl.warps_per_head < 1) pl.warps_per_head = 1;
-    pl.slots = static_cast<int64_t>(hkv) * (pl.warps_per_head + num_req);
+    pl.pieces = static_cast<int>(most < resident ? most : resident);
+    if (pl.pieces < 1) pl.pieces = 1;
+    pl.slots = static_cast<int64_t>(hkv) * (pl.pieces + num_req);
     return pl;
 }
 

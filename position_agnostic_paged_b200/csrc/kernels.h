@@ -138,7 +138,7 @@ inline size_t q8_write_ws_bytes(int num_blocks) {
 }
 cudaError_t launch_kv_write_q8(const Q8WriteParams &p, cudaStream_t s);
 
-// Streaming decode (decode_lane.cu) over the 8-bit pool, or over the bf16 pool with block mass.
+// Streaming decode, over the 8-bit pool (decode_q8.cu) or over the bf16 pool with block mass (decode_lane.cu).
 // a.ws_acc: partial outputs [slot][G][128]; ws_ml: per partial (running max, sum, output
 // reference, 0) [slot][G]; ws_lse: log2 of each word's weight sum [num_req][max_words][Hq].
 struct LaneParams {
@@ -147,22 +147,21 @@ struct LaneParams {
     float4 *ws_ml;
     float *ws_lse;
     float *mass;                     // null: no accumulators
-    int warps_per_head;              // warps that share one KV head's words
+    int pieces;                      // of one KV head's words
 };
 struct LanePlan {
-    int warps_per_head;
+    int pieces;
     int64_t slots;                   // partials in the workspace
 };
-LanePlan lane_plan(int num_req, int hkv, int max_words, int group, bool q8, bool mass, int sms);
-// tk, tv: the codes as rows of 128 bytes (one box = one block of one head), or the bf16 pools as rows of 128
-// elements (one box = half of one).
 // Joins the partials of every request; min_words: the least words of a piece of the line.
 cudaError_t launch_lane_combine(const LaneParams &p, int min_words, cudaStream_t s);
-// Decode over the 8-bit pool (decode_q8.cu): warps_per_head is the number of pieces, one CTA each.
+// tk, tv: the codes as rows of 128 bytes, one box = one block of one head; a piece per CTA.
 constexpr int kLineMinWordsQ8 = 8;
 LanePlan decode_q8_plan(int num_req, int hkv, int max_words, int group, bool mass, int sms);
 cudaError_t launch_decode_q8(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s);
-cudaError_t launch_decode_lane(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, bool q8, cudaStream_t s);
+// tk, tv: the bf16 pools as rows of 128 elements, one box = half of one block of one head; a piece per warp.
+LanePlan decode_mass_plan(int num_req, int hkv, int max_words, int group, int sms);
+cudaError_t launch_decode_mass(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s);
 
 // Prefill over the 8-bit pool (prefill_q8.cu).  a.q_prep: prepared query tiles; row_scale: their row
 // factors [units][256]; units from a.pf_base run as `parts` CTAs each.
