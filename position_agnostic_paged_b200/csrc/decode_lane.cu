@@ -61,24 +61,14 @@ constexpr int kQParts = 3;
 constexpr int kTileBytes = 2 * kBoxBytes;        // K (or V) of one word and head
 constexpr int kStageBytes = 2 * kTileBytes;
 
-// NT: groups of 8 query heads per KV head.
-template <int NT>
-struct Cfg {
-    static constexpr bool kRegQ = NT == 1;                     // query fragments in registers, else in shared memory
-    static constexpr int kQBytes = kRegQ ? 0 : NT * kQParts * 8 * 32 * 8;      // query fragments per warp
-    static constexpr int kExtra = kQBytes + 512 + 64;                     // query fragments, angles, barriers
-    static constexpr int kLeast = 2 * kStageBytes + kExtra;               // shared memory per warp, two stages
-    // CTAs per SM by registers (4 warps each); where the query fragments leave no room for two stages of so
-    // many warps (G > 8): one CTA of as many warps as fit
-    static constexpr int kOcc0 = NT == 4 ? 2 : 3;
-    static constexpr bool kFits = kOcc0 * (4 * kLeast + 2048) <= 227 * 1024;
-    static constexpr int kOcc = kFits ? kOcc0 : 1;
-    static constexpr int kWarps = kFits ? 4 : 225 * 1024 / kLeast;
-    static constexpr int kStages0 = ((227 * 1024 / kOcc - 2048) / kWarps - kExtra) / kStageBytes;
-    static constexpr int kStages = kStages0 > 8 ? 8 : kStages0;
-    static constexpr int kSmem = kWarps * (kStages * kStageBytes + kExtra) + 1024;   // stages 1 KiB aligned
-    static_assert(kStages >= 2 && kWarps <= 8, "pipeline depth");
-};
+constexpr int kWarps = 4, kOcc = 3;              // per CTA; CTAs per SM, by registers
+constexpr int kExtra = 512 + 64;                 // angles, barriers of a warp
+constexpr int kStages = ((227 * 1024 / kOcc - 2048) / kWarps - kExtra) / kStageBytes;
+constexpr int kSmem = kWarps * (kStages * kStageBytes + kExtra) + 1024;   // stages 1 KiB aligned
+static_assert(kStages >= 2 && kStages <= 8, "pipeline depth");
+
+// Groups of 8 query heads of a KV head.
+__host__ __device__ inline int head_groups(int group) { return (group + 7) / 8; }
 
 // First of the four head dims of the query fragment's registers for k-step s: rows are two halves of 64 dims,
 // lane c has dims 16c .. + 15 of each, and rotation pairs lie in k-steps s and s + 4.
@@ -86,13 +76,11 @@ __device__ __forceinline__ int qdim(int s, int c) { return 16 * c + 4 * (s & 3) 
 // First head dim of output tile t's row pair (rows rr and rr + 8 hold odim and odim + 1).
 __device__ __forceinline__ int odim(int t, int rr) { return 64 * (t >> 2) + 8 * rr + 2 * (t & 3); }
 
-template <int NT>
-__global__ void __launch_bounds__((Cfg<NT>::kWarps * 32), (Cfg<NT>::kOcc))
+__global__ void __launch_bounds__(kWarps * 32, kOcc)
     decode_lane_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ LaneParams p) {
-    using C = Cfg<NT>;
     pdl_trigger();
-    constexpr int QP = kQParts, S = C::kStages, kWarps = C::kWarps;
+    constexpr int QP = kQParts, S = kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -100,7 +88,9 @@ __global__ void __launch_bounds__((Cfg<NT>::kWarps * 32), (Cfg<NT>::kOcc))
     const AttnParams &a = p.a;
     const int G = a.group, hkv = a.hkv, B = a.num_req;
     const int gw = blockIdx.x * kWarps + warp;
-    const int kvh = gw % hkv, wi = gw / hkv;
+    // neighbouring warps take the head groups of one KV head: its words come from L2 for all but the first
+    const int groups = head_groups(G), wi = gw / (hkv * groups), line = gw - wi * hkv * groups;
+    const int kvh = line / groups, g0 = 8 * (line - kvh * groups);
     // the rotation frequencies: a per-lane read of the parameter table takes 32 turns
     __shared__ double theta[kHalfDim];
     for (int i = threadIdx.x; i < kHalfDim; i += kWarps * 32) theta[i] = a.rope.theta[i];
@@ -114,10 +104,9 @@ __global__ void __launch_bounds__((Cfg<NT>::kWarps * 32), (Cfg<NT>::kOcc))
     const int lo = wi * per, cnt = min(total - lo, per);
 
     uint8_t *stages = sm + warp * S * kStageBytes;
-    uint8_t *extra = sm + kWarps * S * kStageBytes + warp * C::kExtra;
-    uint2 *qs = reinterpret_cast<uint2 *>(extra);                              // [NT][QP][8][32]
-    float2 *cs = reinterpret_cast<float2 *>(extra + C::kQBytes);               // [64]
-    uint64_t *bars = reinterpret_cast<uint64_t *>(extra + C::kQBytes + 512);   // [S]
+    uint8_t *extra = sm + kWarps * S * kStageBytes + warp * kExtra;
+    float2 *cs = reinterpret_cast<float2 *>(extra);               // [64]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(extra + 512);   // [S]
     if (lane < S) mbar_init(&bars[lane], 1);
     fence_barrier_init();
     fence_proxy_async_smem();
@@ -177,49 +166,46 @@ __global__ void __launch_bounds__((Cfg<NT>::kWarps * 32), (Cfg<NT>::kOcc))
     }
     int r_beg = a.table_indptr[r] - base, r_end = a.table_indptr[r + 1] - base;
     int qpos = 0, cur_off = -1;
-    uint32_t qb[C::kRegQ ? QP : 1][C::kRegQ ? 8 : 1][2];
-    float qn[NT];            // 2^-e of this lane's fragment head (8 n + rr)
-    float hm[NT][2];         // score factor of heads 8 n + 2c, + 1: softmax scale * log2(e) * 2^e
+    uint32_t qb[QP][8][2];
+    float qn;            // 2^-e of this lane's fragment head (g0 + rr)
+    float hm[2];         // score factor of heads g0 + 2c, + 1: softmax scale * log2(e) * 2^e
     // per head, in log2 units: reference mu of the weights (0 and l_run 0 before the first visible key)
-    float mu[NT][2], l_run[NT][2];
-    float oacc[NT][8][4];
+    float mu[2], l_run[2];
+    float oacc[8][4];
 
     auto begin_request = [&]() {
         qpos = a.q_pos[r];
         cur_off = -1;
-        if (lo <= r_beg && r_end - r_beg > a.max_words && kvh == 0 && lane == 0)
+        if (lo <= r_beg && r_end - r_beg > a.max_words && line == 0 && lane == 0)
             set_status(a.d_status, LAZY_DSTATUS_BAD_TABLE);
+        const int g = g0 + rr;
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(
+            a.q_raw + (static_cast<size_t>(r) * a.hq + kvh * G + min(g, G - 1)) * kHeadDim);
+        float am = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int g = 8 * n + rr;
-            const uint32_t *q = reinterpret_cast<const uint32_t *>(
-                a.q_raw + (static_cast<size_t>(r) * a.hq + kvh * G + min(g, G - 1)) * kHeadDim);
-            float am = 0.f;
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const int d = qdim(s, c);
-                uint32_t w0 = 0u, w1 = 0u;
-                if (g < G) {
-                    w0 = q[d >> 1];
-                    w1 = q[(d >> 1) + 1];
-                }
-                am = fmaxf(am, fmaxf(fmaxf(fabsf(bf16_lo(w0)), fabsf(bf16_hi(w0))),
-                                     fmaxf(fabsf(bf16_lo(w1)), fabsf(bf16_hi(w1)))));
+        for (int s = 0; s < 8; ++s) {
+            const int d = qdim(s, c);
+            uint32_t w0 = 0u, w1 = 0u;
+            if (g < G) {
+                w0 = q[d >> 1];
+                w1 = q[(d >> 1) + 1];
             }
-            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
-            am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
-            // q 2^-e in [1, 2); e = 0 for an all-zero or non-finite head
-            int e = static_cast<int>(__float_as_uint(am) >> 23) - 127;
-            e = (am == 0.f || e == 128) ? 0 : max(-126, min(126, e));
-            qn[n] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            const float q2 = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.scale_log2;
-            hm[n][0] = __shfl_sync(0xffffffffu, q2, 8 * c);
-            hm[n][1] = __shfl_sync(0xffffffffu, q2, 8 * c + 4);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) mu[n][j] = l_run[n][j] = 0.f;
-#pragma unroll
-            for (int t = 0; t < 8; ++t) oacc[n][t][0] = oacc[n][t][1] = oacc[n][t][2] = oacc[n][t][3] = 0.f;
+            am = fmaxf(am, fmaxf(fmaxf(fabsf(bf16_lo(w0)), fabsf(bf16_hi(w0))),
+                                 fmaxf(fabsf(bf16_lo(w1)), fabsf(bf16_hi(w1)))));
         }
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        // q 2^-e in [1, 2); e = 0 for an all-zero or non-finite head
+        int e = static_cast<int>(__float_as_uint(am) >> 23) - 127;
+        e = (am == 0.f || e == 128) ? 0 : max(-126, min(126, e));
+        qn = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const float q2 = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.scale_log2;
+        hm[0] = __shfl_sync(0xffffffffu, q2, 8 * c);
+        hm[1] = __shfl_sync(0xffffffffu, q2, 8 * c + 4);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mu[j] = l_run[j] = 0.f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) oacc[t][0] = oacc[t][1] = oacc[t][2] = oacc[t][3] = 0.f;
     };
     // the query turned by (qpos - off), as fragments: angles once per warp (two per lane), shared
     auto rotate = [&](int off) {
@@ -232,69 +218,59 @@ __global__ void __launch_bounds__((Cfg<NT>::kWarps * 32), (Cfg<NT>::kOcc))
         cs[lane] = z0;
         cs[lane + 32] = z1;
         __syncwarp();
+        const int g = g0 + rr;
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(
+            a.q_raw + (static_cast<size_t>(r) * a.hq + kvh * G + min(g, G - 1)) * kHeadDim);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int g = 8 * n + rr;
-            const uint32_t *q = reinterpret_cast<const uint32_t *>(
-                a.q_raw + (static_cast<size_t>(r) * a.hq + kvh * G + min(g, G - 1)) * kHeadDim);
+        for (int s = 0; s < 4; ++s) {
+            // k-steps s and s + 4: dims d .. d + 3 and their pairs
+            const int d = qdim(s, c);
+            float x[8];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                // k-steps s and s + 4: dims d .. d + 3 and their pairs
-                const int d = qdim(s, c);
-                float x[8];
+            for (int y = 0; y < 2; ++y) {
+                const uint32_t wa = g < G ? q[(d >> 1) + y] : 0u, wb = g < G ? q[(d >> 1) + 32 + y] : 0u;
+                const float4 z = *reinterpret_cast<const float4 *>(&cs[d + 2 * y]);   // (cos, sin) of two pairs
+                const float a0 = bf16_lo(wa) * qn, a1 = bf16_hi(wa) * qn;
+                const float b0 = bf16_lo(wb) * qn, b1 = bf16_hi(wb) * qn;
+                x[2 * y] = a0 * z.x - b0 * z.y;
+                x[2 * y + 1] = a1 * z.z - b1 * z.w;
+                x[4 + 2 * y] = b0 * z.x + a0 * z.y;
+                x[5 + 2 * y] = b1 * z.z + a1 * z.w;
+            }
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const uint32_t wa = g < G ? q[(d >> 1) + y] : 0u, wb = g < G ? q[(d >> 1) + 32 + y] : 0u;
-                    const float4 z = *reinterpret_cast<const float4 *>(&cs[d + 2 * y]);   // (cos, sin) of two pairs
-                    const float a0 = bf16_lo(wa) * qn[n], a1 = bf16_hi(wa) * qn[n];
-                    const float b0 = bf16_lo(wb) * qn[n], b1 = bf16_hi(wb) * qn[n];
-                    x[2 * y] = a0 * z.x - b0 * z.y;
-                    x[2 * y + 1] = a1 * z.z - b1 * z.w;
-                    x[4 + 2 * y] = b0 * z.x + a0 * z.y;
-                    x[5 + 2 * y] = b1 * z.z + a1 * z.w;
+            for (int part = 0; part < QP; ++part) {
+                uint32_t w[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    w[y] = pack_bf16(x[2 * y], x[2 * y + 1]);
+                    x[2 * y] -= bf16_lo(w[y]);
+                    x[2 * y + 1] -= bf16_hi(w[y]);
                 }
-#pragma unroll
-                for (int part = 0; part < QP; ++part) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        w[y] = pack_bf16(x[2 * y], x[2 * y + 1]);
-                        x[2 * y] -= bf16_lo(w[y]);
-                        x[2 * y + 1] -= bf16_hi(w[y]);
-                    }
-                    if (C::kRegQ) {
-                        qb[part][C::kRegQ ? s : 0][0] = w[0];
-                        qb[part][C::kRegQ ? s : 0][1] = w[1];
-                        qb[part][C::kRegQ ? s + 4 : 0][0] = w[2];
-                        qb[part][C::kRegQ ? s + 4 : 0][1] = w[3];
-                    } else {
-                        qs[((n * QP + part) * 8 + s) * 32 + lane] = make_uint2(w[0], w[1]);
-                        qs[((n * QP + part) * 8 + s + 4) * 32 + lane] = make_uint2(w[2], w[3]);
-                    }
-                }
+                qb[part][s][0] = w[0];
+                qb[part][s][1] = w[1];
+                qb[part][s + 4][0] = w[2];
+                qb[part][s + 4][1] = w[3];
             }
         }
     };
     auto end_request = [&]() {
         const size_t slot = static_cast<size_t>(kvh) * (p.pieces + B) + wi + r;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int j = 0; j < 2; ++j) {
+            const int g = g0 + 2 * c + j;
+            if (g < G) {
+                float *o = a.ws_acc + (slot * G + g) * kHeadDim;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int g = 8 * n + 2 * c + j;
-                if (g < G) {
-                    float *o = a.ws_acc + (slot * G + g) * kHeadDim;
-#pragma unroll
-                    for (int t = 0; t < 8; t += 2) {
-                        // tiles t and t + 1: four consecutive head dims
-                        *reinterpret_cast<float4 *>(o + odim(t, rr)) =
-                            make_float4(oacc[n][t][j], oacc[n][t][j + 2], oacc[n][t + 1][j], oacc[n][t + 1][j + 2]);
-                    }
-                    if (rr == 0)
-                        p.ws_ml[slot * G + g] = l_run[n][j] == 0.f ? make_float4(-INFINITY, 0.f, -INFINITY, 0.f)
-                                                                   : make_float4(mu[n][j], l_run[n][j], mu[n][j], 0.f);
+                for (int t = 0; t < 8; t += 2) {
+                    // tiles t and t + 1: four consecutive head dims
+                    *reinterpret_cast<float4 *>(o + odim(t, rr)) =
+                        make_float4(oacc[t][j], oacc[t][j + 2], oacc[t + 1][j], oacc[t + 1][j + 2]);
                 }
+                if (rr == 0)
+                    p.ws_ml[slot * G + g] = l_run[j] == 0.f ? make_float4(-INFINITY, 0.f, -INFINITY, 0.f)
+                                                               : make_float4(mu[j], l_run[j], mu[j], 0.f);
             }
+        }
     };
     begin_request();
 
@@ -338,16 +314,14 @@ __global__ void __launch_bounds__((Cfg<NT>::kWarps * 32), (Cfg<NT>::kOcc))
         const int lim = i_req < a.max_words ? min(meta_valid(meta), qpos - pos0 + 1) : 0;
         float *lse = p.ws_lse + (static_cast<size_t>(r) * a.max_words + i_req) * a.hq + kvh * G;
         if (lim <= 0) {
-            if (i_req < a.max_words && lane < G) lse[lane] = -INFINITY;
+            if (i_req < a.max_words && lane < 8 && g0 + lane < G) lse[g0 + lane] = -INFINITY;
             continue;
         }
         if (cur_off < 0 || (off != cur_off && !a.alibi)) rotate(off);
 
         const uint32_t st = smem_u32(stages) + sg * kStageBytes;
         // ---- S^T [16 keys][8 heads] = K q^T
-        float sa[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) sa[n][0] = sa[n][1] = sa[n][2] = sa[n][3] = 0.f;
+        float sa[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             // piece 2c + (m & 1) of half m >> 1 of key rows rr and rr + 8: two k-steps
@@ -359,89 +333,75 @@ __global__ void __launch_bounds__((Cfg<NT>::kWarps * 32), (Cfg<NT>::kOcc))
                 const int s = 2 * m + u;
                 const uint32_t a0 = aw[2 * u], a1 = bw[2 * u], a2 = aw[2 * u + 1], a3 = bw[2 * u + 1];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int part = 0; part < QP; ++part) {
-                        uint2 b;
-                        if (C::kRegQ)
-                            b = make_uint2(qb[part][C::kRegQ ? s : 0][0], qb[part][C::kRegQ ? s : 0][1]);
-                        else
-                            b = qs[((n * QP + part) * 8 + s) * 32 + lane];
-                        mma_bf16(sa[n], a0, a1, a2, a3, b.x, b.y);
-                    }
+                for (int part = 0; part < QP; ++part) mma_bf16(sa, a0, a1, a2, a3, qb[part][s][0], qb[part][s][1]);
             }
         }
         // ---- softmax over the word's keys (rr and rr + 8 in this lane).  A reference moves
         // only when some score passes it by kSlack: weights stay below 2^8 and most words need neither the
         // maxima nor rescaling.
-        uint32_t pb[NT][2];
+        // scores relative to mu
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            // scores relative to mu
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float f = hm[n][j];
-                sa[n][j] = fmaf(sa[n][j], f, -mu[n][j]);
-                sa[n][j + 2] = fmaf(sa[n][j + 2], f, -mu[n][j]);
-            }
-            if (a.alibi) {
-                const float d0 = static_cast<float>(pos0 + rr - qpos);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float sl = 8 * n + 2 * c + j < G ? a.alibi_log2[kvh * G + 8 * n + 2 * c + j] : 0.f;
-                    sa[n][j] = fmaf(sl, d0, sa[n][j]);
-                    sa[n][j + 2] = fmaf(sl, d0 + 8.f, sa[n][j + 2]);
-                }
-            }
-            if (lim < kBlockTokens) {
-                if (rr >= lim) sa[n][0] = sa[n][1] = -INFINITY;
-                if (rr + 8 >= lim) sa[n][2] = sa[n][3] = -INFINITY;
-            }
-            bool past = false;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float top = fmaxf(sa[n][j], sa[n][j + 2]);
-                past |= top > (l_run[n][j] == 0.f ? -INFINITY : kSlack);
-            }
-            if (__any_sync(0xffffffffu, past)) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float bm = fmaxf(sa[n][j], sa[n][j + 2]);
-#pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
-                    if (bm == -INFINITY) continue;   // this head sees no key of the word
-                    const float up = l_run[n][j] == 0.f ? bm : fmaxf(bm, 0.f);
-                    if (l_run[n][j] != 0.f) {
-                        const float sc = fast_exp2(-up);
-                        l_run[n][j] *= sc;
-#pragma unroll
-                        for (int t = 0; t < 8; ++t) {
-                            oacc[n][t][j] *= sc;
-                            oacc[n][t][j + 2] *= sc;
-                        }
-                    }
-                    mu[n][j] += up;
-                    sa[n][j] -= up;
-                    sa[n][j + 2] -= up;
-                }
-            }
-            float pr[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float p0 = fast_exp2(sa[n][j]), p1 = fast_exp2(sa[n][j + 2]);
-                float ps = p0 + p1;
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, x);
-                const int g = 8 * n + 2 * c + j;
-                if (rr == 0 && g < G) lse[g] = mu[n][j] + fast_log2(ps);
-                l_run[n][j] += ps;
-                pr[j] = p0;
-                pr[j + 2] = p1;
-            }
-            // P^T (keys x heads) to the B fragment
-            pb[n][0] = movmatrix_t(pack_bf16(pr[0], pr[1]));
-            pb[n][1] = movmatrix_t(pack_bf16(pr[2], pr[3]));
+        for (int j = 0; j < 2; ++j) {
+            sa[j] = fmaf(sa[j], hm[j], -mu[j]);
+            sa[j + 2] = fmaf(sa[j + 2], hm[j], -mu[j]);
         }
+        if (a.alibi) {
+            const float d0 = static_cast<float>(pos0 + rr - qpos);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float sl = g0 + 2 * c + j < G ? a.alibi_log2[kvh * G + g0 + 2 * c + j] : 0.f;
+                sa[j] = fmaf(sl, d0, sa[j]);
+                sa[j + 2] = fmaf(sl, d0 + 8.f, sa[j + 2]);
+            }
+        }
+        if (lim < kBlockTokens) {
+            if (rr >= lim) sa[0] = sa[1] = -INFINITY;
+            if (rr + 8 >= lim) sa[2] = sa[3] = -INFINITY;
+        }
+        bool past = false;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float top = fmaxf(sa[j], sa[j + 2]);
+            past |= top > (l_run[j] == 0.f ? -INFINITY : kSlack);
+        }
+        if (__any_sync(0xffffffffu, past)) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float bm = fmaxf(sa[j], sa[j + 2]);
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, x));
+                if (bm == -INFINITY) continue;   // this head sees no key of the word
+                const float up = l_run[j] == 0.f ? bm : fmaxf(bm, 0.f);
+                if (l_run[j] != 0.f) {
+                    const float sc = fast_exp2(-up);
+                    l_run[j] *= sc;
+#pragma unroll
+                    for (int t = 0; t < 8; ++t) {
+                        oacc[t][j] *= sc;
+                        oacc[t][j + 2] *= sc;
+                    }
+                }
+                mu[j] += up;
+                sa[j] -= up;
+                sa[j + 2] -= up;
+            }
+        }
+        float pr[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float p0 = fast_exp2(sa[j]), p1 = fast_exp2(sa[j + 2]);
+            float ps = p0 + p1;
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) ps += __shfl_xor_sync(0xffffffffu, ps, x);
+            const int g = g0 + 2 * c + j;
+            if (rr == 0 && g < G) lse[g] = mu[j] + fast_log2(ps);
+            l_run[j] += ps;
+            pr[j] = p0;
+            pr[j + 2] = p1;
+        }
+        // P^T (keys x heads) to the B fragment
+        const uint32_t pb0 = movmatrix_t(pack_bf16(pr[0], pr[1]));
+        const uint32_t pb1 = movmatrix_t(pack_bf16(pr[2], pr[3]));
         // ---- O^T [128][8 heads] += V^T P^T
         const uint32_t sv = st + kTileBytes + 2 * c * 128;
         const uint32_t x0 = (rr ^ (2 * c)) << 4, x1 = (rr ^ (2 * c + 1)) << 4;
@@ -463,8 +423,7 @@ __global__ void __launch_bounds__((Cfg<NT>::kWarps * 32), (Cfg<NT>::kOcc))
             for (int x = 0; x < 4; ++x) {
                 const uint32_t a0 = __byte_perm(w0[x], w1[x], 0x5410), a1 = __byte_perm(w0[x], w1[x], 0x7632);
                 const uint32_t a2 = __byte_perm(w2[x], w3[x], 0x5410), a3 = __byte_perm(w2[x], w3[x], 0x7632);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_bf16(oacc[n][4 * m + x], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                mma_bf16(oacc[4 * m + x], a0, a1, a2, a3, pb0, pb1);
             }
         }
     }
@@ -504,7 +463,7 @@ __device__ __forceinline__ void join_head(const float4 *ml, int nw, int G, int l
 // One warp per word.
 template <int JOIN>
 __global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kernel(const __grid_constant__ LaneParams p, int min_words) {
-    constexpr int kWarps = JOIN > 1 ? JOIN : 4;
+    constexpr int kJoinWarps = JOIN > 1 ? JOIN : 4;
     pdl_wait();
     const AttnParams &a = p.a;
     const unsigned B = a.num_req, G = a.group, hq = a.hq;
@@ -561,7 +520,7 @@ __global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kerne
         extern __shared__ float z[];   // [Hq]
         const int c0 = (blockIdx.y - out_ctas) * kMassWords;
         if (c0 >= n) return;
-        for (unsigned h = JOIN > 1 ? warp : threadIdx.x; h < hq; h += JOIN > 1 ? kWarps : 128) {
+        for (unsigned h = JOIN > 1 ? warp : threadIdx.x; h < hq; h += JOIN > 1 ? kJoinWarps : 128) {
             const unsigned kvh = h / G, g = h - kvh * G;
             const float4 *ml = p.ws_ml + (static_cast<size_t>(kvh) * (p.pieces + B) + w0 + r) * G + g;
             float M = -INFINITY, L = 0.f, MO;
@@ -579,7 +538,7 @@ __global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kerne
         }
         __syncthreads();
 #pragma unroll 4
-        for (int i = c0 + warp; i < min(n, c0 + kMassWords); i += kWarps) {
+        for (int i = c0 + warp; i < min(n, c0 + kMassWords); i += kJoinWarps) {
             const float *lse = p.ws_lse + (static_cast<size_t>(r) * a.max_words + i) * hq;
             float s = 0.f;
             for (unsigned h = lane; h < hq; h += 32) s += fast_exp2(lse[h] - z[h]);
@@ -590,30 +549,13 @@ __global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kerne
     }
 }
 
-template <int NT>
-cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
-    using C = Cfg<NT>;
-    auto kern = decode_lane_kernel<NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    const int ctas = (p.pieces * p.a.hkv + C::kWarps - 1) / C::kWarps;
-    kern<<<ctas, C::kWarps * 32, C::kSmem, s>>>(tk, tv, p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return launch_lane_combine(p, kMinWords, s);
-}
-
-template <int NT>
-constexpr int kResident = Cfg<NT>::kOcc * Cfg<NT>::kWarps;
-
 }  // namespace
 
 LanePlan decode_mass_plan(int num_req, int hkv, int max_words, int group, int sms) {
     // one wave of resident warps, but at least kMinWords words each
-    const int per_sm = group <= 8 ? kResident<1> : group <= 16 ? kResident<2> : kResident<4>;
     const int64_t words = static_cast<int64_t>(num_req) * max_words;
     const int64_t most = (words + kMinWords - 1) / kMinWords;
-    const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * per_sm / hkv;
+    const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * kOcc * kWarps / (hkv * head_groups(group));
     LanePlan pl;
     pl.pieces = static_cast<int>(most < resident ? most : resident);
     if (pl.pieces < 1) pl.pieces = 1;
@@ -631,8 +573,13 @@ cudaError_t launch_lane_combine(const LaneParams &p, int min_words, cudaStream_t
 }
 
 cudaError_t launch_decode_mass(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
-    if (p.a.group <= 8) return launch_t<1>(tk, tv, p, s);
-    return p.a.group <= 16 ? launch_t<2>(tk, tv, p, s) : launch_t<4>(tk, tv, p, s);
+    cudaError_t e = cudaFuncSetAttribute(decode_lane_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    const int ctas = (p.pieces * p.a.hkv * head_groups(p.a.group) + kWarps - 1) / kWarps;
+    decode_lane_kernel<<<ctas, kWarps * 32, kSmem, s>>>(tk, tv, p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_lane_combine(p, kMinWords, s);
 }
 
 }  // namespace lazy
