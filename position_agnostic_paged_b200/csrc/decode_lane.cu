@@ -438,21 +438,34 @@ constexpr int kMassWords = 32;   // words per CTA of the mass part
 __device__ __forceinline__ void join_head(const float4 *ml, int nw, int G, int lane, float &M, float &L, float &MO) {
     M = MO = -INFINITY;
     L = 0.f;
-    for (int i = lane; i < nw; i += 32) {
-        const float4 v = ml[static_cast<size_t>(i) * G];
-        M = fmaxf(M, v.x);
-        MO = fmaxf(MO, v.z);
+    // eight loads in flight per lane
+    for (int i0 = 0; i0 < nw; i0 += 256) {
+        float4 v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const int i = i0 + 32 * x + lane;
+            v[x] = i < nw ? ml[static_cast<size_t>(i) * G] : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        }
+        float top = M;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            top = fmaxf(top, v[x].x);
+            MO = fmaxf(MO, v[x].z);
+        }
+        const float mu = top == -INFINITY ? 0.f : top;
+        L *= fast_exp2(M - mu);
+        M = top;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) L += v[x].y * fast_exp2(v[x].x - mu);
     }
+    float all = M;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) {
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+        all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, x));
         MO = fmaxf(MO, __shfl_xor_sync(0xffffffffu, MO, x));
     }
-    const float mu = M == -INFINITY ? 0.f : M;
-    for (int i = lane; i < nw; i += 32) {
-        const float4 v = ml[static_cast<size_t>(i) * G];
-        L += v.y * fast_exp2(v.x - mu);
-    }
+    L *= fast_exp2(M - (all == -INFINITY ? 0.f : all));
+    M = all;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
 }
