@@ -60,7 +60,11 @@ struct Tile {
     float ks[kTileWords], vs[kTileWords];
 };
 
-// NG: query heads per KV head, rounded up to 4, 8, 16 or 32.  QP: parts of the query.
+constexpr int kCtaHeads = 16;
+// CTAs that share a KV head's query heads.
+__host__ __device__ inline int head_groups(int group) { return (group + kCtaHeads - 1) / kCtaHeads; }
+
+// NG: query heads of a CTA, rounded up to 4, 8 or 16.  QP: parts of the query.
 template <int NG, int QP>
 struct Cfg {
     static constexpr int kHT = NG < 8 ? NG : 8, kGroups = NG / kHT;          // heads per softmax thread, groups of 128 threads
@@ -184,8 +188,11 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
 
     const AttnParams &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = a.group, hkv = a.hkv, B = a.num_req;
-    const int kvh = blockIdx.x % hkv, wi = blockIdx.x / hkv;
+    const int hkv = a.hkv, B = a.num_req;
+    // neighbouring CTAs take the head groups of one KV head: its words come from L2 for all but the first
+    const int groups = head_groups(a.group), wi = blockIdx.x / (hkv * groups), line = blockIdx.x - wi * hkv * groups;
+    const int kvh = line / groups, hg = kCtaHeads * (line - kvh * groups);
+    const int G = min(kCtaHeads, a.group - hg), head0 = kvh * a.group + hg;   // heads here; the first of them
     const int base = a.table_indptr[0];
     const int total = a.table_indptr[B] - base;
     if (total <= 0) return;
@@ -215,7 +222,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
     // rows of the operands that hold no head stay zero
     for (int i = threadIdx.x; i < (2 * C::kQBytes + 2 * C::kPBytes) / 16; i += C::kThreads)
         reinterpret_cast<uint4 *>(sm + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
-    if (a.alibi && threadIdx.x < 32) h_slope[threadIdx.x] = threadIdx.x < G ? a.alibi_log2[kvh * G + threadIdx.x] : 0.f;
+    if (a.alibi && threadIdx.x < 32) h_slope[threadIdx.x] = threadIdx.x < G ? a.alibi_log2[head0 + threadIdx.x] : 0.f;
     if (warp == kIssue) {
         tc::tmem_alloc(tmem_slot, C::kCols);
         tc::tmem_relinquish();
@@ -247,12 +254,12 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
         int j = 0, first = 0;     // tiles; the first tile of the request
         bool ok = true;
         auto enter = [&]() {
-            if (lo <= r_beg && r_end - r_beg > a.max_words && kvh == 0 && lane == 0) set_status(a.d_status, LAZY_DSTATUS_BAD_TABLE);
+            if (lo <= r_beg && r_end - r_beg > a.max_words && line == 0 && lane == 0) set_status(a.d_status, LAZY_DSTATUS_BAD_TABLE);
         };
         // a request none of whose words here is visible has no tile to write its partial result
         auto leave = [&]() {
             if (j == first && lane < G)
-                p.ws_ml[((static_cast<size_t>(kvh) * (p.pieces + B)) + wi + r) * G + lane] =
+                p.ws_ml[((static_cast<size_t>(kvh) * (p.pieces + B)) + wi + r) * a.group + hg + lane] =
                     make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
             first = j;
         };
@@ -299,7 +306,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 if (MASS)
                     for (int y = k; y < k + skip; ++y)
                         if (lo + y - r_beg < a.max_words && lane < G)
-                            p.ws_lse[(static_cast<size_t>(r) * a.max_words + lo + y - r_beg) * a.hq + kvh * G + lane] = -INFINITY;
+                            p.ws_lse[(static_cast<size_t>(r) * a.max_words + lo + y - r_beg) * a.hq + head0 + lane] = -INFINITY;
                 k += skip;
                 continue;
             }
@@ -452,7 +459,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 const int h = h0 + (threadIdx.x >> 4);
                 uint2 lo2 = make_uint2(0u, 0u), hi2 = lo2;
                 if (h < G) {
-                    const uint2 *q = reinterpret_cast<const uint2 *>(a.q_raw + (static_cast<size_t>(r) * a.hq + kvh * G + h) * kHeadDim);
+                    const uint2 *q = reinterpret_cast<const uint2 *>(a.q_raw + (static_cast<size_t>(r) * a.hq + head0 + h) * kHeadDim);
                     lo2 = __ldg(q + c);
                     hi2 = __ldg(q + 16 + c);
                 }
@@ -678,7 +685,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 }
                 // HT lanes of the word hold a head each
                 if (blk < n && (slot & (16 / HT - 1)) == 0 && g0 + head < G)
-                    p.ws_lse[(static_cast<size_t>(r) * a.max_words + tl.word + blk) * a.hq + kvh * G + g0 + head] =
+                    p.ws_lse[(static_cast<size_t>(r) * a.max_words + tl.word + blk) * a.hq + head0 + g0 + head] =
                         h_mu[g0 + head] + log2_of(v[0]);
             }
             if (closes) {
@@ -686,7 +693,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 ok = !any_softmax<C::kSoft>(!warp_wait(&odone[buf], (i >> 1) & 1, abort_flag, a.d_status));
                 if (!ok) break;
                 tc::fence_after_sync();
-                const size_t slot_g = (static_cast<size_t>(kvh) * (p.pieces + B) + wi + r) * G;
+                const size_t slot_g = (static_cast<size_t>(kvh) * (p.pieces + B) + wi + r) * a.group + hg;
 #pragma unroll
                 for (int h = 0; h < HT; ++h) {
                     float s = l[h];
@@ -743,7 +750,7 @@ cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const LanePar
     auto kern = decode_q8_kernel<NG, QP, MASS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<p.pieces * p.a.hkv, C::kThreads, C::kSmem, s>>>(tk, tv, p);
+    kern<<<p.pieces * p.a.hkv * head_groups(p.a.group), C::kThreads, C::kSmem, s>>>(tk, tv, p);
     return cudaGetLastError();
 }
 template <int NG>
@@ -752,7 +759,7 @@ cudaError_t launch_g(const CUtensorMap &tk, const CUtensorMap &tv, const LanePar
 }
 template <int QP>
 int occupancy(int group) {
-    return group <= 4 ? Cfg<4, QP>::kOcc : group <= 8 ? Cfg<8, QP>::kOcc : group <= 16 ? Cfg<16, QP>::kOcc : Cfg<32, QP>::kOcc;
+    return group <= 4 ? Cfg<4, QP>::kOcc : group <= 8 ? Cfg<8, QP>::kOcc : Cfg<16, QP>::kOcc;
 }
 
 }  // namespace
@@ -761,7 +768,8 @@ LanePlan decode_q8_plan(int num_req, int hkv, int max_words, int group, bool mas
     // one wave of resident CTAs, at least one tile of words each
     const int64_t words = static_cast<int64_t>(num_req) * max_words;
     const int64_t most = (words + kLineMinWordsQ8 - 1) / kLineMinWordsQ8;
-    const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * (mass ? occupancy<5>(group) : occupancy<3>(group)) / hkv;
+    const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * (mass ? occupancy<5>(group) : occupancy<3>(group)) /
+                             (hkv * head_groups(group));
     LanePlan pl;
     pl.pieces = static_cast<int>(most < resident ? most : resident);
     if (pl.pieces < 1) pl.pieces = 1;
@@ -773,8 +781,7 @@ cudaError_t launch_decode_q8(const CUtensorMap &tk, const CUtensorMap &tv, const
     const int g = p.a.group;
     const cudaError_t e = g <= 4    ? launch_g<4>(tk, tv, p, s)
                           : g <= 8  ? launch_g<8>(tk, tv, p, s)
-                          : g <= 16 ? launch_g<16>(tk, tv, p, s)
-                                    : launch_g<32>(tk, tv, p, s);
+                                    : launch_g<16>(tk, tv, p, s);
     return e == cudaSuccess ? launch_lane_combine(p, kLineMinWordsQ8, s) : e;
 }
 
