@@ -225,15 +225,28 @@ int64_t prefill_units(const lazy_attn_cfg *cfg, int num_req, int max_q) {
     return (rows + kPrefillRows - 1) / kPrefillRows * cfg->num_kv_heads * num_req;
 }
 
+// A prefill whose query rows per KV head and request are few enough for the decode's kernel.
+bool few_rows(const lazy_attn_cfg *cfg, int max_q) {
+    return static_cast<int64_t>(max_q) * (cfg->num_q_heads / cfg->num_kv_heads) <= kFewRows;
+}
+
 // Workspace of the streaming decode: partial outputs, their (max, sum, reference), and with block
 // mass one log2 weight sum per (request, word, query head).
-size_t lane_ws(const lazy_attn_cfg *cfg, int num_req, int max_words, bool q8, bool mass, LanePlan &pl) {
-    const int G = cfg->num_q_heads / cfg->num_kv_heads;
-    pl = q8 ? decode_q8_plan(num_req, cfg->num_kv_heads, max_words, G, mass, sm_count())
-            : decode_mass_plan(num_req, cfg->num_kv_heads, max_words, G, sm_count());
-    size_t n = static_cast<size_t>(pl.slots) * G * (128 * sizeof(float) + sizeof(float4));
+size_t lane_ws(const lazy_attn_cfg *cfg, int num_req, int max_q, int max_words, bool q8, bool mass, LanePlan &pl) {
+    const int rows = max_q * (cfg->num_q_heads / cfg->num_kv_heads);
+    pl = q8 ? decode_q8_plan(num_req, cfg->num_kv_heads, max_words, rows, mass, sm_count())
+            : decode_mass_plan(num_req, cfg->num_kv_heads, max_words, rows, sm_count());
+    size_t n = static_cast<size_t>(pl.slots) * rows * (128 * sizeof(float) + sizeof(float4));
     if (mass) n += static_cast<size_t>(num_req) * max_words * cfg->num_q_heads * sizeof(float);
     return n;
+}
+
+void place_lane_ws(LaneParams &p, const LanePlan &pl, void *workspace) {
+    const size_t rows = static_cast<size_t>(pl.slots) * p.rows;
+    p.a.ws_acc = static_cast<float *>(workspace);
+    p.ws_ml = reinterpret_cast<float4 *>(p.a.ws_acc + rows * 128);
+    p.ws_lse = reinterpret_cast<float *>(p.ws_ml + rows);
+    p.pieces = pl.pieces;
 }
 
 int lane_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_pos, int num_req,
@@ -254,19 +267,17 @@ int lane_impl(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_
     // the joining grid is (requests, heads, and with block mass 32 words of a request each)
     if (num_req > (1 << 24) || (mass && max_words > (1 << 20))) return LAZY_ERANGE;
     LanePlan pl;
-    const size_t need = lane_ws(cfg, num_req, max_words, q8, mass != nullptr, pl);
+    const size_t need = lane_ws(cfg, num_req, 1, max_words, q8, mass != nullptr, pl);
     if (!workspace || ws_bytes < need) return LAZY_EWORKSPACE;
     if (!aligned(workspace, 16)) return LAZY_EINVAL;
     p.a.q_raw = q_raw;
     p.a.q_pos = q_pos;
-    const size_t rows = static_cast<size_t>(pl.slots) * p.a.group;
-    p.a.ws_acc = static_cast<float *>(workspace);
-    p.ws_ml = reinterpret_cast<float4 *>(p.a.ws_acc + rows * 128);
-    p.ws_lse = reinterpret_cast<float *>(p.ws_ml + rows);
+    p.a.cu_q = nullptr;
+    p.rows = p.a.group;
+    place_lane_ws(p, pl, workspace);
     p.mass = mass;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    p.pieces = pl.pieces;
     CUtensorMap tk, tv;
     const int64_t pool_rows = static_cast<int64_t>(num_blocks) * p.a.hkv * 16;
     if (q8 ? !make_codes_map(&tk, k, pool_rows) || !make_codes_map(&tv, v, pool_rows)
@@ -498,7 +509,7 @@ int lazy_kv_write_q8(const lazy_attn_cfg *cfg, const uint16_t *k_raw, const uint
 size_t lazy_decode_q8_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, int max_words, int with_mass) {
     if (check_cfg(cfg) != LAZY_OK || num_req <= 0 || max_words <= 0) return 0;
     LanePlan pl;
-    return lane_ws(cfg, num_req, max_words, true, with_mass != 0, pl);
+    return lane_ws(cfg, num_req, 1, max_words, true, with_mass != 0, pl);
 }
 
 int lazy_decode_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_pos, int num_req,
@@ -517,7 +528,7 @@ int lazy_decode_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const i
 size_t lazy_decode_mass_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, int max_words) {
     if (check_cfg(cfg) != LAZY_OK || num_req <= 0 || max_words <= 0) return 0;
     LanePlan pl;
-    return lane_ws(cfg, num_req, max_words, false, true, pl);
+    return lane_ws(cfg, num_req, 1, max_words, false, true, pl);
 }
 
 int lazy_decode_attn_mass(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *q_pos, int num_req,
@@ -537,7 +548,9 @@ size_t lazy_prefill_q8_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, in
     (void)total_q;
     (void)total_words;
     if (check_cfg(cfg) != LAZY_OK || num_req <= 0 || max_q <= 0 || max_words < 0) return 0;
-    return q8_prefill_ws_bytes(prefill_units(cfg, num_req, max_q), max_words, sm_count());
+    LanePlan pl;
+    return few_rows(cfg, max_q) ? lane_ws(cfg, num_req, max_q, max_words, true, false, pl)
+                                : q8_prefill_ws_bytes(prefill_units(cfg, num_req, max_q), max_words, sm_count());
 }
 
 int lazy_prefill_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *cu_q,
@@ -566,12 +579,29 @@ int lazy_prefill_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const 
     if (static_cast<int64_t>(max_q) * p.a.group > (int64_t(1) << 30) || units > (int64_t(1) << 22) || num_req > 65535)
         return LAZY_ERANGE;
     const int sms = sm_count();
-    if (!workspace || ws_bytes < q8_prefill_ws_bytes(units, max_words, sms)) return LAZY_EWORKSPACE;
+    const bool few = few_rows(cfg, max_q);
+    LanePlan pl;
+    const size_t need = few ? lane_ws(cfg, num_req, max_q, max_words, true, false, pl)
+                            : q8_prefill_ws_bytes(units, max_words, sms);
+    if (!workspace || ws_bytes < need) return LAZY_EWORKSPACE;
     if (!aligned(workspace, 16)) return LAZY_EINVAL;
     p.a.q_raw = q_raw;
     p.a.cu_q = cu_q;
     p.a.q_pos0 = q_pos0;
     p.a.max_q = max_q;
+    if (few) {
+        LaneParams f;
+        f.a = p.a;
+        f.rows = max_q * p.a.group;
+        place_lane_ws(f, pl, workspace);
+        f.mass = nullptr;
+        f.k_scale = pool->k_scale;
+        f.v_scale = pool->v_scale;
+        CUtensorMap tk, tv;
+        const int64_t rows = static_cast<int64_t>(pool->num_blocks) * p.a.hkv * 16;
+        if (!make_codes_map(&tk, pool->k_codes, rows) || !make_codes_map(&tv, pool->v_codes, rows)) return LAZY_ECUDA;
+        return launch_rc(launch_decode_q8(tk, tv, f, static_cast<cudaStream_t>(stream)));
+    }
     p.a.pf_mtiles = static_cast<int>((static_cast<int64_t>(max_q) * p.a.group + kPrefillRows - 1) / kPrefillRows);
     p.k_codes = pool->k_codes;
     p.v_codes = pool->v_codes;

@@ -470,7 +470,7 @@ __device__ __forceinline__ void join_head(const float4 *ml, int nw, int G, int l
     for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
 }
 
-// Grid (request, y).  y < heads / heads per CTA: out[r][h] from the request's partials, four head dims per lane; one
+// Grid (request, y).  y < rows / rows per CTA: a row of the output from the request's partials, four head dims per lane; one
 // head per warp, or (JOIN warps, where a request has many partials) one per CTA with every JOIN-th partial
 // per warp.  y behind them: the word accumulators, mass[w] += sum_h 2^(lse[w][h] - z_h), z_h = M_h + log2 L_h.
 // One warp per word.
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kerne
     constexpr int kJoinWarps = JOIN > 1 ? JOIN : 4;
     pdl_wait();
     const AttnParams &a = p.a;
-    const unsigned B = a.num_req, G = a.group, hq = a.hq;
+    const unsigned B = a.num_req, G = p.rows, hq = p.rows * a.hkv;   // rows per KV head, and of all
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned r = blockIdx.x, out_ctas = JOIN > 1 ? hq : (hq + 3) / 4;
     const int base = a.table_indptr[0];
@@ -493,6 +493,13 @@ __global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kerne
         const unsigned h = JOIN > 1 ? blockIdx.y : blockIdx.y * 4 + warp;
         if (h >= hq) return;
         const unsigned kvh = h / G, g = h - kvh * G;
+        size_t row = static_cast<size_t>(r) * hq + h;
+        if (a.cu_q) {
+            // a request's few tokens: row g is (token, head of the group)
+            const int q0 = a.cu_q[r], tokens = min(a.cu_q[r + 1] - q0, a.max_q), tok = g / a.group;
+            if (tok >= tokens) return;
+            row = static_cast<size_t>(q0 + tok) * a.hq + kvh * a.group + g - tok * a.group;
+        }
         const size_t s0 = static_cast<size_t>(kvh) * (p.pieces + B) + w0 + r;
         const float4 *ml = p.ws_ml + s0 * G + g;
         float M, L, MO;
@@ -527,7 +534,7 @@ __global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kerne
         }
         // A is relative to 2^MO, L to 2^M (fminf only keeps an overflow of the factor from making 0 * inf)
         const float f = fast_exp2(fminf(mou - mu, 126.f)), inv = L > 0.f || L != L ? 1.f / L : 0.f;
-        reinterpret_cast<uint2 *>(a.out + (static_cast<size_t>(r) * hq + h) * kHeadDim)[lane] =
+        reinterpret_cast<uint2 *>(a.out + row * kHeadDim)[lane] =
             make_uint2(pack_bf16(A.x * inv * f, A.y * inv * f), pack_bf16(A.z * inv * f, A.w * inv * f));
     } else {
         extern __shared__ float z[];   // [Hq]
@@ -577,12 +584,13 @@ LanePlan decode_mass_plan(int num_req, int hkv, int max_words, int group, int sm
 }
 
 cudaError_t launch_lane_combine(const LaneParams &p, int min_words, cudaStream_t s) {
+    const int rows = p.rows * p.a.hkv;
     const int chunks = p.mass ? (p.a.max_words + kMassWords - 1) / kMassWords : 0;
     const size_t smem = p.mass ? p.a.hq * sizeof(float) : 0;
     // a request has about pieces / requests partials
     if (p.pieces > 8 * p.a.num_req)
-        return launch_dependent(lane_combine_kernel<8>, dim3(p.a.num_req, p.a.hq + chunks), 256, smem, s, p, min_words);
-    return launch_dependent(lane_combine_kernel<1>, dim3(p.a.num_req, (p.a.hq + 3) / 4 + chunks), 128, smem, s, p, min_words);
+        return launch_dependent(lane_combine_kernel<8>, dim3(p.a.num_req, rows + chunks), 256, smem, s, p, min_words);
+    return launch_dependent(lane_combine_kernel<1>, dim3(p.a.num_req, (rows + 3) / 4 + chunks), 128, smem, s, p, min_words);
 }
 
 cudaError_t launch_decode_mass(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {

@@ -55,14 +55,15 @@ constexpr int kPP = 4;                // parts of the weights
 // One tile of the walk; n = 0 ends it.
 struct Tile {
     int n, off, req, word;            // words, offset, request, index of the first word in the request
+    int rows, qpos;                   // query rows of the request here; position of its first query
     int lim[kTileWords];              // visible slots of each word
     int pos[kTileWords];              // position of its slot 0
     float ks[kTileWords], vs[kTileWords];
 };
 
-constexpr int kCtaHeads = 16;
-// CTAs that share a KV head's query heads.
-__host__ __device__ inline int head_groups(int group) { return (group + kCtaHeads - 1) / kCtaHeads; }
+constexpr int kCtaRows = 16;         // query rows of a CTA
+// CTAs that share a KV head's query rows.
+__host__ __device__ inline int row_groups(int rows) { return (rows + kCtaRows - 1) / kCtaRows; }
 
 // NG: query heads of a CTA, rounded up to 4, 8 or 16.  QP: parts of the query.
 template <int NG, int QP>
@@ -86,9 +87,9 @@ struct Cfg {
 // small state, from kOffState
 constexpr int kOffTile = 0;                                      // records
 constexpr int kOffBars = kOffTile + kRecords * static_cast<int>(sizeof(Tile));
-constexpr int kOffHead = kOffBars + 256;                         // mu, dm, dv, step of O, hm of two Q buffers, slope: [32] each
-constexpr int kOffRed = kOffHead + 7 * 128;                      // [2][4][32] reductions
-constexpr int kOffAngle = kOffRed + 1024;                        // [64] float2
+constexpr int kOffHead = kOffBars + 256;                         // mu, dm, dv, step of O, hm of two Q buffers, slope, token: [32] each
+constexpr int kOffRed = kOffHead + 8 * 128;                      // [2][4][32] reductions
+constexpr int kOffAngle = kOffRed + 1024;                        // [64] float2, or [64] double
 constexpr int kOffMisc = kOffAngle + 512;
 static_assert(kOffMisc + 16 <= 4096, "state");
 
@@ -165,7 +166,9 @@ __device__ __forceinline__ int words_per_piece(int total, int pieces) {
     return max(kLineMinWordsQ8, (total + pieces - 1) / pieces);
 }
 
-template <int NG, int QP, bool MASS>
+// CHUNK: a row is a (token, head of the group) pair of a request's few tokens, with a position and visible keys
+// of its own, else one of the request's one token's heads.
+template <int NG, int QP, bool MASS, bool CHUNK>
 __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) decode_q8_kernel(const __grid_constant__ CUtensorMap tmK,
                                                                                   const __grid_constant__ CUtensorMap tmV,
                                                                                   const __grid_constant__ LaneParams p) {
@@ -180,19 +183,25 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
     uint64_t *full = bars, *empty = bars + 4, *ifull = bars + 8, *iempty = bars + 12, *qready = bars + 16, *sfull = bars + 18,
              *pready = bars + 20, *odone = bars + 22, *drain = bars + 24;
     float *h_mu = reinterpret_cast<float *>(state + kOffHead), *h_dm = h_mu + 32, *h_dv = h_mu + 64, *h_step = h_mu + 96,
-          *h_hm = h_mu + 128, *h_slope = h_mu + 192;
+          *h_hm = h_mu + 128, *h_slope = h_mu + 192, *h_tok = h_mu + 224;
     float(*red)[32] = reinterpret_cast<float(*)[32]>(state + kOffRed), (*red_o)[32] = red + 4;
     float2 *angle = reinterpret_cast<float2 *>(state + kOffAngle);
+    double *theta = reinterpret_cast<double *>(state + kOffAngle);   // CHUNK
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(state + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(state + kOffMisc + 4);
 
     const AttnParams &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int hkv = a.hkv, B = a.num_req;
-    // neighbouring CTAs take the head groups of one KV head: its words come from L2 for all but the first
-    const int groups = head_groups(a.group), wi = blockIdx.x / (hkv * groups), line = blockIdx.x - wi * hkv * groups;
-    const int kvh = line / groups, hg = kCtaHeads * (line - kvh * groups);
-    const int G = min(kCtaHeads, a.group - hg), head0 = kvh * a.group + hg;   // heads here; the first of them
+    // neighbouring CTAs take the row groups of one KV head: its words come from L2 for all but the first
+    const int groups = row_groups(p.rows), wi = blockIdx.x / (hkv * groups), line = blockIdx.x - wi * hkv * groups;
+    const int kvh = line / groups, hg = kCtaRows * (line - kvh * groups);   // hg: the first row here
+    // rows of request r here
+    auto rows_of = [&](int r) {
+        if (!CHUNK) return min(kCtaRows, a.group - hg);
+        const int tokens = max(0, min(a.cu_q[r + 1] - a.cu_q[r], a.max_q));
+        return max(0, min(kCtaRows, tokens * a.group - hg));
+    };
     const int base = a.table_indptr[0];
     const int total = a.table_indptr[B] - base;
     if (total <= 0) return;
@@ -222,7 +231,13 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
     // rows of the operands that hold no head stay zero
     for (int i = threadIdx.x; i < (2 * C::kQBytes + 2 * C::kPBytes) / 16; i += C::kThreads)
         reinterpret_cast<uint4 *>(sm + C::kOffQ)[i] = make_uint4(0, 0, 0, 0);
-    if (a.alibi && threadIdx.x < 32) h_slope[threadIdx.x] = threadIdx.x < G ? a.alibi_log2[head0 + threadIdx.x] : 0.f;
+    if (threadIdx.x < 32) {
+        const int row = hg + threadIdx.x, tok = CHUNK ? row / a.group : 0;
+        if (a.alibi) h_slope[threadIdx.x] = row < p.rows ? a.alibi_log2[kvh * a.group + row - tok * a.group] : 0.f;
+        if (CHUNK) h_tok[threadIdx.x] = static_cast<float>(tok);
+    }
+    if (CHUNK)
+        for (int i = threadIdx.x; i < kHalfDim; i += C::kThreads) theta[i] = a.rope.theta[i];
     if (warp == kIssue) {
         tc::tmem_alloc(tmem_slot, C::kCols);
         tc::tmem_relinquish();
@@ -250,16 +265,19 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             r += step * k;
             hi = min(hi, r + step);
         }
-        int r_beg = a.table_indptr[r] - base, r_end = a.table_indptr[r + 1] - base, qpos = a.q_pos[r];
+        int r_beg = a.table_indptr[r] - base, r_end = a.table_indptr[r + 1] - base, rows, qpos, last;   // last: position of the last query
         int j = 0, first = 0;     // tiles; the first tile of the request
         bool ok = true;
         auto enter = [&]() {
+            rows = rows_of(r);
+            qpos = CHUNK ? a.q_pos0[r] : a.q_pos[r];
+            last = !CHUNK ? qpos : rows > 0 ? qpos + (hg + rows - 1) / a.group : -1;
             if (lo <= r_beg && r_end - r_beg > a.max_words && line == 0 && lane == 0) set_status(a.d_status, LAZY_DSTATUS_BAD_TABLE);
         };
         // a request none of whose words here is visible has no tile to write its partial result
         auto leave = [&]() {
-            if (j == first && lane < G)
-                p.ws_ml[((static_cast<size_t>(kvh) * (p.pieces + B)) + wi + r) * a.group + hg + lane] =
+            if (j == first && lane < rows)
+                p.ws_ml[((static_cast<size_t>(kvh) * (p.pieces + B)) + wi + r) * p.rows + hg + lane] =
                     make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
             first = j;
         };
@@ -275,7 +293,6 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                     r_beg = r_end;
                     r_end = a.table_indptr[r + 1] - base;
                 } while (lo + k >= r_end);
-                qpos = a.q_pos[r];
                 enter();
             }
             if (k - b0 + kTileWords > 32 && b0 + 32 < cnt) {
@@ -298,15 +315,15 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             const int i = k - b0, x = b0 + lane;             // lane `lane` holds word x
             const int pos = word_offset(wl) + meta_j0(ml);
             const bool mine = x >= k && x < cnt && lo + x < r_end;
-            const int lim = mine && lo + x - r_beg < a.max_words ? min(meta_valid(ml), qpos - pos + 1) : 0;
+            const int lim = mine && lo + x - r_beg < a.max_words ? min(meta_valid(ml), last - pos + 1) : 0;
             const uint32_t seen = __ballot_sync(0xffffffffu, lim > 0);
             const int here = __popc(__ballot_sync(0xffffffffu, mine));      // words of the request from k on, in this batch
             if (!((seen >> i) & 1u)) {
                 const int skip = min(here, seen ? __ffs(seen) - 1 - i : 32);
                 if (MASS)
                     for (int y = k; y < k + skip; ++y)
-                        if (lo + y - r_beg < a.max_words && lane < G)
-                            p.ws_lse[(static_cast<size_t>(r) * a.max_words + lo + y - r_beg) * a.hq + head0 + lane] = -INFINITY;
+                        if (lo + y - r_beg < a.max_words && lane < rows)
+                            p.ws_lse[(static_cast<size_t>(r) * a.max_words + lo + y - r_beg) * a.hq + kvh * a.group + hg + lane] = -INFINITY;
                 k += skip;
                 continue;
             }
@@ -331,6 +348,8 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 t.n = n;
                 t.off = off;
                 t.req = r;
+                t.rows = rows;
+                t.qpos = qpos;
                 t.word = lo + k - r_beg;
             }
             __syncwarp();
@@ -444,22 +463,26 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
         int qbuf = 1, cur_req = -1, cur_off = 0;   // of the Q operand made last
         // the query of tile `tl` as e4m3 parts, if it is not the one made last
         auto query = [&](const Tile &tl) {
-            const int off = tl.off, r = tl.req;
+            const int off = tl.off, r = tl.req, rows = tl.rows;
             if (r == cur_req && (off == cur_off || a.alibi)) return;
             qbuf ^= 1;
             cur_req = r;
             cur_off = off;
-            if (threadIdx.x < kHalfDim)
-                rope_cos_sin(a.alibi ? 0 : a.q_pos[r] - off, a.rope.theta[threadIdx.x], angle[threadIdx.x].x, angle[threadIdx.x].y);
-            sync_softmax<C::kSoft>();
+            if (!CHUNK) {
+                if (threadIdx.x < kHalfDim)
+                    rope_cos_sin(a.alibi ? 0 : tl.qpos - off, a.rope.theta[threadIdx.x], angle[threadIdx.x].x, angle[threadIdx.x].y);
+                sync_softmax<C::kSoft>();
+            }
             uint8_t *qd = sm + C::kOffQ + qbuf * C::kQBytes;
-            // 16 threads per head: dims 4c .. + 3 and 64 above
+            // 16 threads per row: dims 4c .. + 3 and 64 above
             const int c = threadIdx.x & 15;
-            for (int h0 = 0; h0 < G; h0 += C::kSoft / 16) {
+            for (int h0 = 0; h0 < rows; h0 += C::kSoft / 16) {
                 const int h = h0 + (threadIdx.x >> 4);
+                const int tok = CHUNK ? (hg + h) / a.group : 0, head = kvh * a.group + hg + h - tok * a.group;
                 uint2 lo2 = make_uint2(0u, 0u), hi2 = lo2;
-                if (h < G) {
-                    const uint2 *q = reinterpret_cast<const uint2 *>(a.q_raw + (static_cast<size_t>(r) * a.hq + head0 + h) * kHeadDim);
+                if (h < rows) {
+                    const uint2 *q = reinterpret_cast<const uint2 *>(
+                        a.q_raw + (static_cast<size_t>(CHUNK ? a.cu_q[r] + tok : r) * a.hq + head) * kHeadDim);
                     lo2 = __ldg(q + c);
                     hi2 = __ldg(q + 16 + c);
                 }
@@ -477,12 +500,16 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 float x[4], y[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const float2 z = angle[4 * c + u];
+                    float2 z;
+                    if (CHUNK)
+                        rope_cos_sin(a.alibi ? 0 : tl.qpos + tok - off, theta[4 * c + u], z.x, z.y);
+                    else
+                        z = angle[4 * c + u];
                     const float xa = av[u] * dn, xb = bv[u] * dn;
                     x[u] = xa * z.x - xb * z.y;
                     y[u] = xb * z.x + xa * z.y;
                 }
-                if (h < G) {
+                if (h < rows) {
 #pragma unroll
                     for (int part = 0; part < QP; ++part) {
                         const int row = part * NG + h;
@@ -492,7 +519,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                     if (c == 0) h_hm[32 * qbuf + h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.scale_log2 * 0x1p-7f);
                 }
             }
-            if (threadIdx.x >= G && threadIdx.x < 32) h_hm[32 * qbuf + threadIdx.x] = 0.f;
+            if (threadIdx.x >= rows && threadIdx.x < 32) h_hm[32 * qbuf + threadIdx.x] = 0.f;
             fence_proxy_async_smem();
             sync_softmax<C::kSoft>();   // hm and the angles' next use
         };
@@ -516,13 +543,15 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
         bool opens = true;
         for (int i = 0; ok && n > 0; ++i) {
             const Tile &tl = tiles[i % kRecords], &nx = tiles[(i + 1) % kRecords];
-            const int buf = i & 1, my_q = qbuf, r = tl.req;
+            const int buf = i & 1, my_q = qbuf, r = tl.req, rows = tl.rows;
             // ---- scores
             const int blk = t >> 4, slot = t & 15;
             const int lim = tl.lim[blk];
             const bool vis = slot < lim;
+            // the first row here, from g0 on, that sees the key
+            const int seer = CHUNK ? min(max(tl.pos[blk] + slot - tl.qpos, 0), kFewRows) * a.group - hg - g0 : 0;
             const float ks = tl.ks[blk], vs = tl.vs[blk], lv = log2_of(vs);
-            const float dpos = a.alibi ? static_cast<float>(tl.pos[blk] + slot - a.q_pos[r]) : 0.f;
+            const float dpos = a.alibi ? static_cast<float>(tl.pos[blk] + slot - tl.qpos) : 0.f;
             const bool got = warp_wait(&sfull[buf], (i >> 1) & 1, abort_flag, a.d_status) &&
                              warp_wait(&ifull[(i + 1) % kRecords], ((i + 1) / kRecords) & 1, abort_flag, a.d_status);
             tc::fence_after_sync();
@@ -544,8 +573,8 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                         for (int part = QP - 2; part >= 0; --part)
                             s = fmaf(s, 1.f / kPartStep, __uint_as_float(sv[part][h + y]));
                         x[h + y] = fmaf(s, ks * hm4[y], -mu4[y]);
-                        if (a.alibi) x[h + y] = fmaf(h_slope[g0 + h + y], dpos, x[h + y]);
-                        if (!vis) x[h + y] = -INFINITY;
+                        if (a.alibi) x[h + y] = fmaf(h_slope[g0 + h + y], CHUNK ? dpos - h_tok[g0 + h + y] : dpos, x[h + y]);
+                        if (!vis || (CHUNK && h + y < seer)) x[h + y] = -INFINITY;
                     }
                 }
             }
@@ -642,7 +671,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 const float dv4[4] = {dv.x, dv.y, dv.z, dv.w};
                 float w[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) w[y] = vis ? x[h + y] * (vs * dv4[y] * 0x1p20f) : 0.f;
+                for (int y = 0; y < 4; ++y) w[y] = vis && !(CHUNK && h + y < seer) ? x[h + y] * (vs * dv4[y] * 0x1p20f) : 0.f;
 #pragma unroll
                 for (int part = 0; part < kPP; ++part) {
                     const uint32_t codes = take_part(w);
@@ -684,8 +713,8 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                     }
                 }
                 // HT lanes of the word hold a head each
-                if (blk < n && (slot & (16 / HT - 1)) == 0 && g0 + head < G)
-                    p.ws_lse[(static_cast<size_t>(r) * a.max_words + tl.word + blk) * a.hq + head0 + g0 + head] =
+                if (blk < n && (slot & (16 / HT - 1)) == 0 && g0 + head < rows)
+                    p.ws_lse[(static_cast<size_t>(r) * a.max_words + tl.word + blk) * a.hq + kvh * a.group + hg + g0 + head] =
                         h_mu[g0 + head] + log2_of(v[0]);
             }
             if (closes) {
@@ -693,7 +722,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 ok = !any_softmax<C::kSoft>(!warp_wait(&odone[buf], (i >> 1) & 1, abort_flag, a.d_status));
                 if (!ok) break;
                 tc::fence_after_sync();
-                const size_t slot_g = (static_cast<size_t>(kvh) * (p.pieces + B) + wi + r) * a.group + hg;
+                const size_t slot_g = (static_cast<size_t>(kvh) * (p.pieces + B) + wi + r) * p.rows + hg;
 #pragma unroll
                 for (int h = 0; h < HT; ++h) {
                     float s = l[h];
@@ -702,7 +731,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                     if (lane == 0) red[wq][g0 + h] = s;
                 }
                 sync_softmax<C::kSoft>();
-                if (threadIdx.x < G) {
+                if (threadIdx.x < rows) {
                     const int h = threadIdx.x;
                     const float s = (red[0][h] + red[1][h]) + (red[2][h] + red[3][h]);
                     const bool none = h_dm[h] == INFINITY && s == s;
@@ -717,7 +746,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                     tc::wait_ld();
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
-                        if (g0 + h + y < G) {
+                        if (g0 + h + y < rows) {
                             float v = __uint_as_float(o[kPP - 1][y]);
 #pragma unroll
                             for (int part = kPP - 2; part >= 0; --part) v = fmaf(v, 1.f / kPartStep, __uint_as_float(o[part][y]));
@@ -744,32 +773,33 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
     }
 }
 
-template <int NG, int QP, bool MASS>
+template <int NG, int QP, bool MASS, bool CHUNK>
 cudaError_t launch_t(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
     using C = Cfg<NG, QP>;
-    auto kern = decode_q8_kernel<NG, QP, MASS>;
+    auto kern = decode_q8_kernel<NG, QP, MASS, CHUNK>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<p.pieces * p.a.hkv * head_groups(p.a.group), C::kThreads, C::kSmem, s>>>(tk, tv, p);
+    kern<<<p.pieces * p.a.hkv * row_groups(p.rows), C::kThreads, C::kSmem, s>>>(tk, tv, p);
     return cudaGetLastError();
 }
 template <int NG>
 cudaError_t launch_g(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
-    return p.mass ? launch_t<NG, 5, true>(tk, tv, p, s) : launch_t<NG, 3, false>(tk, tv, p, s);
+    if (p.a.cu_q) return launch_t<NG, 3, false, true>(tk, tv, p, s);
+    return p.mass ? launch_t<NG, 5, true, false>(tk, tv, p, s) : launch_t<NG, 3, false, false>(tk, tv, p, s);
 }
 template <int QP>
-int occupancy(int group) {
-    return group <= 4 ? Cfg<4, QP>::kOcc : group <= 8 ? Cfg<8, QP>::kOcc : Cfg<16, QP>::kOcc;
+int occupancy(int rows) {
+    return rows <= 4 ? Cfg<4, QP>::kOcc : rows <= 8 ? Cfg<8, QP>::kOcc : Cfg<16, QP>::kOcc;
 }
 
 }  // namespace
 
-LanePlan decode_q8_plan(int num_req, int hkv, int max_words, int group, bool mass, int sms) {
+LanePlan decode_q8_plan(int num_req, int hkv, int max_words, int rows, bool mass, int sms) {
     // one wave of resident CTAs, at least one tile of words each
     const int64_t words = static_cast<int64_t>(num_req) * max_words;
     const int64_t most = (words + kLineMinWordsQ8 - 1) / kLineMinWordsQ8;
-    const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * (mass ? occupancy<5>(group) : occupancy<3>(group)) /
-                             (hkv * head_groups(group));
+    const int64_t resident = static_cast<int64_t>(sms > 0 ? sms : 1) * (mass ? occupancy<5>(rows) : occupancy<3>(rows)) /
+                             (hkv * row_groups(rows));
     LanePlan pl;
     pl.pieces = static_cast<int>(most < resident ? most : resident);
     if (pl.pieces < 1) pl.pieces = 1;
@@ -778,10 +808,9 @@ LanePlan decode_q8_plan(int num_req, int hkv, int max_words, int group, bool mas
 }
 
 cudaError_t launch_decode_q8(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s) {
-    const int g = p.a.group;
-    const cudaError_t e = g <= 4    ? launch_g<4>(tk, tv, p, s)
-                          : g <= 8  ? launch_g<8>(tk, tv, p, s)
-                                    : launch_g<16>(tk, tv, p, s);
+    const cudaError_t e = p.rows <= 4   ? launch_g<4>(tk, tv, p, s)
+                          : p.rows <= 8 ? launch_g<8>(tk, tv, p, s)
+                                        : launch_g<16>(tk, tv, p, s);
     return e == cudaSuccess ? launch_lane_combine(p, kLineMinWordsQ8, s) : e;
 }
 

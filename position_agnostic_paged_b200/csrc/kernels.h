@@ -139,14 +139,15 @@ inline size_t q8_write_ws_bytes(int num_blocks) {
 cudaError_t launch_kv_write_q8(const Q8WriteParams &p, cudaStream_t s);
 
 // Streaming decode, over the 8-bit pool (decode_q8.cu) or over the bf16 pool with block mass (decode_lane.cu).
-// a.ws_acc: partial outputs [slot][G][128]; ws_ml: per partial (running max, sum, output
-// reference, 0) [slot][G]; ws_lse: log2 of each word's weight sum [num_req][max_words][Hq].
+// a.ws_acc: partial outputs [slot][rows][128]; ws_ml: per partial (running max, sum, output
+// reference, 0) [slot][rows]; ws_lse: log2 of each word's weight sum [num_req][max_words][Hq].
 struct LaneParams {
     AttnParams a;
     const float *k_scale, *v_scale;  // null for bf16 pools
     float4 *ws_ml;
     float *ws_lse;
     float *mass;                     // null: no accumulators
+    int rows;                        // query rows of a request per KV head: group, or with a.cu_q max_q x group
     int pieces;                      // of one KV head's words
 };
 struct LanePlan {
@@ -156,8 +157,9 @@ struct LanePlan {
 // Joins the partials of every request; min_words: the least words of a piece of the line.
 cudaError_t launch_lane_combine(const LaneParams &p, int min_words, cudaStream_t s);
 // tk, tv: the codes as rows of 128 bytes, one box = one block of one head; a piece per CTA.
-constexpr int kLineMinWordsQ8 = 8;
-LanePlan decode_q8_plan(int num_req, int hkv, int max_words, int group, bool mass, int sms);
+// With a.cu_q it computes a prefill of up to kFewRows query rows per KV head and request.
+constexpr int kLineMinWordsQ8 = 8, kFewRows = 32;
+LanePlan decode_q8_plan(int num_req, int hkv, int max_words, int rows, bool mass, int sms);
 cudaError_t launch_decode_q8(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s);
 // tk, tv: the bf16 pools as rows of 128 elements, one box = half of one block of one head; a piece per warp.
 LanePlan decode_mass_plan(int num_req, int hkv, int max_words, int group, int sms);
