@@ -264,6 +264,15 @@ def test_prefill_few_rows(hq, hkv, most, kind):
     assert c.dev["status"].item() == 0
 
 
+@pytest.mark.parametrize("most", [2, 5])
+def test_prefill_few_rows_many_requests(most):
+    """More units than two per SM: five tokens of four heads take the kernel of long prompts."""
+    docs, reqs = _requests(7)
+    reqs = [(s, max(0, p - most + 1), most) for s, p, _ in reqs] * 12
+    c = PoolCase(la.Cfg(16, 4), docs, reqs, seed=most).to()
+    check(c.prefill(), *c.reference(**PREFILL_U)[:2], f"prefill of {most} tokens, {len(reqs)} requests")
+
+
 def test_prefill_few_rows_one_long_request():
     """Many partial results of one request; a document met again at another offset."""
     c = PoolCase(la.Cfg(8, 2), [2000, 333], [([(1, 0), (0, 333), (1, 2400), (1, 2733)], 3060, 6)], seed=3).to()
