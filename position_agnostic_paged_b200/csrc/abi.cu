@@ -225,14 +225,11 @@ int64_t prefill_units(const lazy_attn_cfg *cfg, int num_req, int max_q) {
     return (rows + kPrefillRows - 1) / kPrefillRows * cfg->num_kv_heads * num_req;
 }
 
-// A prefill whose query rows per KV head and request are few enough for the decode's kernel, which takes 16 of
-// them per CTA where the prefill's takes 256 (8 requests of 126 words, 32 heads on 8: 4 tokens 29 us against
-// 47, 5 to 8 tokens 41 against 46, 12 tokens 50 against 47).  Two CTAs' worth of rows pay only while the
-// work is too little to fill the SMs for long (64 requests of 261 words: 4 tokens 221 us against 393, 8 tokens 424 against 394).
-bool few_rows(const lazy_attn_cfg *cfg, int num_req, int max_q) {
-    const int64_t rows = static_cast<int64_t>(max_q) * (cfg->num_q_heads / cfg->num_kv_heads);
-    return rows <= kFewRows / 2 ||
-           (rows <= kFewRows && static_cast<int64_t>(num_req) * cfg->num_kv_heads <= 2 * sm_count());
+// A prefill whose query rows per KV head and request fit a CTA of the decode's kernel (8 requests of 126 words,
+// 32 heads on 8: 4 tokens 29 us, the prefill's kernel 39; 64 of 261 words: 221 us, 302.  Two CTAs' worth of rows
+// are slower: 8 requests of 8 tokens 41 us against 39, 64 requests 424 against 302).
+bool few_rows(const lazy_attn_cfg *cfg, int max_q) {
+    return static_cast<int64_t>(max_q) * (cfg->num_q_heads / cfg->num_kv_heads) <= kFewRows;
 }
 
 // Workspace of the streaming decode: partial outputs, their (max, sum, reference), and with block
@@ -554,7 +551,7 @@ size_t lazy_prefill_q8_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, in
     (void)total_words;
     if (check_cfg(cfg) != LAZY_OK || num_req <= 0 || max_q <= 0 || max_words < 0) return 0;
     LanePlan pl;
-    return few_rows(cfg, num_req, max_q) ? lane_ws(cfg, num_req, max_q, max_words, true, false, pl)
+    return few_rows(cfg, max_q) ? lane_ws(cfg, num_req, max_q, max_words, true, false, pl)
                                 : q8_prefill_ws_bytes(prefill_units(cfg, num_req, max_q), max_words, sm_count());
 }
 
@@ -584,7 +581,7 @@ int lazy_prefill_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const 
     if (static_cast<int64_t>(max_q) * p.a.group > (int64_t(1) << 30) || units > (int64_t(1) << 22) || num_req > 65535)
         return LAZY_ERANGE;
     const int sms = sm_count();
-    const bool few = few_rows(cfg, num_req, max_q);
+    const bool few = few_rows(cfg, max_q);
     LanePlan pl;
     const size_t need = few ? lane_ws(cfg, num_req, max_q, max_words, true, false, pl)
                             : q8_prefill_ws_bytes(units, max_words, sms);

@@ -158,7 +158,7 @@ struct LanePlan {
 cudaError_t launch_lane_combine(const LaneParams &p, int min_words, cudaStream_t s);
 // tk, tv: the codes as rows of 128 bytes, one box = one block of one head; a piece per CTA.
 // With a.cu_q it computes a prefill of up to kFewRows query rows per KV head and request.
-constexpr int kLineMinWordsQ8 = 8, kFewRows = 32;
+constexpr int kLineMinWordsQ8 = 8, kFewRows = 16;
 LanePlan decode_q8_plan(int num_req, int hkv, int max_words, int rows, bool mass, int sms);
 cudaError_t launch_decode_q8(const CUtensorMap &tk, const CUtensorMap &tv, const LaneParams &p, cudaStream_t s);
 // tk, tv: the bf16 pools as rows of 128 elements, one box = half of one block of one head; a piece per warp.

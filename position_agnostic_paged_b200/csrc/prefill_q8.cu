@@ -36,6 +36,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pdl.cuh"
 #include "q8.cuh"
 #include "tc.cuh"
 
@@ -134,9 +135,11 @@ __device__ __forceinline__ int64_t unit_rows(const AttnParams &a, int mt, int kv
     return ((static_cast<int64_t>(r) * a.hkv + kvh) * a.pf_mtiles + mt) * kRows;
 }
 
-template <bool ALIBI>
+// TILES: row tiles with rows; with one the other's issuer and softmax warps have nothing to do.
+template <bool ALIBI, int TILES>
 __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_constant__ Q8PrefillParams P) {
     const AttnParams &p = P.a;
+    pdl_trigger();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + kOffBar);
@@ -178,14 +181,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
         mbar_init(&bars[B_VCEMPTY], 4);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bars[B_KFULL + i], 4);
-            mbar_init(&bars[B_KEMPTY + i], 2);
+            mbar_init(&bars[B_KEMPTY + i], TILES);
             mbar_init(&bars[B_VFULL + i], 4);
-            mbar_init(&bars[B_VEMPTY + i], 2);
+            mbar_init(&bars[B_VEMPTY + i], TILES);
             mbar_init(&bars[B_AFULL + i], 1);
         }
         for (int i = 0; i < kInfoStages; ++i) {
             mbar_init(&bars[B_IFULL + i], 1);
-            mbar_init(&bars[B_IEMPTY + i], kInfoConsumers);
+            mbar_init(&bars[B_IEMPTY + i], TILES == 2 ? kInfoConsumers : kInfoConsumers - 5);
         }
         for (int t = 0; t < 4; ++t) {
             mbar_init(&bars[B_SFULL + t], 1);
@@ -208,8 +211,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tbase = *tmem_slot;
+    pdl_wait();   // the prepared query
 
-    if (warp < 4) {
+    const int role = TILES == 1 && (warp == 1 || (warp >= 8 && warp < 12)) ? 16 : warp;
+    if (role < 4) {
         const bool leader = tc::elect_one();
         if (warp == 0) {
             // ======================================================== table walk and code copies
@@ -397,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
         } else {
             // ======================================================== query tiles and angles
             if (leader) {
-                mbar_arrive_expect_tx(&bars[B_QFULL], 2 * kTileBytes);
+                mbar_arrive_expect_tx(&bars[B_QFULL], TILES * kTileBytes);
                 const uint16_t *q = p.q_prep + unit_rows(p, mt, kvh, r) * kHeadDim;
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                for (int t = 0; t < 2 * TILES; ++t)
                     bulk_load(sm + kOffQ + t * kHalfPlane, q + t * (kHalfPlane / 2), kHalfPlane, &bars[B_QFULL]);
             }
             __syncwarp();
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
             }
             mbar_wait(&bars[B_QFULL], 0);   // landed before the kernel can end
         }
-    } else if (warp < 12) {
+    } else if (role < 12) {
         // ============================================================ softmax (one row per thread)
         const int t = (warp - 4) >> 2;
         const int row = threadIdx.x - 128 - 128 * t;
@@ -608,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
                 }
             }
         }
-    } else {
+    } else if (role < 16) {
         // ============================================================ codes to f16 operand tiles
         // Thread (ch, rb) takes elements 8 ch .. + 7 (a) and 64 above (b) of slot rb of every block.  Where rb is
         // odd b is loaded first: two rows' 8-byte loads then cover all banks.  K: (a, b) -> (a c - b s, b c + a s);
@@ -719,6 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
 // Joins the parts of each split unit: O = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i.  One warp per
 // query row, 4 head dims per lane.
 __global__ void __launch_bounds__(256) prefill_q8_join_kernel(const __grid_constant__ Q8PrefillParams P) {
+    pdl_wait();
     const AttnParams &p = P.a;
     const int row_in = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     int mt, kvh, r;
@@ -758,7 +764,9 @@ __global__ void __launch_bounds__(256) prefill_q8_query_kernel(const __grid_cons
     const int R = blockIdx.x * 16 + (threadIdx.x >> 4);
     const int G = p.group, q0 = p.cu_q[r], T = p.cu_q[r + 1] - q0;
     const int mt = R / kRows, row = R % kRows;
-    if (mt >= p.pf_mtiles || mt * kRows >= T * G) return;   // uniform for the 16 rows of the block
+    pdl_trigger();
+    // uniform for the 16 rows of the block; a second row tile is read where some request has rows for it
+    if (mt >= p.pf_mtiles || mt * kRows >= T * G || (row >= kTileRows && p.max_q * G <= kTileRows)) return;
     const bool live = R < T * G;
     const int tok = live ? R / G : 0, g = R % G;
     float cs[4], sn[4];
@@ -766,7 +774,7 @@ __global__ void __launch_bounds__(256) prefill_q8_query_kernel(const __grid_cons
     for (int u = 0; u < 4; ++u) rope_cos_sin(live ? tok - (mt * kRows) / G : 0, p.rope.theta[4 * c + u], cs[u], sn[u]);
     // byte offset of dims 4 c .. + 3 of this row in its half plane
     const uint32_t at = (row / kTileRows) * kTileBytes + (row % kTileRows) * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8;
-    for (int kvh = 0; kvh < p.hkv; ++kvh) {
+    for (int kvh = blockIdx.z; kvh < p.hkv; kvh += gridDim.z) {
         uint2 lo = make_uint2(0u, 0u), hi = lo;
         if (live) {
             const uint2 *q = reinterpret_cast<const uint2 *>(p.q_raw + (static_cast<size_t>(q0 + tok) * p.hq + kvh * G + g) * kHeadDim);
@@ -799,19 +807,23 @@ __global__ void __launch_bounds__(256) prefill_q8_query_kernel(const __grid_cons
     }
 }
 
-template <bool ALIBI>
+constexpr int kQuerySplit = 512;   // CTAs of the query kernel up to which it takes a CTA per KV head
+
+template <bool ALIBI, int TILES>
 cudaError_t launch_t(const Q8PrefillParams &p, cudaStream_t s) {
-    auto kern = prefill_q8_kernel<ALIBI>;
+    auto kern = prefill_q8_kernel<ALIBI, TILES>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
     if (e != cudaSuccess) return e;
-    prefill_q8_query_kernel<<<dim3(p.a.pf_mtiles * (kRows / 16), p.a.num_req), 256, 0, s>>>(p);
+    // with few rows a CTA per KV head, which evaluates the angles again (8 requests of 12 tokens, 8 heads,
+    // with the launches overlapped: 47 us -> 39 in all)
+    const int64_t ctas = static_cast<int64_t>(p.a.pf_mtiles) * (kRows / 16) * p.a.num_req;
+    const dim3 grid(p.a.pf_mtiles * (kRows / 16), p.a.num_req, ctas <= kQuerySplit ? p.a.hkv : 1);
+    prefill_q8_query_kernel<<<grid, 256, 0, s>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    kern<<<p.a.pf_base + p.parts * p.a.pf_nsplit, kThreads, kSmem, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_dependent(kern, dim3(p.a.pf_base + p.parts * p.a.pf_nsplit), kThreads, kSmem, s, p);
     if (e != cudaSuccess || p.a.pf_nsplit == 0) return e;
-    prefill_q8_join_kernel<<<dim3(p.a.pf_nsplit, kRows / 8), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(prefill_q8_join_kernel, dim3(p.a.pf_nsplit, kRows / 8), 256, 0, s, p);
 }
 
 }  // namespace
@@ -845,7 +857,11 @@ cudaError_t launch_prefill_q8(Q8PrefillParams &p, void *workspace, int64_t units
     p.a.ws_acc = reinterpret_cast<float *>(p.a.q_prep + units * kRows * kHeadDim);
     p.a.ws_ml = p.a.ws_acc + (pl.nsplit ? static_cast<size_t>(pl.nsplit) * pl.parts * kRows * kHeadDim : 0);
     p.row_scale = p.a.ws_ml + (pl.nsplit ? static_cast<size_t>(pl.nsplit) * pl.parts * kRows * 2 : 0);
-    return p.a.alibi ? launch_t<true>(p, s) : launch_t<false>(p, s);
+    // One row tile where no request has rows for two (64 requests of 261 words, 12 tokens, 32 heads on 8: 393 us ->
+    // 302).  A choice per CTA cost the long prompts 2 % (registers).
+    if (static_cast<int64_t>(p.a.max_q) * p.a.group <= kTileRows)
+        return p.a.alibi ? launch_t<true, 1>(p, s) : launch_t<false, 1>(p, s);
+    return p.a.alibi ? launch_t<true, 2>(p, s) : launch_t<false, 2>(p, s);
 }
 
 }  // namespace lazy

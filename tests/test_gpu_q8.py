@@ -247,10 +247,11 @@ def test_prefill_extreme_scales():
 
 
 @pytest.mark.parametrize("kind", ["rope", "alibi", "llama31"])
-@pytest.mark.parametrize("hq,hkv,most", [(8, 8, 32), (6, 2, 10), (8, 2, 8), (8, 2, 4), (32, 8, 1), (16, 1, 2), (22, 2, 2),
-                                         (32, 1, 1), (5, 5, 17)])
+@pytest.mark.parametrize("hq,hkv,most", [(8, 8, 32), (8, 8, 16), (6, 2, 10), (6, 2, 5), (8, 2, 8), (8, 2, 4), (32, 8, 1),
+                                         (16, 1, 1), (16, 1, 8), (22, 2, 1), (22, 2, 2), (32, 1, 1), (5, 5, 17), (8, 2, 32),
+                                         (8, 2, 33)])
 def test_prefill_few_rows(hq, hkv, most, kind):
-    """Up to 32 query rows per KV head: of several tokens with positions of their own, in one or two CTAs."""
+    """Query rows of a few tokens, with positions of their own: up to 16, 128 and more rows per KV head."""
     docs, reqs = _requests(14)
     lens = [most, 1, max(1, most // 2), most, 0, (most + 1) // 2, most] * 2
     # the last query keeps its place; the fourth request has tokens in front of its only key
@@ -266,7 +267,7 @@ def test_prefill_few_rows(hq, hkv, most, kind):
 
 @pytest.mark.parametrize("most", [2, 5])
 def test_prefill_few_rows_many_requests(most):
-    """More units than two per SM: five tokens of four heads take the kernel of long prompts."""
+    """More units than two per SM, of 8 and of 20 rows."""
     docs, reqs = _requests(7)
     reqs = [(s, max(0, p - most + 1), most) for s, p, _ in reqs] * 12
     c = PoolCase(la.Cfg(16, 4), docs, reqs, seed=most).to()
@@ -275,27 +276,29 @@ def test_prefill_few_rows_many_requests(most):
 
 def test_prefill_few_rows_one_long_request():
     """Many partial results of one request; a document met again at another offset."""
-    c = PoolCase(la.Cfg(8, 2), [2000, 333], [([(1, 0), (0, 333), (1, 2400), (1, 2733)], 3060, 6)], seed=3).to()
-    check(c.prefill(), *c.reference(**PREFILL_U)[:2], "prefill of 6 tokens over 3000")
+    c = PoolCase(la.Cfg(8, 2), [2000, 333], [([(1, 0), (0, 333), (1, 2400), (1, 2733)], 3060, 4)], seed=3).to()
+    check(c.prefill(), *c.reference(**PREFILL_U)[:2], "prefill of 4 tokens over 3000")
 
 
-def test_prefill_few_rows_bad_block():
+@pytest.mark.parametrize("most", [3, 5])
+def test_prefill_few_rows_bad_block(most):
     docs, reqs = _requests(4)
-    reqs = [(s, max(0, p - 4), 5) for s, p, _ in reqs]
+    reqs = [(s, max(0, p - most + 1), most) for s, p, _ in reqs]
     c = PoolCase(la.Cfg(8, 2), docs, reqs, seed=2)
     c.words[3] = la_pack(c.num_blocks + 5, 48)
     c.to()
-    check(c.prefill(), *c.reference(**PREFILL_U)[:2], "prefill of 5 tokens with a bad block")
+    check(c.prefill(), *c.reference(**PREFILL_U)[:2], f"prefill of {most} tokens with a bad block")
     assert c.dev["status"].item() == la.DSTATUS_BAD_BLOCK
 
 
-def test_prefill_extreme_scales_many_rows():
+@pytest.mark.parametrize("most", [4, 40])
+def test_prefill_extreme_scales_rows(most):
     docs, reqs = _requests(7)
-    reqs = [(s, max(0, p - 11), 12) for s, p, _ in reqs]
+    reqs = [(s, max(0, p - most + 1), most) for s, p, _ in reqs]
     for k_exp, v_exp in (((-120, -100), (-125, -90)), ((90, 100), (100, 110))):
         c = PoolCase(la.Cfg(8, 2), docs, reqs, seed=9, k_exp=k_exp, v_exp=v_exp,
                      q_scale=2.0 ** -100 if k_exp[0] > 0 else 1.0).to()
-        check(c.prefill(), *c.reference(**PREFILL_U)[:2], f"prefill of 12 tokens, scales {k_exp} {v_exp}", rel=np.inf)
+        check(c.prefill(), *c.reference(**PREFILL_U)[:2], f"prefill of {most} tokens, scales {k_exp} {v_exp}", rel=np.inf)
 
 
 def test_prefill_faults_and_rows_behind_the_last_sequence():
