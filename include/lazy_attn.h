@@ -330,7 +330,8 @@ size_t lazy_prefill_q8_workspace_bytes(const lazy_attn_cfg *cfg, int num_req, in
 
 /* lazy_prefill_attn over an 8-bit pool.  The workspace is required (LAZY_EWORKSPACE).  Slots that
  * no query of the request sees (unwritten ones, and keys behind its last query's position) have
- * no influence, whatever they hold.  Words past max_words of a request (LAZY_DSTATUS_BAD_TABLE) are
+ * no influence, whatever they hold (a NaN value in a slot that only some of its queries see may reach
+ * the output of the others).  Words past max_words of a request (LAZY_DSTATUS_BAD_TABLE) are
  * ignored.  q_raw: 8-byte, out: 16-byte aligned (LAZY_EINVAL); num_req <= 65535 and at most 2^22
  * units of 256 query rows (LAZY_ERANGE). */
 int lazy_prefill_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const int32_t *cu_q,

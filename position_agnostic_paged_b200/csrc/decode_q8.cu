@@ -25,9 +25,20 @@
 // partial result (m, l, acc) to workspace slot (piece + request), unique because each new partial moves
 // on to the next piece or the next request.  A second kernel joins a request's partials in order.
 //
-// Warps: four per group of 8 query heads (or 4) for the softmax (thread t of a group: key t of the tile, later
-// head dim t), one for the table walk and the TMA loads, one for MMA issue.  A tile is up to 8 words of one request with one offset; K and V of a tile (32 KiB)
-// share a stage.  Scores are double-buffered and a tile ahead of the softmax.
+// A CTA takes up to 16 query rows of a KV head; a wider group of heads is taken by neighbouring CTAs, two per
+// SM, whose barriers and waits overlap (32 heads on one KV head with block mass: one CTA of 32 rows 136 us, two
+// of 16 131).  A prefill of a few tokens runs here too, its rows (token, head) pairs: 128 keys cost a CTA of the
+// prefill's kernel about 4 us however few its rows, here 2.
+//
+// Warps: four per group of 8 query rows (or 4) for the softmax (thread t of a group: key t of the tile, later
+// head dim t), one for the table walk and the TMA loads, one for MMA issue.  A tile is up to 8 words of one
+// request with one offset; K and V of a tile (32 KiB) share a stage.  Scores are double-buffered; QK of tile
+// i + 1 runs under the weights of tile i.  (Making tile i + 1's query before the scores of tile i, to run QK
+// under all of it: 107 -> 111 us, 131 -> 137.)
+//
+// What bounds it: HBM for long tables with few rows (64 requests of 4161 tokens, 32 heads on 8: 548 MB in 106 us
+// with the joining kernel, 5.2 TB/s, 79 % of the copy rate), the chain of a tile (scores, references, weights'
+// parts, about 1900 cycles with 4 rows and 3200 with 16) where rows are many.
 #include <climits>
 
 #include "common.cuh"
