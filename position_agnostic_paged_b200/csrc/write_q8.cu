@@ -272,6 +272,7 @@ __global__ void __launch_bounds__(kBulkWarps * 32, 5) kv_write_q8_bulk_kernel(co
     }
     __syncthreads();
     uint32_t phase[2] = {0u, 0u};
+    bool ok = true, flying[2] = {false, false};   // copies that have not landed
     for (int k = 0; k < n_owned; ++k) {
         const int blk = owned[k], *tok = toks[k];
         const int my = lane < kBlockTokens ? tok[lane] : -1;
@@ -279,6 +280,7 @@ __global__ void __launch_bounds__(kBulkWarps * 32, 5) kv_write_q8_bulk_kernel(co
         // rows of K (0) or V (1) of head h; lane r copies row r
         auto fetch = [&](int which, int h) {
             __syncwarp();   // the last head's rows are read
+            flying[which] = true;
             if (lane == 0) mbar_arrive_expect_tx(&bars[warp][which], __popc(have) * 256);
             __syncwarp();
             if (my >= 0) {
@@ -290,10 +292,14 @@ __global__ void __launch_bounds__(kBulkWarps * 32, 5) kv_write_q8_bulk_kernel(co
             }
         };
         auto landed = [&](int which) {
-            const bool ok = __all_sync(0xffffffffu, mbar_wait(&bars[warp][which], phase[which]));
+            const bool got = __all_sync(0xffffffffu, mbar_wait(&bars[warp][which], phase[which]));
+            if (!got) {
+                set_status(p.d_status, LAZY_DSTATUS_TIMEOUT);
+                return false;
+            }
             phase[which] ^= 1;
-            if (!ok) set_status(p.d_status, LAZY_DSTATUS_TIMEOUT);
-            return ok;
+            flying[which] = false;
+            return true;
         };
         if (warp < p.hkv) {
             fetch(0, warp);
@@ -323,7 +329,6 @@ __global__ void __launch_bounds__(kBulkWarps * 32, 5) kv_write_q8_bulk_kernel(co
             cs[r][1][d] = static_cast<float>(z.y);
         }
         __syncthreads();
-        bool ok = true;
 #pragma unroll 1
         for (int h = warp; h < p.hkv && ok; h += kBulkWarps) {
             auto key_row = [&](int r, float(&x)[8]) {
@@ -336,6 +341,7 @@ __global__ void __launch_bounds__(kBulkWarps * 32, 5) kv_write_q8_bulk_kernel(co
                 unpack_row(q[c], q[16 + c], x);
             };
             ok = landed(0);
+            if (!ok) break;
             float am = 0.f;
             if (have == 0xFFFFu) {
 #pragma unroll 2
@@ -356,7 +362,8 @@ __global__ void __launch_bounds__(kBulkWarps * 32, 5) kv_write_q8_bulk_kernel(co
             __syncwarp();
             code_head<true>(p, blk, h, nv, tok, pos, have, lane, am, kErrLarge, key_row);
             if (h + kBulkWarps < p.hkv) fetch(0, h + kBulkWarps);
-            ok &= landed(1);
+            ok = landed(1);
+            if (!ok) break;
             // max |v| as bf16 pairs (a NaN does not enter)
             __nv_bfloat162 v2 = __float2bfloat162_rn(0.f);
 #pragma unroll 2
@@ -373,10 +380,14 @@ __global__ void __launch_bounds__(kBulkWarps * 32, 5) kv_write_q8_bulk_kernel(co
             code_head<false>(p, blk, h, nv, tok, pos, have, lane, vm, 0.f, val_row);
             if (h + kBulkWarps < p.hkv) fetch(1, h + kBulkWarps);
         }
-        __syncthreads();   // (a warp whose wait ran out comes here too, its copies may be in flight: they hold only its buffers)
+        const bool stop = __syncthreads_or(!ok);
         if (tid == 0) p.blk_meta[blk] = max(meta, ws_metas(p)[blk]);
-        if (!ok) break;
+        if (stop) break;
     }
+    // a wait that ran out: no copy may land in the memory of a CTA that is gone
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+        if (flying[which]) mbar_wait(&bars[warp][which], phase[which]);
 }
 
 // A small call: CTA t owns token t's block if t is the call's first token there.
