@@ -366,7 +366,7 @@ int lazy_decode_attn_mass(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const
  * the input's words; none may be an input (LAZY_EINVAL for equal pointers).  A request with
  * more than max_words words sets LAZY_DSTATUS_BAD_TABLE; it is shortened all the same, with
  * its words past max_words dropped (evicted).  A dropped word only leaves this request's table:
- * the block itself is the caller's, and other requests may go on using it.  num_req <= 2^24
+ * the block itself is the caller's, and other requests may go on using it.  num_req <= 2^20
  * (LAZY_ERANGE). */
 int lazy_evict_blocks(const uint32_t *table, const int32_t *table_indptr, int num_req, int max_words,
                       const float *block_mass, const int32_t *keep, int n_first, int n_last,

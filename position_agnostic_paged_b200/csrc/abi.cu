@@ -618,7 +618,7 @@ int lazy_evict_blocks(const uint32_t *table, const int32_t *table_indptr, int nu
                       int *d_status, void *stream) {
     if (num_req < 0 || max_words < 0 || n_first < 0 || n_last < 0) return LAZY_EINVAL;
     if (!indptr_out || (num_req > 0 && (!table_indptr || !keep))) return LAZY_EINVAL;
-    if (num_req > (1 << 24)) return LAZY_ERANGE;
+    if (num_req > (1 << 20)) return LAZY_ERANGE;
     if (num_req == 0) return launch_rc(cudaMemsetAsync(indptr_out, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream)));
     if (max_words > 0 && (!block_mass || !table_out || !mass_out)) return LAZY_EINVAL;
     if ((max_words > 0 || evicted) && !table) return LAZY_EINVAL;

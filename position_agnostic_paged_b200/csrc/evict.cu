@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t s) {
     const long long waves = (p.num_req + kWave - 1) / kWave;
     const bool cluster = p.max_words > kLongWords + kWaveWords * (waves - 1);
-    const int per_cta = cluster ? (p.max_words + kCluster - 1) / kCluster + 32 : p.max_words;
+    const int per_cta = cluster ? p.max_words / kCluster + 64 : p.max_words;
     const int smem_keys = per_cta < kSmemKeys ? per_cta : kSmemKeys;
     auto kern = cluster ? evict_kernel<kCluster> : evict_kernel<1>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemKeys * 4);

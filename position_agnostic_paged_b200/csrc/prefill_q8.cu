@@ -839,7 +839,7 @@ Q8PrefillPlan q8_prefill_plan(int64_t units, int max_words, int sms) {
     if (units <= 0 || sms <= 0) return pl;
     const int64_t rem = units % sms;
     if (rem == 0 || 2 * rem > sms) return pl;
-    const int64_t parts = std::min<int64_t>(std::min<int64_t>(sms / rem, 16), (max_words + 2 * kTileBlocks - 1) / (2 * kTileBlocks));
+    const int64_t parts = std::min<int64_t>(std::min<int64_t>(sms / rem, 16), (int64_t(max_words) + 2 * kTileBlocks - 1) / (2 * kTileBlocks));
     if (parts < 2) return pl;
     pl.nsplit = static_cast<int>(rem);
     pl.parts = static_cast<int>(parts);

@@ -542,6 +542,25 @@ def test_evict_no_requests_and_many():
 
 
 # ----------------------------------------------------------------------- as a program uses them
+@pytest.mark.parametrize("most", [1, 4, 12, 70])
+def test_max_words_far_above_the_tables(most):
+    """max_words only bounds: the largest int is a valid bound."""
+    docs, reqs = _requests(7)
+    reqs = [(s, max(0, p - most + 1), most) for s, p, _ in reqs]
+    c = PoolCase(la.Cfg(8, 2), docs, reqs, seed=most).to()
+    d, n, big = c.dev, c.q_pos0.size, 2 ** 31 - 1
+    out = torch.full_like(d["q"], 7.0)
+    if most == 1:
+        ws = c.ws(la.decode_q8_workspace_bytes(c.cfg, n, big))
+        la.decode_attn_q8(c.cfg, d["q"], d["pos0"], d["table"], d["indptr"], big, c.pool, out, ws, None, d["status"])
+        check(out, *c.reference()[:2], "decode, largest max_words")
+    ws = c.ws(la.prefill_q8_workspace_bytes(c.cfg, n, out.shape[0], most, big, c.words.size))
+    la.prefill_attn_q8(c.cfg, d["q"], d["cu"], d["pos0"], most, d["table"], d["indptr"], big, c.pool, out, ws, d["status"])
+    check(out, *c.reference(**PREFILL_U)[:2], f"prefill of {most} tokens, largest max_words")
+    words = np.arange(50, dtype=np.uint32)
+    assert _check_evict(words, [0, 20, 50], big, np.linspace(0, 1, 50, dtype=np.float32), [5, 7], 1, 2) == 0
+
+
 def test_write_decode_evict_decode_together():
     """Prompts written in 8 bits, prefilled, decoded token by token with their weights accumulated,
     the tables halved, and decoded further over the shorter tables."""

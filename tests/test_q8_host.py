@@ -134,7 +134,7 @@ def test_evict_refusals():
         assert _evict(**{f: None}) == la.LAZY_EINVAL
     for f in ("n", "mw", "nf", "nl"):
         assert _evict(**{f: -1}) == la.LAZY_EINVAL
-    assert _evict(n=(1 << 24) + 1) == la.LAZY_ERANGE
+    assert _evict(n=(1 << 20) + 1) == la.LAZY_ERANGE
     # outputs must not be inputs or each other
     assert _evict(to=P) == la.LAZY_EINVAL
     assert _evict(mo=3 * P) == la.LAZY_EINVAL
