@@ -65,14 +65,6 @@ class Cfg:
     alibi_slopes: tuple | None = None
 
     def c(self) -> LazyAttnCfg:
-        """The C structure, made once (the fields of a Cfg do not change)."""
-        st = self.__dict__.get("_c")
-        if st is None:
-            st = self._make_c()
-            object.__setattr__(self, "_c", st)
-        return st
-
-    def _make_c(self) -> LazyAttnCfg:
         st = LazyAttnCfg(self.num_q_heads, self.num_kv_heads, self.head_dim, self.block_size,
                          float(self.rope_base), float(self.softmax_scale), None, None)
         if self.alibi_slopes is not None:
@@ -86,6 +78,20 @@ class Cfg:
             st._theta_keepalive = arr
             st.rope_theta = ctypes.cast(arr, ctypes.POINTER(ctypes.c_double))
         return st
+
+    def _shared_c(self) -> LazyAttnCfg:
+        """c(), made once where no field can change; to be read only."""
+        if type(self.rope_theta) not in (tuple, type(None)) or type(self.alibi_slopes) not in (tuple, type(None)):
+            return self.c()
+        st = self.__dict__.get("_c")
+        if st is None:
+            st = self.c()
+            object.__setattr__(self, "_c", st)
+        return st
+
+    def __getstate__(self):
+        """Without the C structure: its pointers belong to this object."""
+        return {k: v for k, v in self.__dict__.items() if k != "_c"}
 
 
 _vp, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -428,13 +434,13 @@ def _heads(cfg: Cfg, pool: Q8Pool) -> None:
 
 
 def kv_write_q8_workspace_bytes(cfg: Cfg, n_tok: int, num_blocks: int) -> int:
-    c = cfg.c()
+    c = cfg._shared_c()
     return int(_lib.lazy_kv_write_q8_workspace_bytes(ctypes.byref(c), int(n_tok), int(num_blocks)))
 
 
 def kv_write_q8(cfg: Cfg, k_raw, v_raw, slot, local_j, pool: Q8Pool, workspace=None, d_status=None, stream=None):
     """New tokens into an 8-bit pool (lazy_kv_write_q8): scales, codes and metadata of the blocks they fall in."""
-    c, q, n = cfg.c(), pool.c(), int(slot.numel())
+    c, q, n = cfg._shared_c(), pool.c(), int(slot.numel())
     _heads(cfg, pool)
     for name, t in (("k_raw", k_raw), ("v_raw", v_raw)):
         _take(name, t, _BF16, (n, cfg.num_kv_heads, 128))
@@ -465,7 +471,7 @@ def _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass):
 
 
 def decode_q8_workspace_bytes(cfg: Cfg, num_req: int, max_words: int, with_mass: bool = False) -> int:
-    c = cfg.c()
+    c = cfg._shared_c()
     return int(_lib.lazy_decode_q8_workspace_bytes(ctypes.byref(c), int(num_req), int(max_words), 1 if with_mass else 0))
 
 
@@ -473,7 +479,7 @@ def decode_attn_q8(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: int, 
                    block_mass=None, d_status=None, stream=None):
     """One decode step over an 8-bit pool (lazy_decode_attn_q8).  block_mass: optional float32
     accumulators, one per table word, that grow by the words' attention weights."""
-    c, q = cfg.c(), pool.c()
+    c, q = cfg._shared_c(), pool.c()
     _heads(cfg, pool)
     n = _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass)
     _launch("lazy_decode_attn_q8", _lib.lazy_decode_attn_q8,
@@ -483,7 +489,7 @@ def decode_attn_q8(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: int, 
 
 
 def decode_mass_workspace_bytes(cfg: Cfg, num_req: int, max_words: int) -> int:
-    c = cfg.c()
+    c = cfg._shared_c()
     return int(_lib.lazy_decode_mass_workspace_bytes(ctypes.byref(c), int(num_req), int(max_words)))
 
 
@@ -491,7 +497,7 @@ def decode_attn_mass(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: int
                      block_mass, workspace, d_status=None, stream=None):
     """decode_attn over the bf16 pool that also adds each table word's attention weight to block_mass
     (lazy_decode_attn_mass)."""
-    c = cfg.c()
+    c = cfg._shared_c()
     n = _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass)
     nb = int(k_pool.shape[0])
     for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
@@ -506,7 +512,7 @@ def decode_attn_mass(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: int
 
 def prefill_q8_workspace_bytes(cfg: Cfg, num_req: int, total_q: int, max_q: int, max_words: int,
                                total_words: int) -> int:
-    c = cfg.c()
+    c = cfg._shared_c()
     return int(_lib.lazy_prefill_q8_workspace_bytes(ctypes.byref(c), int(num_req), int(total_q), int(max_q),
                                                     int(max_words), int(total_words)))
 
@@ -514,7 +520,7 @@ def prefill_q8_workspace_bytes(cfg: Cfg, num_req: int, total_q: int, max_q: int,
 def prefill_attn_q8(cfg: Cfg, q_raw, cu_q, q_pos0, max_q: int, table, table_indptr, max_words: int, pool: Q8Pool,
                     out, workspace, d_status=None, stream=None):
     """Causal prefill over an 8-bit pool (lazy_prefill_attn_q8)."""
-    c, q = cfg.c(), pool.c()
+    c, q = cfg._shared_c(), pool.c()
     _heads(cfg, pool)
     n, total_q = int(q_pos0.numel()), int(q_raw.shape[0])
     _take("q_raw", q_raw, _BF16, (total_q, cfg.num_q_heads, 128))

@@ -1,6 +1,8 @@
 """Refusals and workspace sizes of the 8-bit pool, block mass and eviction calls.  Every call here
 is refused, or does nothing, on the host: nothing is launched and no pointer is read."""
+import copy
 import ctypes
+import pickle
 
 import pytest
 import torch
@@ -173,3 +175,17 @@ def test_binding_checks_types_shapes_and_devices():
     f = torch.zeros(2)
     with pytest.raises(ValueError):                                                      # too little room
         la.evict_blocks(i(0, 0), i(0, 2), 2, f, i(1), 0, 0, i(0), i(0, 0), f.clone())
+
+
+def test_cfg_stays_a_plain_value():
+    """The calls keep a C structure of the configuration; copies, pickles and mutable fields are as without it."""
+    for cfg in (la.Cfg(8, 2), la.Cfg(8, 2, alibi_slopes=(0.5,) * 8), la.Cfg(8, 2, rope_theta=(0.1,) * 64)):
+        assert la.decode_q8_workspace_bytes(cfg, 1, 1) == la.decode_q8_workspace_bytes(cfg, 1, 1)
+        for other in (copy.copy(cfg), copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg))):
+            assert other == cfg and other._shared_c() is not cfg._shared_c()
+        assert cfg.c() is not cfg.c() and cfg._shared_c() is cfg._shared_c()
+    theta = [0.1] * 64
+    cfg = la.Cfg(8, 2, rope_theta=theta)
+    assert cfg._shared_c().rope_theta[3] == 0.1
+    theta[3] = 0.25
+    assert cfg._shared_c().rope_theta[3] == 0.25
