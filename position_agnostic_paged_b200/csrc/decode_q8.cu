@@ -83,6 +83,9 @@ struct Cfg {
     static constexpr int kSoft = 128 * kGroups, kThreads = kSoft + 64;
     static constexpr int kQRows = QP * NG, kQN = (kQRows + 15) / 16 * 16;    // rows of the Q operand, N of the S product
     static constexpr int kPRows = kPP * NG, kPN = (kPRows + 15) / 16 * 16;
+    // The P operand: keys as rows of kPN bytes (MN-major), which a thread writes eight heads at a time; with 4
+    // heads too narrow for that, rows of 128 keys (K-major), a byte per store
+    static constexpr bool kKeyRows = NG >= 8;
     static constexpr int kQBytes = (kQN + 7) / 8 * 1024, kPBytes = (kPN + 7) / 8 * 1024;
     static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 4096 + 1024;   // buffers, small state, alignment
     static constexpr int kOcc = 2 * (kFixed + 2 * kStageBytes + 1024) <= 227 * 1024 ? 2 : 1;
@@ -91,6 +94,7 @@ struct Cfg {
     static constexpr int kSmem = kFixed + kStages * kStageBytes;
     static constexpr int kCols0 = 2 * kQN + kPN;
     static constexpr int kCols = kCols0 <= 64 ? 64 : kCols0 <= 128 ? 128 : kCols0 <= 256 ? 256 : 512;   // tensor memory
+    static_assert(!kKeyRows || kPN == 32 || kPN == 64, "swizzle");
     static_assert(kStages >= 2 && kOcc * kCols <= 512, "resources");
     // shared memory, from a 1 KiB boundary
     static constexpr int kOffQ = kStages * kStageBytes, kOffP = kOffQ + 2 * kQBytes, kOffState = kOffP + 2 * kPBytes;
@@ -105,8 +109,8 @@ constexpr int kOffMisc = kOffAngle + 512;
 static_assert(kOffMisc + 16 <= 4096, "state");
 
 // kind::f8f6f4 with e4m3 A/B and fp32 accumulation, M = 128.
-constexpr uint32_t idesc_e4m3(int n, bool a_mn_major) {
-    return (1u << 4) | (a_mn_major ? (1u << 15) : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+constexpr uint32_t idesc_e4m3(int n, bool a_mn_major, bool b_mn_major) {
+    return (1u << 4) | (a_mn_major ? (1u << 15) : 0u) | (b_mn_major ? (1u << 16) : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -396,9 +400,12 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
         // ============================================================ MMA issue
         //   QK(0) | QK(1) PV(0) | QK(2) PV(1) | ...; PV(i) goes first where tile i + 1 has not landed
         const bool leader = tc::elect_one();
-        constexpr uint32_t idq = idesc_e4m3(C::kQN, false), idp = idesc_e4m3(C::kPN, true);
+        constexpr uint32_t idq = idesc_e4m3(C::kQN, false, false), idp = idesc_e4m3(C::kPN, true, C::kKeyRows);
         const uint64_t dA = tc::smem_desc(smem_u32(sm), 16, 1024);
-        const uint64_t dQ = tc::smem_desc(smem_u32(sm + C::kOffQ), 16, 1024), dP = tc::smem_desc(smem_u32(sm + C::kOffP), 16, 1024);
+        const uint64_t dQ = tc::smem_desc(smem_u32(sm + C::kOffQ), 16, 1024), dP0 = tc::smem_desc(smem_u32(sm + C::kOffP), 16, C::kKeyRows ? 8 * C::kPN : 1024);
+        // rows of 64 bytes: 64-byte swizzle (4), of 32 bytes: 32-byte swizzle (6), in place of 128-byte (2)
+        const uint64_t dP = C::kKeyRows ? (dP0 & ~(7ull << 61)) | (C::kPN == 64 ? 4ull : 6ull) << 61 : dP0;
+        constexpr int kPStep = (C::kKeyRows ? 32 * C::kPN : 32) >> 4;   // 32 keys
         bool ok = true;
         int off = 0, req = -1, qbuf = 1;       // of the tile whose QK was issued last
         // record of tile i: words, and whether it opens a request
@@ -453,7 +460,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 const uint64_t va = dA + static_cast<uint64_t>((st * kStageBytes + kHalfStage) >> 4);
                 const uint64_t pb = dP + static_cast<uint64_t>(((i & 1) * C::kPBytes) >> 4);
                 for (int s = 0; 2 * s < n; ++s)
-                    mma_e4m3(tO, va + static_cast<uint64_t>((s * 32 * 128) >> 4), pb + 2 * s, idp, (opens && s == 0) ? 0u : 1u);
+                    mma_e4m3(tO, va + static_cast<uint64_t>((s * 32 * 128) >> 4), pb + kPStep * s, idp, (opens && s == 0) ? 0u : 1u);
                 tc::commit(&empty[st]);
                 tc::commit(&odone[i & 1]);
             }
@@ -676,18 +683,26 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 l[h] += x[h];
             }
             uint8_t *pd = sm + C::kOffP + buf * C::kPBytes;
+            float w[HT / 4][4];
 #pragma unroll
             for (int h = 0; h < HT; h += 4) {
                 const float4 dv = *reinterpret_cast<const float4 *>(&h_dv[g0 + h]);
                 const float dv4[4] = {dv.x, dv.y, dv.z, dv.w};
-                float w[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) w[y] = vis && !(CHUNK && h + y < seer) ? x[h + y] * (vs * dv4[y] * 0x1p20f) : 0.f;
+                for (int y = 0; y < 4; ++y)
+                    w[h / 4][y] = vis && !(CHUNK && h + y < seer) ? x[h + y] * (vs * dv4[y] * 0x1p20f) : 0.f;
+            }
 #pragma unroll
-                for (int part = 0; part < kPP; ++part) {
-                    const uint32_t codes = take_part(w);
+            for (int part = 0; part < kPP; ++part) {
+                if constexpr (C::kKeyRows) {
+                    // columns part * NG + head; 16-byte pieces swizzled by the row's bits above 128 bytes
+                    const int at = t * C::kPN + part * NG + g0;
+                    const uint32_t lo4 = take_part(w[0]), hi4 = take_part(w[1]);
+                    *reinterpret_cast<uint2 *>(pd + (at ^ (((at >> 7) & (C::kPN / 16 - 1)) << 4))) = make_uint2(lo4, hi4);
+                } else {
+                    const uint32_t codes = take_part(w[0]);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) pd[swz8(part * NG + g0 + h + y, t)] = static_cast<uint8_t>(codes >> (8 * y));
+                    for (int y = 0; y < 4; ++y) pd[swz8(part * NG + g0 + y, t)] = static_cast<uint8_t>(codes >> (8 * y));
                 }
             }
             // a weight of 0 does not undo a NaN in a slot that the query does not see
