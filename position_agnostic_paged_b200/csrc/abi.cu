@@ -226,7 +226,7 @@ int64_t prefill_units(const lazy_attn_cfg *cfg, int num_req, int max_q) {
 }
 
 // A prefill whose query rows per KV head and request fit a CTA of the decode's kernel (8 requests of 126 words,
-// 32 heads on 8: 4 tokens 29 us, the prefill's kernel 39; 64 of 261 words: 221 us, 302.  Two CTAs' worth of rows
+// 32 heads on 8: 4 tokens 28 us, the prefill's kernel 39; 64 of 261 words: 195 us, 302.  Two CTAs' worth of rows
 // are slower: 8 requests of 8 tokens 41 us against 39, 64 requests 424 against 302).
 bool few_rows(const lazy_attn_cfg *cfg, int max_q) {
     return static_cast<int64_t>(max_q) * (cfg->num_q_heads / cfg->num_kv_heads) <= kFewRows;

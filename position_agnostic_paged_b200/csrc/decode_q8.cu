@@ -28,7 +28,7 @@
 // A CTA takes up to 16 query rows of a KV head; a wider group of heads is taken by neighbouring CTAs, two per
 // SM, whose barriers and waits overlap (32 heads on one KV head with block mass: one CTA of 32 rows 136 us, two
 // of 16 131).  A prefill of a few tokens runs here too, its rows (token, head) pairs: 128 keys cost a CTA of the
-// prefill's kernel about 4 us however few its rows, here 2.
+// prefill's kernel about 3 us however few its rows, here under 2.
 //
 // Warps: four per group of 8 query rows (or 4) for the softmax (thread t of a group: key t of the tile, later
 // head dim t), one for the table walk and the TMA loads, one for MMA issue.  A tile is up to 8 words of one
@@ -38,7 +38,8 @@
 //
 // What bounds it: HBM for long tables with few rows (64 requests of 4161 tokens, 32 heads on 8: 548 MB in 106 us
 // with the joining kernel, 5.2 TB/s, 79 % of the copy rate), the chain of a tile (scores, references, weights'
-// parts, about 1900 cycles with 4 rows and 3200 with 16) where rows are many.
+// parts, about 1900 cycles with 4 rows) and its instructions where rows are many (32 heads with block mass:
+// 117 us, 57 % of issue slots).
 #include <climits>
 
 #include "common.cuh"
@@ -84,7 +85,7 @@ struct Cfg {
     static constexpr int kQRows = QP * NG, kQN = (kQRows + 15) / 16 * 16;    // rows of the Q operand, N of the S product
     static constexpr int kPRows = kPP * NG, kPN = (kPRows + 15) / 16 * 16;
     // The P operand: keys as rows of kPN bytes (MN-major), which a thread writes eight heads at a time; with 4
-    // heads too narrow for that, rows of 128 keys (K-major), a byte per store
+    // heads too narrow for that, rows of 128 keys (K-major), a byte per store (which cost 16 heads 131 us for 117)
     static constexpr bool kKeyRows = NG >= 8;
     static constexpr int kQBytes = (kQN + 7) / 8 * 1024, kPBytes = (kPN + 7) / 8 * 1024;
     static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 4096 + 1024;   // buffers, small state, alignment
@@ -169,7 +170,10 @@ __device__ __forceinline__ uint32_t take_part(float (&x)[4]) {
     f16x2_to_f32(h0, y[0], y[1]);
     f16x2_to_f32(h1, y[2], y[3]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = (x[i] - y[i]) * kPartStep;
+    for (int i = 0; i < 4; i += 2) {
+        mul2(x[i], x[i + 1], x[i], x[i + 1], kPartStep, kPartStep);
+        fma2v(x[i], x[i + 1], y[i], y[i + 1], -kPartStep, -kPartStep, x[i], x[i + 1]);
+    }
     return w;
 }
 // byte offset of column `col` of row `row` in an operand of 128-byte rows, 128-byte swizzled
