@@ -96,7 +96,7 @@ struct Cfg {
     static constexpr int kCols0 = 2 * kQN + kPN;
     static constexpr int kCols = kCols0 <= 64 ? 64 : kCols0 <= 128 ? 128 : kCols0 <= 256 ? 256 : 512;   // tensor memory
     static_assert(!kKeyRows || kPN == 32 || kPN == 64, "swizzle");
-    static_assert(kStages >= 2 && kOcc * kCols <= 512, "resources");
+    static_assert(kStages >= 2 && kOcc * kCols <= 512 && kSoft / 16 >= NG, "resources");
     // shared memory, from a 1 KiB boundary
     static constexpr int kOffQ = kStages * kStageBytes, kOffP = kOffQ + 2 * kQBytes, kOffState = kOffP + 2 * kPBytes;
 };
@@ -228,6 +228,23 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
     if (wi > (total - 1) / per) return;
     const int lo = wi * per, cnt = min(total - lo, per);
 
+    // the walk's first loads, while the others set up: the request of the first word (the largest r with
+    // table_indptr[r] <= its index), its bounds, and 32 words, one per lane
+    int r = 0, r_beg = 0, r_end = 0;
+    uint32_t wl = 0u;
+    if (warp == kWalk) {
+        if (lane < cnt) wl = a.table[base + lo + lane];
+        int hi = B;
+        while (hi - r > 1) {
+            const int step = (hi - r + 31) >> 5, x = r + step * lane;
+            const bool below = x < hi && a.table_indptr[x] - base <= lo;
+            const int k = __popc(__ballot_sync(0xffffffffu, below)) - 1;
+            r += step * k;
+            hi = min(hi, r + step);
+        }
+        r_beg = a.table_indptr[r] - base;
+        r_end = a.table_indptr[r + 1] - base;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&full[i], 1);
@@ -275,16 +292,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
         }
-        // the request of the first word: the largest r with table_indptr[r] <= its index
-        int r = 0, hi = B;
-        while (hi - r > 1) {
-            const int step = (hi - r + 31) >> 5, x = r + step * lane;
-            const bool below = x < hi && a.table_indptr[x] - base <= lo;
-            const int k = __popc(__ballot_sync(0xffffffffu, below)) - 1;
-            r += step * k;
-            hi = min(hi, r + step);
-        }
-        int r_beg = a.table_indptr[r] - base, r_end = a.table_indptr[r + 1] - base, rows, qpos, last;   // last: position of the last query
+        int rows, qpos, last;     // of the request: rows here, positions of its first and last query
         int j = 0, first = 0;     // tiles; the first tile of the request
         bool ok = true;
         auto enter = [&]() {
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             first = j;
         };
         enter();
-        uint32_t wl = 0u, ml = 0u;
+        uint32_t ml = 0u;
         float ksl = 1.f, vsl = 1.f;
         int b0 = INT_MIN / 2;
         for (int k = 0; k < cnt;) {
@@ -317,9 +325,9 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             if (k - b0 + kTileWords > 32 && b0 + 32 < cnt) {
                 // 32 words, one per lane, with their blocks' metadata and scales
                 b0 = k;
-                wl = ml = 0u;
+                ml = 0u;
+                if (k > 0) wl = k + lane < cnt ? a.table[base + lo + k + lane] : 0u;
                 if (k + lane < cnt) {
-                    wl = a.table[base + lo + k + lane];
                     const uint32_t b = word_block(wl);
                     if (b < static_cast<uint32_t>(a.num_blocks)) {
                         const size_t bh = static_cast<size_t>(b) * hkv + kvh;
@@ -481,6 +489,8 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
         const int t = threadIdx.x & 127, wq = warp & 3;   // key of the tile, later head dim; warp of the group
         const int g0 = (threadIdx.x >> 7) * HT;           // first head of this thread
         const uint32_t lane_off = static_cast<uint32_t>(32 * wq) << 16;
+        // (read once: a per-lane read of the parameter table takes 32 turns)
+        const double my_theta = !CHUNK && threadIdx.x < kHalfDim ? a.rope.theta[threadIdx.x] : 0.0;
         float l[HT];
         int qbuf = 1, cur_req = -1, cur_off = 0;   // of the Q operand made last
         // the query of tile `tl` as e4m3 parts, if it is not the one made last
@@ -490,56 +500,53 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             qbuf ^= 1;
             cur_req = r;
             cur_off = off;
+            // 16 threads per row: dims 4c .. + 3 and 64 above
+            const int c = threadIdx.x & 15, h = threadIdx.x >> 4;
+            const int tok = CHUNK ? (hg + h) / a.group : 0, head = kvh * a.group + hg + h - tok * a.group;
+            uint2 lo2 = make_uint2(0u, 0u), hi2 = lo2;
+            if (h < rows) {
+                const uint2 *q = reinterpret_cast<const uint2 *>(
+                    a.q_raw + (static_cast<size_t>(CHUNK ? a.cu_q[r] + tok : r) * a.hq + head) * kHeadDim);
+                lo2 = __ldg(q + c);
+                hi2 = __ldg(q + 16 + c);
+            }
             if (!CHUNK) {
                 if (threadIdx.x < kHalfDim)
-                    rope_cos_sin(a.alibi ? 0 : tl.qpos - off, a.rope.theta[threadIdx.x], angle[threadIdx.x].x, angle[threadIdx.x].y);
+                    rope_cos_sin(a.alibi ? 0 : tl.qpos - off, my_theta, angle[threadIdx.x].x, angle[threadIdx.x].y);
                 sync_softmax<C::kSoft>();
             }
             uint8_t *qd = sm + C::kOffQ + qbuf * C::kQBytes;
-            // 16 threads per row: dims 4c .. + 3 and 64 above
-            const int c = threadIdx.x & 15;
-            for (int h0 = 0; h0 < rows; h0 += C::kSoft / 16) {
-                const int h = h0 + (threadIdx.x >> 4);
-                const int tok = CHUNK ? (hg + h) / a.group : 0, head = kvh * a.group + hg + h - tok * a.group;
-                uint2 lo2 = make_uint2(0u, 0u), hi2 = lo2;
-                if (h < rows) {
-                    const uint2 *q = reinterpret_cast<const uint2 *>(
-                        a.q_raw + (static_cast<size_t>(CHUNK ? a.cu_q[r] + tok : r) * a.hq + head) * kHeadDim);
-                    lo2 = __ldg(q + c);
-                    hi2 = __ldg(q + 16 + c);
+            const float av[4] = {bf16_lo(lo2.x), bf16_hi(lo2.x), bf16_lo(lo2.y), bf16_hi(lo2.y)};
+            const float bv[4] = {bf16_lo(hi2.x), bf16_hi(hi2.x), bf16_lo(hi2.y), bf16_hi(hi2.y)};
+            float am = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) am = fmaxf(am, fmaxf(fabsf(av[u]), fabsf(bv[u])));
+#pragma unroll
+            for (int x = 1; x < 16; x <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, x));
+            // largest element in [128, 256): a rotation keeps it below 363; e = 0 for an all-zero or non-finite head
+            int e = static_cast<int>(__float_as_uint(am) >> 23) - 127;
+            e = (am == 0.f || e == 128) ? 0 : max(-119, e);
+            const float dn = __uint_as_float(static_cast<uint32_t>(134 - e) << 23);   // 2^(7 - e)
+            float x[4], y[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float2 z;
+                if (CHUNK)
+                    rope_cos_sin(a.alibi ? 0 : tl.qpos + tok - off, theta[4 * c + u], z.x, z.y);
+                else
+                    z = angle[4 * c + u];
+                const float xa = av[u] * dn, xb = bv[u] * dn;
+                x[u] = xa * z.x - xb * z.y;
+                y[u] = xb * z.x + xa * z.y;
+            }
+            if (h < rows) {
+#pragma unroll
+                for (int part = 0; part < QP; ++part) {
+                    const int row = part * NG + h;
+                    *reinterpret_cast<uint32_t *>(qd + swz8(row, 4 * c)) = take_part(x);
+                    *reinterpret_cast<uint32_t *>(qd + swz8(row, 64 + 4 * c)) = take_part(y);
                 }
-                const float av[4] = {bf16_lo(lo2.x), bf16_hi(lo2.x), bf16_lo(lo2.y), bf16_hi(lo2.y)};
-                const float bv[4] = {bf16_lo(hi2.x), bf16_hi(hi2.x), bf16_lo(hi2.y), bf16_hi(hi2.y)};
-                float am = 0.f;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) am = fmaxf(am, fmaxf(fabsf(av[u]), fabsf(bv[u])));
-#pragma unroll
-                for (int x = 1; x < 16; x <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, x));
-                // largest element in [128, 256): a rotation keeps it below 363; e = 0 for an all-zero or non-finite head
-                int e = static_cast<int>(__float_as_uint(am) >> 23) - 127;
-                e = (am == 0.f || e == 128) ? 0 : max(-119, e);
-                const float dn = __uint_as_float(static_cast<uint32_t>(134 - e) << 23);   // 2^(7 - e)
-                float x[4], y[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    float2 z;
-                    if (CHUNK)
-                        rope_cos_sin(a.alibi ? 0 : tl.qpos + tok - off, theta[4 * c + u], z.x, z.y);
-                    else
-                        z = angle[4 * c + u];
-                    const float xa = av[u] * dn, xb = bv[u] * dn;
-                    x[u] = xa * z.x - xb * z.y;
-                    y[u] = xb * z.x + xa * z.y;
-                }
-                if (h < rows) {
-#pragma unroll
-                    for (int part = 0; part < QP; ++part) {
-                        const int row = part * NG + h;
-                        *reinterpret_cast<uint32_t *>(qd + swz8(row, 4 * c)) = take_part(x);
-                        *reinterpret_cast<uint32_t *>(qd + swz8(row, 64 + 4 * c)) = take_part(y);
-                    }
-                    if (c == 0) h_hm[32 * qbuf + h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.scale_log2 * 0x1p-7f);
-                }
+                if (c == 0) h_hm[32 * qbuf + h] = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * (a.scale_log2 * 0x1p-7f);
             }
             if (threadIdx.x >= rows && threadIdx.x < 32) h_hm[32 * qbuf + threadIdx.x] = 0.f;
             fence_proxy_async_smem();
