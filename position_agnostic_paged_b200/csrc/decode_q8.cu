@@ -39,7 +39,7 @@
 // What bounds it: HBM for long tables with few rows (64 requests of 4161 tokens, 32 heads on 8: 548 MB in 106 us
 // with the joining kernel, 5.2 TB/s, 79 % of the copy rate), the chain of a tile (scores, references, weights'
 // parts, about 1900 cycles with 4 rows) and its instructions where rows are many (32 heads with block mass:
-// 117 us, 57 % of issue slots).
+// 120 us, 57 % of issue slots).
 #include <climits>
 
 #include "common.cuh"
