@@ -634,7 +634,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
             if (!warp_wait(&bars[B_IFULL + is], (j / kInfoStages) & 1, abort_flag, p.d_status)) break;
             const TileInfo &ti = info[is];
             if (ti.n == 0) {
-                // the end, for the MMA issuers
+                // The end, for the MMA issuers.  As before a tile's keys: they have seen the stage's last phase, so
+                // that none of them waits for one that is two phases back (a walk of two tiles could end before
+                // the query lets them see the first).
+                if (!warp_wait(&bars[B_KEMPTY + st], ((j / kStages) & 1) ^ 1, abort_flag, p.d_status)) break;
                 if (lane == 0) mbar_arrive(&bars[B_KFULL + st]);
                 break;
             }
