@@ -536,10 +536,11 @@ __global__ void __launch_bounds__(JOIN > 1 ? 32 * JOIN : 128) lane_combine_kerne
                 A.w += v.w;
             }
         }
-        // A is relative to 2^MO, L to 2^M (fminf only keeps an overflow of the factor from making 0 * inf)
-        const float f = fast_exp2(fminf(mou - mu, 126.f)), inv = L > 0.f || L != L ? 1.f / L : 0.f;
+        // A is relative to 2^MO, L to 2^M; 2^(MO - M) may pass the range of a float where the output does not: as a square
+        const float f = fast_exp2(0.5f * fminf(fmaxf(mou - mu, -250.f), 250.f)), inv = L > 0.f || L != L ? 1.f / L : 0.f;
+        auto value = [&](float x) { return x * inv * f * f; };
         reinterpret_cast<uint2 *>(a.out + row * kHeadDim)[lane] =
-            make_uint2(pack_bf16(A.x * inv * f, A.y * inv * f), pack_bf16(A.z * inv * f, A.w * inv * f));
+            make_uint2(pack_bf16(value(A.x), value(A.y)), pack_bf16(value(A.z), value(A.w)));
     } else {
         extern __shared__ float z[];   // [Hq]
         const int c0 = (blockIdx.y - out_ctas) * kMassWords;

@@ -103,8 +103,8 @@ struct Cfg {
 // small state, from kOffState
 constexpr int kOffTile = 0;                                      // records
 constexpr int kOffBars = kOffTile + kRecords * static_cast<int>(sizeof(Tile));
-constexpr int kOffHead = kOffBars + 256;                         // mu, dm, dv, step of O, hm of two Q buffers, slope, token: [32] each
-constexpr int kOffRed = kOffHead + 8 * 128;                      // [2][4][32] reductions
+constexpr int kOffHead = kOffBars + 256;                         // mu, dm, step of O, hm of two Q buffers, slope, token: [32] each
+constexpr int kOffRed = kOffHead + 7 * 128;                      // [2][4][32] reductions
 constexpr int kOffAngle = kOffRed + 1024;                        // [64] float2, or [64] double
 constexpr int kOffMisc = kOffAngle + 512;
 static_assert(kOffMisc + 16 <= 4096, "state");
@@ -201,8 +201,8 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
     uint64_t *bars = reinterpret_cast<uint64_t *>(state + kOffBars);
     uint64_t *full = bars, *empty = bars + 4, *ifull = bars + 8, *iempty = bars + 12, *qready = bars + 16, *sfull = bars + 18,
              *pready = bars + 20, *odone = bars + 22, *drain = bars + 24;
-    float *h_mu = reinterpret_cast<float *>(state + kOffHead), *h_dm = h_mu + 32, *h_dv = h_mu + 64, *h_step = h_mu + 96,
-          *h_hm = h_mu + 128, *h_slope = h_mu + 192, *h_tok = h_mu + 224;
+    float *h_mu = reinterpret_cast<float *>(state + kOffHead), *h_dm = h_mu + 32, *h_step = h_mu + 64,
+          *h_hm = h_mu + 96, *h_slope = h_mu + 160, *h_tok = h_mu + 192;
     float(*red)[32] = reinterpret_cast<float(*)[32]>(state + kOffRed), (*red_o)[32] = red + 4;
     float2 *angle = reinterpret_cast<float2 *>(state + kOffAngle);
     double *theta = reinterpret_cast<double *>(state + kOffAngle);   // CHUNK
@@ -558,7 +558,6 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             if (threadIdx.x < 32) {
                 h_mu[threadIdx.x] = 0.f;
                 h_dm[threadIdx.x] = INFINITY;
-                h_dv[threadIdx.x] = 0.f;
             }
         };
         open();
@@ -579,7 +578,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             const bool vis = slot < lim;
             // the first row here, from g0 on, that sees the key
             const int seer = CHUNK ? min(max(tl.pos[blk] + slot - tl.qpos, 0), kFewRows) * a.group - hg - g0 : 0;
-            const float ks = tl.ks[blk], vs = tl.vs[blk], lv = log2_of(vs);
+            const float ks = tl.ks[blk], lv = log2_of(tl.vs[blk]);
             const float dpos = a.alibi ? static_cast<float>(tl.pos[blk] + slot - tl.qpos) : 0.f;
             const bool got = warp_wait(&sfull[buf], (i >> 1) & 1, abort_flag, a.d_status) &&
                              warp_wait(&ifull[(i + 1) % kRecords], ((i + 1) / kRecords) & 1, abort_flag, a.d_status);
@@ -647,8 +646,6 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                         if (!none) {
                             h_mu[gh] = mu + top[h];
                             h_dm[gh] = mu + top[h] - mo;
-                            // weights times 2^7; 2^-20 of it later, as s_v spans the range of a float
-                            h_dv[gh] = fast_exp2(fminf(mu + top[h] - mo - 13.f, 126.f));
                         }
                     }
                 }
@@ -687,21 +684,22 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&qready[buf ^ 1]);
             }
-            // ---- weights, their sums, and their parts as the P operand
-#pragma unroll
-            for (int h = 0; h < HT; ++h) {
-                x[h] = fast_exp2(x[h]);
-                l[h] += x[h];
-            }
+            // ---- weights, their sums, and their parts as the P operand: 2^7 2^(s + log2 s_v - mo).  The V scale joins in
+            // the exponent: as factors, a scale and the references' difference over- or underflow each for itself where
+            // scales span the range of a float.
             uint8_t *pd = sm + C::kOffP + buf * C::kPBytes;
             float w[HT / 4][4];
 #pragma unroll
             for (int h = 0; h < HT; h += 4) {
-                const float4 dv = *reinterpret_cast<const float4 *>(&h_dv[g0 + h]);
-                const float dv4[4] = {dv.x, dv.y, dv.z, dv.w};
+                const float4 d = *reinterpret_cast<const float4 *>(&h_dm[g0 + h]);
+                const float dm4[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    w[h / 4][y] = vis && !(CHUNK && h + y < seer) ? x[h + y] * (vs * dv4[y] * 0x1p20f) : 0.f;
+                for (int y = 0; y < 4; ++y) {
+                    // (a key that no row sees before the first that one sees: dm is infinite, the score -infinity)
+                    w[h / 4][y] = vis && !(CHUNK && h + y < seer) ? fast_exp2(x[h + y] + (lv + 7.f + dm4[y])) : 0.f;
+                    x[h + y] = fast_exp2(x[h + y]);
+                    l[h + y] += x[h + y];
+                }
             }
 #pragma unroll
             for (int part = 0; part < kPP; ++part) {

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from position_agnostic_paged_b200 import lazy_attn as la
-from tests._q8_cases import U_F16, PoolCase, check
+from tests._q8_cases import U_BF16, U_F16, PoolCase, check
 
 pytestmark = pytest.mark.gpu
 
@@ -27,4 +27,69 @@ def test_prefill_of_short_walks(segs, tokens):
     check(out[:2 * tokens], *few.reference(**PREFILL_U)[:2], f"prefill of {tokens} tokens over {len(segs)} short walks")
     for _ in range(20):
         assert torch.equal(c.prefill(), out)
+    assert c.dev["status"].item() == 0
+
+
+# ------------------------------------------------------------------------------- scales far from 1
+def _attend_all(c, what, u=None):
+    """Decode with and without block mass, and prefill (the decode's kernel for up to 16 rows, the prefill's above)."""
+    ref, bound, mref, mbound = c.reference(**(u or {}))
+    c.to()
+    check(c.decode(), ref, bound, f"decode {what}", rel=np.inf)
+    m = torch.zeros(c.words.size, device="cuda")
+    check(c.decode(m), ref, bound, f"decode with mass {what}", rel=np.inf)
+    check(m, mref, mbound, f"mass {what}", rel=np.inf)
+    check(c.prefill(), *c.reference(**(u or PREFILL_U))[:2], f"prefill {what}", rel=np.inf)
+    assert c.dev["status"].item() == 0
+
+
+@pytest.mark.parametrize("hq", [2, 8, 10, 40])
+@pytest.mark.parametrize("v_exp", [(119, 126), (-126 + 6, 126), (110, 126)])
+def test_largest_value_scales(v_exp, hq):
+    """V scales up to 2^119, the largest that a write makes of bf16 values, beside each other and beside the smallest."""
+    reqs = [([(0, 0), (1, 100)], 150, 1), ([(2, 0)], 40, 1), ([(1, 0), (0, 60)], 159, 1)]
+    _attend_all(PoolCase(la.Cfg(hq, 2), [100, 60, 33], reqs, seed=hq, v_exp=v_exp), f"V scales 2^{v_exp}, {hq} heads")
+
+
+@pytest.mark.parametrize("hq", [4, 20])
+def test_value_scales_at_the_end_of_a_float(hq):
+    """Scales of 2^127 and 1.5 x 2^127 times codes of at most 1: values that bf16 holds."""
+    c = PoolCase(la.Cfg(hq, 1), [40, 40], [([(0, 0), (1, 40)], 79, 1), ([(1, 0)], 20, 1)], seed=1)
+    rng = np.random.default_rng(0)
+    one = np.array([0x38, 0x30, 0xB8, 0x00], np.uint8)                        # 1, 0.5, -1, 0
+    live = (np.arange(16) < (c.meta & 255)[:, None])[:, None, :, None]
+    c.v_codes = np.where(live, one[rng.integers(0, 4, c.v_codes.shape)], c.v_codes)
+    c.v_scale[:] = 2.0 ** 127
+    c.v_scale[c.doc_blocks[1]] = 1.5 * 2.0 ** 127
+    _attend_all(c, f"V scales 2^127, {hq} heads")
+
+
+@pytest.mark.parametrize("order", [0, 1])
+@pytest.mark.parametrize("hq,n", [(4, 1), (4, 4), (8, 2), (16, 1), (16, 20)])
+def test_small_weight_times_large_values(hq, n, order):
+    """A block whose weights are about 2^-130, below the smallest float, with values about 2^127: it
+    contributes like the near blocks of ordinary values.  Scores come from ALiBi alone (a query of zeros)."""
+    slope, far = 0.05, 1800                                                   # 0.05 x 1800 x log2 e = 130
+    segs = [[(0, 0), (1, far)], [(1, far), (0, 0)]][order]
+    c = PoolCase(la.Cfg(hq, 1, alibi_slopes=(slope,) * hq), [16, 32], [(segs, far + 40, n), ([(1, 0)], 31, 1)], seed=2, k_exp=(0, 1))
+    c.v_scale[c.doc_blocks[0]] = 2.0 ** 119
+    c.v_scale[c.doc_blocks[1]] = 2.0 ** -5
+    c.q.zero_()
+    ref, _, mref, mbound = c.reference()
+    codes, c.v_codes = c.v_codes, c.v_codes & 0x7F
+    total = c.reference()[0]                                                  # sum of weight times |value|
+    c.v_codes = codes
+    # The scores have no error but the bias's rounding to float (2^-16 of the largest is taken for it), the weights
+    # 2^-11 as f16 (parts of e4m3: less) and 2^-14 for their exponents, sums of numbers up to 256 in fp32, and
+    # for what underflows f16 (48 keys x 2^-24 of the largest product); the output is rounded to bf16.
+    bound = 1.02 * ((np.expm1(2 * slope * (far + 60) * 2.0 ** -16) + U_F16 + 2.0 ** -14) * total + U_BF16 * np.abs(ref))
+    assert np.abs(ref[:n]).mean() > 20 * bound[:n].mean()
+    c.to()
+    what = f"far values of 2^127, {hq} heads"
+    if n == 1:
+        check(c.decode(), ref, bound, f"decode {what}", rel=np.inf)
+        m = torch.zeros(c.words.size, device="cuda")
+        check(c.decode(m), ref, bound, f"decode with mass {what}", rel=np.inf)
+        check(m, mref, mbound, f"mass {what}", rel=np.inf)
+    check(c.prefill(), ref, bound, f"prefill of {n} tokens, {what}", rel=np.inf)
     assert c.dev["status"].item() == 0
