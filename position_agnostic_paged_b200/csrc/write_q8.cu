@@ -118,15 +118,19 @@ __device__ __forceinline__ uint2 code_row(const Q8WriteParams &p, const float (&
     for (int u = 0; u < 8; ++u) y[u] = x[u] * inv;
     uint2 code;
     if (KEY || err != 0.f) {
-        // codes of both ends of the error interval: they differ where it holds a rounding border
-        float e[4];
+        // Codes of both ends of the error interval: they differ where it holds a rounding border.  A key's error is
+        // that of its pair; a value's is its own (its partner may be NaN or infinite).
+        float e[8];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) e[u] = (fabsf(y[u]) + fabsf(y[u + 4])) * err;
+        for (int u = 0; u < 4; ++u) {
+            e[u] = (KEY ? fabsf(y[u]) + fabsf(y[u + 4]) : fabsf(y[u])) * err;
+            e[u + 4] = KEY ? e[u] : fabsf(y[u + 4]) * err;
+        }
         code.x = f32_to_codes(y[0] + e[0], y[1] + e[1], y[2] + e[2], y[3] + e[3]);
-        code.y = f32_to_codes(y[4] + e[0], y[5] + e[1], y[6] + e[2], y[7] + e[3]);
+        code.y = f32_to_codes(y[4] + e[4], y[5] + e[5], y[6] + e[6], y[7] + e[7]);
         if (code.x != f32_to_codes(y[0] - e[0], y[1] - e[1], y[2] - e[2], y[3] - e[3]))
             code.x = codes_f64<KEY>(p, t, j, h, c, 0, scale);
-        if (code.y != f32_to_codes(y[4] - e[0], y[5] - e[1], y[6] - e[2], y[7] - e[3]))
+        if (code.y != f32_to_codes(y[4] - e[4], y[5] - e[5], y[6] - e[6], y[7] - e[7]))
             code.y = codes_f64<KEY>(p, t, j, h, c, 1, scale);
     } else {
         code.x = f32_to_codes(y[0], y[1], y[2], y[3]);

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from position_agnostic_paged_b200 import lazy_attn as la
-from tests._q8_cases import U_BF16, U_F16, PoolCase, check
+from tests._q8_cases import BLK, D, U_BF16, U_F16, PoolCase, bf16, check, write_reference
+from tests.test_gpu_q8 import _device_pool, _same_pool, _state, _write
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +94,24 @@ def test_small_weight_times_large_values(hq, n, order):
         check(m, mref, mbound, f"mass {what}", rel=np.inf)
     check(c.prefill(), ref, bound, f"prefill of {n} tokens, {what}", rel=np.inf)
     assert c.dev["status"].item() == 0
+
+
+# -------------------------------------------------------------------------------------------- write
+@pytest.mark.parametrize("n", [12, 1300])
+@pytest.mark.parametrize("odd", [float("nan"), float("inf"), float("-inf")])
+def test_write_beside_nan_and_infinity(odd, n):
+    """A NaN or infinite value where the block's old scale is no power of two: its partner 64 dims away, like every
+    other element, is stored as it is alone."""
+    rng = np.random.default_rng(n)
+    nb = n // BLK + 2
+    st = _state(nb, 2, 4, [6] + [3] * (nb - 1))
+    for b in range(1, nb):
+        st["meta"][b] = b << 8 | 3
+    st["k_scale"], st["v_scale"] = st["k_scale"] * np.float32(1.37), st["v_scale"] * np.float32(0.77)
+    j = 6 + np.arange(n)
+    k, v = bf16(rng.standard_normal((n, 2, D)) * 0.05), bf16(rng.standard_normal((n, 2, D)) * 0.05)
+    v[np.arange(n), :, np.arange(n) * 7 % D] = odd
+    cfg = la.Cfg(2, 2)
+    pool = _device_pool(st)
+    assert _write(cfg, pool, k, v, j, j) == 0
+    _same_pool(pool, write_reference(cfg, st, k, v, j, j))
