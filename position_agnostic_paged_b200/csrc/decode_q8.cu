@@ -40,7 +40,9 @@
 // with the joining kernel, 5.2 TB/s, 79 % of the copy rate), the chain of a tile (scores, references, weights'
 // parts, about 1900 cycles with 4 rows) and its instructions where rows are many (32 heads with block mass:
 // 120 us, 57 % of issue slots).
+#include <cfloat>
 #include <climits>
+#include <cmath>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -523,10 +525,12 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             for (int u = 0; u < 4; ++u) am = fmaxf(am, fmaxf(fabsf(av[u]), fabsf(bv[u])));
 #pragma unroll
             for (int x = 1; x < 16; x <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, x));
-            // largest element in [128, 256): a rotation keeps it below 363; e = 0 for an all-zero or non-finite head
+            // largest element in [128, 256): a rotation keeps it below 363; e = 0 for an all-zero head.  A head with an
+            // infinite element becomes NaN (codes have no infinity, its parts would be finite).
+            const bool inf = am > FLT_MAX;
             int e = static_cast<int>(__float_as_uint(am) >> 23) - 127;
-            e = (am == 0.f || e == 128) ? 0 : max(-119, e);
-            const float dn = __uint_as_float(static_cast<uint32_t>(134 - e) << 23);   // 2^(7 - e)
+            e = (am == 0.f || inf) ? 0 : max(-119, e);
+            const float dn = inf ? NAN : __uint_as_float(static_cast<uint32_t>(134 - e) << 23);   // 2^(7 - e)
             float x[4], y[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {

@@ -36,7 +36,9 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
+#include <cmath>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -795,10 +797,12 @@ __global__ void __launch_bounds__(256) prefill_q8_query_kernel(const __grid_cons
         for (int u = 0; u < 4; ++u) am = fmaxf(am, fmaxf(fabsf(a[u]), fabsf(b[u])));
 #pragma unroll
         for (int x = 1; x < 16; x <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, x));
-        // q 2^-e in [1, 2); e = 0 for an all-zero or non-finite row
+        // q 2^-e in [1, 2); e = 0 for an all-zero row.  A row with an infinite element becomes NaN, as its softmax
+        // is (scores of -infinity alone would read as keys that it does not see).
+        const bool inf = am > FLT_MAX;
         int e = static_cast<int>(__float_as_uint(am) >> 23) - 127;
-        e = (am == 0.f || e == 128) ? 0 : max(-126, min(126, e));
-        const float dn = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        e = (am == 0.f || inf) ? 0 : max(-126, min(126, e));
+        const float dn = inf ? NAN : __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         float x[4], y[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {

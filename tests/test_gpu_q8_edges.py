@@ -115,3 +115,27 @@ def test_write_beside_nan_and_infinity(odd, n):
     pool = _device_pool(st)
     assert _write(cfg, pool, k, v, j, j) == 0
     _same_pool(pool, write_reference(cfg, st, k, v, j, j))
+
+
+# ------------------------------------------------------------------------------ queries that are not finite
+@pytest.mark.parametrize("odd", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("q8,n", [(True, 1), (True, 4), (True, 5), (True, 40), (False, 1)])
+def test_query_with_an_infinite_element(q8, n, odd):
+    """A head whose query has an infinite or NaN element has NaN as output if it sees a key, and no other does."""
+    reqs = [([(0, 0), (1, 60)], 100, n), ([(1, 0)], 20, n), ([(2, 7)], 7, n), ([(2, 500)], 400, n)]
+    c = PoolCase(la.Cfg(8, 2), [60, 50, 1], reqs, seed=3, q8=q8)
+    u = dict(u_qk=2.0 ** -22, u_p=U_BF16) if not q8 else PREFILL_U if n > 1 else {}
+    ref, bound, mref, mbound = c.reference(**u)
+    # the last sees nothing, the third one key (with which half of all infinite scores are -infinity)
+    seen = [(0, 3), (2 * n - 1, 0)] + [(3 * n - 1, h) for h in range(8)]
+    for row, h in seen + [(3 * n, 1)]:
+        c.q[row, h, 5 + h] = odd
+    c.to()
+    outs = [c.prefill()] if n > 1 else [c.decode(torch.zeros(c.words.size, device="cuda"))] + ([c.decode()] if q8 else [])
+    for out in outs:
+        assert out[[r for r, _ in seen], [h for _, h in seen]].isnan().all()
+        out, want, b = out.clone(), ref.copy(), bound.copy()
+        for row, h in seen:
+            out[row, h], want[row, h] = 0.0, 0.0
+        check(out, want, b, f"rows beside one with {odd}")
+        assert (out[3 * n:] == 0).all()
