@@ -413,6 +413,9 @@ class Q8Pool:
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
             _take(name, t, _F32, (nb, hkv))
         _take("blk_meta", blk_meta, _WORD, (nb,))
+        dev = k_codes.device   # the calls look at k_codes alone
+        if not v_codes.device == k_scale.device == v_scale.device == blk_meta.device == dev:
+            raise ValueError("all tensors of a pool must be on one device")
         self.k_codes, self.v_codes, self.k_scale, self.v_scale, self.blk_meta = k_codes, v_codes, k_scale, v_scale, blk_meta
         self.num_blocks, self.num_kv_heads = nb, hkv
 
