@@ -385,6 +385,15 @@ def _take(name: str, t, dtypes: tuple, shape: tuple | None = None):
                      + f", not {t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}")
 
 
+def _take_aux(workspace, d_status):
+    # (an expanded workspace has fewer bytes than elements)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor")
+    if d_status is not None and (d_status.dtype not in _WORD or d_status.numel() < 1):
+        raise ValueError(f"d_status must be a tensor of {' or '.join(map(str, _WORD))} with an element, not {d_status.dtype} "
+                         f"{tuple(d_status.shape)}")
+
+
 def _launch(name: str, fn, ts, stream, *args):
     """fn(*args, stream) on the tensors' device, which need not be the current one."""
     dev = ts[0].get_device()
@@ -451,6 +460,7 @@ def kv_write_q8(cfg: Cfg, k_raw, v_raw, slot, local_j, pool: Q8Pool, workspace=N
         _take(name, t, _I32)
     if local_j.numel() != n:
         raise ValueError("slot and local_j must have one element per token")
+    _take_aux(workspace, d_status)
     _launch("lazy_kv_write_q8", _lib.lazy_kv_write_q8,
             (k_raw, v_raw, slot, local_j, pool.k_codes, workspace, d_status), stream,
             ctypes.byref(c), _ptr(k_raw), _ptr(v_raw), n, _ptr(slot), _ptr(local_j), ctypes.byref(q),
@@ -485,6 +495,7 @@ def decode_attn_q8(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: int, 
     c, q = cfg._shared_c(), pool.c()
     _heads(cfg, pool)
     n = _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass)
+    _take_aux(workspace, d_status)
     _launch("lazy_decode_attn_q8", _lib.lazy_decode_attn_q8,
             (q_raw, q_pos, table, table_indptr, pool.k_codes, out, workspace, block_mass, d_status), stream,
             ctypes.byref(c), _ptr(q_raw), _ptr(q_pos), n, _ptr(table), _ptr(table_indptr), int(max_words),
@@ -506,6 +517,7 @@ def decode_attn_mass(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: int
     for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
         _take(name, t, _BF16, (nb, cfg.num_kv_heads, 16, 128))
     _take("blk_meta", blk_meta, _WORD, (nb,))
+    _take_aux(workspace, d_status)
     _launch("lazy_decode_attn_mass", _lib.lazy_decode_attn_mass,
             (q_raw, q_pos, table, table_indptr, blk_meta, k_pool, v_pool, out, block_mass, workspace, d_status), stream,
             ctypes.byref(c), _ptr(q_raw), _ptr(q_pos), n, _ptr(table), _ptr(table_indptr), int(max_words),
@@ -533,6 +545,7 @@ def prefill_attn_q8(cfg: Cfg, q_raw, cu_q, q_pos0, max_q: int, table, table_indp
     _take("table", table, _WORD)
     if cu_q.numel() != n + 1 or table_indptr.numel() != n + 1:
         raise ValueError("cu_q and table_indptr must have one element more than q_pos0")
+    _take_aux(workspace, d_status)
     _launch("lazy_prefill_attn_q8", _lib.lazy_prefill_attn_q8,
             (q_raw, cu_q, q_pos0, table, table_indptr, pool.k_codes, out, workspace, d_status), stream,
             ctypes.byref(c), _ptr(q_raw), _ptr(cu_q), _ptr(q_pos0), n, total_q, int(max_q), _ptr(table),
@@ -558,6 +571,7 @@ def evict_blocks(table, table_indptr, max_words: int, block_mass, keep, n_first:
         raise ValueError("block_mass must have one element per table word")
     if min([words] + [t.numel() for t in (table_out, mass_out, evicted) if t is not None]) < words:
         raise ValueError("table_out, mass_out and evicted need room for every table word")
+    _take_aux(None, d_status)
     _launch("lazy_evict_blocks", _lib.lazy_evict_blocks,
             (table, table_indptr, block_mass, keep, table_out, indptr_out, mass_out, evicted, d_status), stream,
             _ptr(table), _ptr(table_indptr), n, int(max_words), _ptr(block_mass), _ptr(keep), int(n_first),

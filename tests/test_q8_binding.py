@@ -15,3 +15,31 @@ def test_pool_members_are_on_one_device(name):
     parts[name] = parts[name].to("meta")
     with pytest.raises(ValueError):
         la.Q8Pool(**parts)
+
+
+def _calls(ws, status):
+    """Every call with arguments that pass all other checks but the last, that the tensors are on a GPU."""
+    cfg, pool = la.Cfg(8, 2), la.Q8Pool.empty(4, 2, device="cpu")
+    i = lambda *a: torch.tensor(a, dtype=torch.int32)                                    # noqa: E731
+    q, x, f = torch.zeros(1, 8, 128).bfloat16(), torch.zeros(1, 2, 128).bfloat16(), torch.zeros(2)
+    kv = torch.zeros(4, 2, 16, 128).bfloat16()
+    return dict(
+        write=lambda: la.kv_write_q8(cfg, x, x, i(0), i(0), pool, ws, status),
+        decode=lambda: la.decode_attn_q8(cfg, q, i(0), i(0, 1), i(0, 2), 2, pool, q, ws, None, status),
+        mass=lambda: la.decode_attn_mass(cfg, q, i(0), i(0, 1), i(0, 2), 2, pool.blk_meta, kv, kv, q, f, ws, status),
+        prefill=lambda: la.prefill_attn_q8(cfg, q, i(0, 1), i(0), 1, i(0, 1), i(0, 2), 2, pool, q, ws, status),
+        evict=lambda: la.evict_blocks(i(0, 1), i(0, 2), 2, f, i(1), 0, 0, i(0, 0), i(0, 0), f.clone(), None, status))
+
+
+@pytest.mark.parametrize("call", ["write", "decode", "mass", "prefill", "evict"])
+def test_workspace_and_status_are_what_they_seem(call):
+    good, status = torch.empty(1 << 20, dtype=torch.uint8), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        _calls(good, status)[call]()
+    if call != "evict":
+        for ws in (torch.empty(1, dtype=torch.uint8).expand(1 << 20), torch.empty(1 << 12, dtype=torch.uint8)[::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                _calls(ws, status)[call]()
+    for st in (torch.zeros(1, dtype=torch.int64), torch.zeros(1, dtype=torch.uint8), torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="d_status"):
+            _calls(good, st)[call]()
