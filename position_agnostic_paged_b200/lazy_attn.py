@@ -13,7 +13,6 @@ import os
 from dataclasses import dataclass
 
 import numpy as np
-import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblazy_attn.so")
@@ -195,15 +194,31 @@ def _ptr(t) -> int | None:
     return int(t.data_ptr())
 
 
-# the current stream's handle without making a Stream object (0.2 us against 3 us), where torch has it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+class _LazyTorch:
+    """What the calls need of torch, imported by the first that does: the codec, the tables and the block cache
+    work without it."""
+
+    def __getattr__(self, name):
+        import torch
+        self.cuda = torch.cuda
+        # the current stream's handle without making a Stream object (0.2 us against 3 us), where torch has it
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.bf16, self.f32, self.i32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+        self.word, self.code = (torch.int32, torch.uint32), (torch.uint8, torch.float8_e4m3fn)
+        self.torch = torch
+        if name not in self.__dict__:
+            raise AttributeError(name)
+        return self.__dict__[name]
+
+
+_t = _LazyTorch()
 
 
 def _stream(stream) -> int | None:
     if stream is None:
-        if _raw_stream is not None:
-            return int(_raw_stream(torch.cuda.current_device())) or None
-        return int(torch.cuda.current_stream().cuda_stream) or None
+        if _t.raw_stream is not None:
+            return int(_t.raw_stream(_t.cuda.current_device())) or None
+        return int(_t.cuda.current_stream().cuda_stream) or None
     return int(getattr(stream, "cuda_stream", stream)) or None
 
 
@@ -374,9 +389,6 @@ def decode_attn_noalloc(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: 
 # ---- the 8-bit pool, block mass and eviction.  These calls check what the C side cannot see: types
 # (two-byte and four-byte elements would be read as something else), contiguity, shapes and the device.
 
-_BF16, _F32, _I32, _WORD = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int32, torch.uint32)
-
-
 def _take(name: str, t, dtypes: tuple, shape: tuple | None = None):
     if t.dtype in dtypes and t.is_contiguous() and (shape is None or t.shape == shape):
         return
@@ -389,8 +401,8 @@ def _take_aux(workspace, d_status):
     # (an expanded workspace has fewer bytes than elements)
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor")
-    if d_status is not None and (d_status.dtype not in _WORD or d_status.numel() < 1):
-        raise ValueError(f"d_status must be a tensor of {' or '.join(map(str, _WORD))} with an element, not {d_status.dtype} "
+    if d_status is not None and (d_status.dtype not in _t.word or d_status.numel() < 1):
+        raise ValueError(f"d_status must be a tensor of {' or '.join(map(str, _t.word))} with an element, not {d_status.dtype} "
                          f"{tuple(d_status.shape)}")
 
 
@@ -402,10 +414,10 @@ def _launch(name: str, fn, ts, stream, *args):
             raise ValueError("all tensors must be on one device")
     if dev < 0:
         raise ValueError("all tensors must be CUDA tensors")
-    if dev == torch.cuda.current_device():
+    if dev == _t.cuda.current_device():
         _check(name, fn(*args, _stream(stream)))
         return
-    with torch.cuda.device(dev):
+    with _t.cuda.device(dev):
         _check(name, fn(*args, _stream(stream)))
 
 
@@ -418,10 +430,10 @@ class Q8Pool:
     def __init__(self, k_codes, v_codes, k_scale, v_scale, blk_meta):
         nb, hkv = int(k_codes.shape[0]), int(k_codes.shape[1])
         for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
-            _take(name, t, (torch.uint8, torch.float8_e4m3fn), (nb, hkv, 16, 128))
+            _take(name, t, _t.code, (nb, hkv, 16, 128))
         for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            _take(name, t, _F32, (nb, hkv))
-        _take("blk_meta", blk_meta, _WORD, (nb,))
+            _take(name, t, _t.f32, (nb, hkv))
+        _take("blk_meta", blk_meta, _t.word, (nb,))
         dev = k_codes.device   # the calls look at k_codes alone
         if not v_codes.device == k_scale.device == v_scale.device == blk_meta.device == dev:
             raise ValueError("all tensors of a pool must be on one device")
@@ -431,6 +443,7 @@ class Q8Pool:
     @classmethod
     def empty(cls, num_blocks: int, num_kv_heads: int, device="cuda") -> "Q8Pool":
         """A pool whose blocks hold no tokens."""
+        torch = _t.torch
         codes = lambda: torch.zeros(num_blocks, num_kv_heads, 16, 128, dtype=torch.uint8, device=device)   # noqa: E731
         scale = lambda: torch.ones(num_blocks, num_kv_heads, dtype=torch.float32, device=device)           # noqa: E731
         return cls(codes(), codes(), scale(), scale(), torch.zeros(num_blocks, dtype=torch.int32, device=device))
@@ -455,9 +468,9 @@ def kv_write_q8(cfg: Cfg, k_raw, v_raw, slot, local_j, pool: Q8Pool, workspace=N
     c, q, n = cfg._shared_c(), pool.c(), int(slot.numel())
     _heads(cfg, pool)
     for name, t in (("k_raw", k_raw), ("v_raw", v_raw)):
-        _take(name, t, _BF16, (n, cfg.num_kv_heads, 128))
+        _take(name, t, _t.bf16, (n, cfg.num_kv_heads, 128))
     for name, t in (("slot", slot), ("local_j", local_j)):
-        _take(name, t, _I32)
+        _take(name, t, _t.i32)
     if local_j.numel() != n:
         raise ValueError("slot and local_j must have one element per token")
     _take_aux(workspace, d_status)
@@ -469,15 +482,15 @@ def kv_write_q8(cfg: Cfg, k_raw, v_raw, slot, local_j, pool: Q8Pool, workspace=N
 
 def _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass):
     n = int(q_pos.numel())
-    _take("q_raw", q_raw, _BF16, (n, cfg.num_q_heads, 128))
-    _take("out", out, _BF16, (n, cfg.num_q_heads, 128))
-    _take("q_pos", q_pos, _I32)
-    _take("table", table, _WORD)
-    _take("table_indptr", table_indptr, _I32)
+    _take("q_raw", q_raw, _t.bf16, (n, cfg.num_q_heads, 128))
+    _take("out", out, _t.bf16, (n, cfg.num_q_heads, 128))
+    _take("q_pos", q_pos, _t.i32)
+    _take("table", table, _t.word)
+    _take("table_indptr", table_indptr, _t.i32)
     if table_indptr.numel() != n + 1:
         raise ValueError("table_indptr must have one element more than q_pos")
     if block_mass is not None:
-        _take("block_mass", block_mass, _F32)
+        _take("block_mass", block_mass, _t.f32)
         if block_mass.numel() != table.numel():
             raise ValueError("block_mass must have one element per table word")
     return n
@@ -515,8 +528,8 @@ def decode_attn_mass(cfg: Cfg, q_raw, q_pos, table, table_indptr, max_words: int
     n = _decode_args(cfg, q_raw, q_pos, table, table_indptr, out, block_mass)
     nb = int(k_pool.shape[0])
     for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-        _take(name, t, _BF16, (nb, cfg.num_kv_heads, 16, 128))
-    _take("blk_meta", blk_meta, _WORD, (nb,))
+        _take(name, t, _t.bf16, (nb, cfg.num_kv_heads, 16, 128))
+    _take("blk_meta", blk_meta, _t.word, (nb,))
     _take_aux(workspace, d_status)
     _launch("lazy_decode_attn_mass", _lib.lazy_decode_attn_mass,
             (q_raw, q_pos, table, table_indptr, blk_meta, k_pool, v_pool, out, block_mass, workspace, d_status), stream,
@@ -538,11 +551,11 @@ def prefill_attn_q8(cfg: Cfg, q_raw, cu_q, q_pos0, max_q: int, table, table_indp
     c, q = cfg._shared_c(), pool.c()
     _heads(cfg, pool)
     n, total_q = int(q_pos0.numel()), int(q_raw.shape[0])
-    _take("q_raw", q_raw, _BF16, (total_q, cfg.num_q_heads, 128))
-    _take("out", out, _BF16, (total_q, cfg.num_q_heads, 128))
+    _take("q_raw", q_raw, _t.bf16, (total_q, cfg.num_q_heads, 128))
+    _take("out", out, _t.bf16, (total_q, cfg.num_q_heads, 128))
     for name, t in (("cu_q", cu_q), ("q_pos0", q_pos0), ("table_indptr", table_indptr)):
-        _take(name, t, _I32)
-    _take("table", table, _WORD)
+        _take(name, t, _t.i32)
+    _take("table", table, _t.word)
     if cu_q.numel() != n + 1 or table_indptr.numel() != n + 1:
         raise ValueError("cu_q and table_indptr must have one element more than q_pos0")
     _take_aux(workspace, d_status)
@@ -560,11 +573,11 @@ def evict_blocks(table, table_indptr, max_words: int, block_mass, keep, n_first:
     n, words = int(keep.numel()), int(table.numel())
     for name, t in (("table", table), ("table_out", table_out), ("evicted", evicted)):
         if t is not None:
-            _take(name, t, _WORD)
+            _take(name, t, _t.word)
     for name, t in (("block_mass", block_mass), ("mass_out", mass_out)):
-        _take(name, t, _F32)
+        _take(name, t, _t.f32)
     for name, t in (("table_indptr", table_indptr), ("indptr_out", indptr_out), ("keep", keep)):
-        _take(name, t, _I32)
+        _take(name, t, _t.i32)
     if table_indptr.numel() != n + 1 or indptr_out.numel() < n + 1:
         raise ValueError("table_indptr and indptr_out must have one element more than keep")
     if block_mass.numel() != words:

@@ -1,4 +1,8 @@
 """What the binding of the 8-bit pool, block mass and eviction calls refuses before anything is launched."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -43,3 +47,22 @@ def test_workspace_and_status_are_what_they_seem(call):
     for st in (torch.zeros(1, dtype=torch.int64), torch.zeros(1, dtype=torch.uint8), torch.zeros(0, dtype=torch.int32)):
         with pytest.raises(ValueError, match="d_status"):
             _calls(good, st)[call]()
+
+
+def test_codec_tables_and_cache_need_no_torch():
+    """A host program without torch: table words, position tables, workspace sizes, the block cache and its simulation."""
+    code = """
+import sys
+sys.modules["torch"] = None          # import torch raises ImportError
+import numpy as np
+from position_agnostic_paged_b200 import cache_sim, lazy_attn as la, rope
+assert la.pack_words(np.array([3]), np.array([16])).tolist() == [16 << 17 | 3]
+assert len(rope.llama31_theta()) == 64 and rope.alibi_slopes(8)[0] == 0.5
+assert la.decode_q8_workspace_bytes(la.Cfg(8, 2), 2, 4) > 0 and la.decode_noalloc_capacity() > 0
+cache = la.BlockCache(8)
+assert cache.access(1, 3)[0] is False and cache.access(1, 3)[0] is True
+assert cache_sim.simulate("agnostic", [16, 16], [[0, 1], [1, 0]], 4)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
