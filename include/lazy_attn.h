@@ -291,7 +291,7 @@ size_t lazy_kv_write_q8_workspace_bytes(const lazy_attn_cfg *cfg, int n_tok, int
  * x = v_raw[t][h][:] for values, every block that the call writes to gets, per head,
  *   scale = max(old scale if blk_meta says that the block holds tokens,
  *               the least power of two s >= 2^-126 with |x| <= 448 s over the call's tokens),
- *   code  = e4m3(x / scale), rounded to nearest even,
+ *   code  = e4m3(float(x / scale)), rounded to float and then to e4m3, each to nearest even,
  * and where the scale grew, the earlier tokens' codes (slots below n_valid that the call does
  * not write) become e4m3(value / scale): exact, but for values that fall below the new scale's
  * normal range.  Other slots keep their codes.  Infinite elements are stored as +-448 scale and

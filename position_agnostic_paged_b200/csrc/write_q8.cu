@@ -2,7 +2,7 @@
 //
 // Per (block, KV head) that the call writes to, with x = RoPE(k, j) or v over the call's tokens there:
 //   s = max(s_old if the block holds tokens, least 2^e >= 2^-126 with max |x| <= 448 2^e),
-//   code = e4m3_rne(x / s),  earlier tokens' codes = e4m3_rne(code s_old / s) where s grew.
+//   code = e4m3_rne(float_rne(x / s)),  earlier tokens' codes = e4m3_rne(code s_old / s) where s grew.
 //
 // One owner (a CTA or a warp) writes all of a block's tokens, so scales, rescaled codes and metadata need
 // no atomics on the pool and no order of execution enters the result.
@@ -19,8 +19,8 @@
 // cache (32768 tokens x 8 heads: 118 us, now 79; 202 MB, 2.5 TB/s).  Bound by instructions: 36.8 M of them,
 // half the issue slots, a third each for angles and rotation, scales, and codes with their error intervals.
 // Half a warp per token row, 8 elements per lane.  Rotations run in fp32.  Where a code or a scale could
-// depend on fp32 rounding (the error interval holds a rounding border: about one element in 10^5) it is
-// computed again in fp64.
+// depend on the rotation's rounding (the error interval holds a rounding border: some elements in 10^5) it is
+// computed again in fp64.  A code is e4m3_rne(float_rne(x / s)): the quotient is rounded to fp32 first, here as there.
 #include <cfloat>
 
 #include "common.cuh"
@@ -35,11 +35,13 @@ namespace {
 constexpr int kThreads = 256;           // small calls
 constexpr int kGroup = 16;              // large calls: tokens per CTA
 constexpr int kBulkWarps = 4;
-// |x in fp32 - x| relative to |x0| + |x1| >= (|a| + |b|) / sqrt(2) of the rotated pair.  Small calls: cos and sin to
-// 2.4e-7 (angle rounded to fp32, sincosf to 2 ulp), two products and a sum of half an ulp (6e-8) each.  Large
-// calls: cos and sin from fp64, so half an ulp (3e-8 below 1), a product and a sum of 3e-8: 9e-8 sqrt(2).
-// Their ninefold finer interval makes the fp64 path, a third of the time otherwise, rare.
-constexpr float kErrSmall = 7.1e-7f, kErrLarge = 1.3e-7f;
+// Bounds of |x in fp32 - x| relative to |x0| + |x1| >= r = sqrt(a^2 + b^2) of the rotated pair; u = 2^-24 is half an ulp
+// relative to the least value of its binade, so a rounding is off by up to u |value|.
+// Large calls: cos and sin rounded from fp64 (below 1, so u / 2 absolute each: u / 2 (|a| + |b|) <= 0.71 u r), a
+// product and a sum of at most r (u r each): 2.71 u r = 1.62e-7 r; 1.45e-7 was met.  The interval's ends
+// y -+ e are rounded as well, but monotonically: the float next to x / scale lies between them.
+// Small calls: cos and sin to 2.4e-7 (angle rounded to fp32, sincosf to 2 ulp): 3.4e-7 r, and 2 u r: 4.6e-7 r.
+constexpr float kErrSmall = 7.1e-7f, kErrLarge = 1.7e-7f;
 constexpr float kAmaxErr = 1.5e-6f;     // relative: twice the larger of them, and its own rounding
 
 // biased fp32 exponent of the least power of two s >= 2^-126 with amax <= 448 s

@@ -139,3 +139,32 @@ def test_query_with_an_infinite_element(q8, n, odd):
             out[row, h], want[row, h] = 0.0, 0.0
         check(out, want, b, f"rows beside one with {odd}")
         assert (out[3 * n:] == 0).all()
+
+
+# Pairs (dim i, position, a, b) whose rotated key a cos - b sin lies within half an fp32 ulp of a border between two codes
+# (at base 500000 and scale 1), but not on it
+NEAR_BORDERS = [
+    (16, 43762, 1.5234375, 0.45703125), (11, 7729, 1.421875, -0.169921875), (6, 14393, 1.4140625, -0.259765625),
+    (18, 3240, 1.3046875, 0.2421875), (23, 36115, 1.0703125, 0.1181640625), (17, 47531, 1.7890625, 1.2578125),
+    (16, 25219, 1.5859375, 0.578125), (13, 28760, 1.7421875, -0.23828125), (2, 52631, 1.40625, -1.203125),
+    (5, 18802, 1.4140625, 1.078125), (2, 12948, 1.21875, -1.8046875), (10, 33080, 1.15625, -0.330078125),
+    (22, 28053, 1.0, -0.365234375), (4, 46713, 1.546875, 0.70703125), (13, 35991, 1.5703125, -1.234375),
+    (8, 44164, 1.6328125, -0.1787109375), (1, 33282, 1.0546875, -0.130859375), (12, 20225, 1.859375, 0.2490234375)]
+
+
+@pytest.mark.parametrize("n", [len(NEAR_BORDERS), 1200])
+def test_write_keys_next_to_a_border(n):
+    """The quotient is rounded to fp32 before it is rounded to a code: in these keys that decides."""
+    rng = np.random.default_rng(n)
+    k = bf16(rng.standard_normal((n, 1, D)))
+    j = rng.integers(0, 60000, n)
+    for t, (i, pos, a, b) in enumerate(NEAR_BORDERS):
+        k[t, 0, i], k[t, 0, i + 64], j[t] = a, b, pos
+    k[:, 0, 63], k[:, 0, 127] = 300.0, 0.0                         # the scale is 1
+    slot = np.arange(n) * BLK + j % BLK                            # a block each
+    cfg, st = la.Cfg(1, 1), _state(n, 1, 1, [0] * n)
+    pool = _device_pool(st)
+    assert _write(cfg, pool, k, k, slot, j) == 0
+    want = write_reference(cfg, st, k, k, slot, j)
+    assert (want["k_scale"] == 1).all()
+    _same_pool(pool, want)
