@@ -42,6 +42,8 @@ constexpr int kBulkWarps = 4;
 // y -+ e are rounded as well, but monotonically: the float next to x / scale lies between them.
 // Small calls: cos and sin to 2.4e-7 (angle rounded to fp32, sincosf to 2 ulp): 3.4e-7 r, and 2 u r: 4.6e-7 r.
 constexpr float kErrSmall = 7.1e-7f, kErrLarge = 1.7e-7f;
+// Where product or sum are below the smallest normal number each is off by up to 2^-150 instead.
+constexpr float kErrTiny = 0x1p-148f;
 constexpr float kAmaxErr = 1.5e-6f;     // relative: twice the larger of them, and its own rounding
 
 // biased fp32 exponent of the least power of two s >= 2^-126 with amax <= 448 s
@@ -125,7 +127,7 @@ __device__ __forceinline__ uint2 code_row(const Q8WriteParams &p, const float (&
         float e[8];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            e[u] = (KEY ? fabsf(y[u]) + fabsf(y[u + 4]) : fabsf(y[u])) * err;
+            e[u] = KEY ? fmaf(fabsf(y[u]) + fabsf(y[u + 4]), err, inv * kErrTiny) : fabsf(y[u]) * err;
             e[u + 4] = KEY ? e[u] : fabsf(y[u + 4]) * err;
         }
         code.x = f32_to_codes(y[0] + e[0], y[1] + e[1], y[2] + e[2], y[3] + e[3]);

@@ -168,3 +168,17 @@ def test_write_keys_next_to_a_border(n):
     want = write_reference(cfg, st, k, k, slot, j)
     assert (want["k_scale"] == 1).all()
     _same_pool(pool, want)
+
+
+@pytest.mark.parametrize("n", [200, 1300])
+def test_write_subnormal_keys(n):
+    """Keys of a few times 2^-133, whose products with cos and sin are rounded below fp32's normal range."""
+    rng = np.random.default_rng(n)
+    k = bf16(rng.integers(-20, 21, (n, 4, D)) * 2.0 ** -133)
+    assert float(k.abs().max()) == 20 * 2.0 ** -133
+    cfg, nb = la.Cfg(4, 4), n // BLK + 1
+    st = _state(nb, 4, 1, [0] * nb)
+    j = np.arange(n)
+    pool = _device_pool(st)
+    assert _write(cfg, pool, k, k, j, j) == 0
+    _same_pool(pool, write_reference(cfg, st, k, k, j, j))
