@@ -182,3 +182,25 @@ def test_write_subnormal_keys(n):
     pool = _device_pool(st)
     assert _write(cfg, pool, k, k, j, j) == 0
     _same_pool(pool, write_reference(cfg, st, k, k, j, j))
+
+
+@pytest.mark.parametrize("hkv,n,order", [(3, 1500, "asc"), (5, 1025, "shuffle"), (8, 1500, "asc"), (8, 1500, "shuffle"),
+                                         (11, 1100, "asc"), (11, 1100, "shuffle"), (64, 1025, "asc")])
+def test_large_write_of_many_heads(hkv, n, order):
+    """More than four heads: a warp takes several, its staging buffers again and their phases on; from slot 5 of a
+    partly filled block on, the last block partly filled, some tokens skipped."""
+    rng = np.random.default_rng([n, hkv])
+    nb = (n + 5) // BLK + 3
+    st = _state(nb, hkv, n, [16] + [5] + [0] * (nb - 2))
+    j = BLK + 5 + np.arange(n)
+    slot = j.copy()
+    slot[40:44] = -1
+    slot[70], j[70] = slot[75], j[75]
+    if order == "shuffle":
+        p = rng.permutation(n)
+        j, slot = j[p], slot[p]
+    k, v = bf16(rng.standard_normal((n, hkv, D)) * 2), bf16(rng.standard_normal((n, hkv, D)) * 2.0 ** rng.integers(-9, 3, (n, hkv, 1)))
+    cfg = la.Cfg(hkv, hkv)
+    pool = _device_pool(st)
+    assert _write(cfg, pool, k, v, slot, j) == la.DSTATUS_BAD_SLOT
+    _same_pool(pool, write_reference(cfg, st, k, v, slot, j))
