@@ -190,7 +190,8 @@ struct EvictParams {
     float *mass_out;
     int num_req, max_words, n_first, n_last;
     int *d_status;
+    int scanned;                 // 1: indptr_out holds the new row pointers already
 };
-cudaError_t launch_evict(const EvictParams &p, cudaStream_t s);
+cudaError_t launch_evict(EvictParams p, cudaStream_t s);
 
 }  // namespace lazy

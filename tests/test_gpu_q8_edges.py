@@ -6,7 +6,7 @@ import torch
 
 from position_agnostic_paged_b200 import lazy_attn as la
 from tests._q8_cases import BLK, D, U_BF16, U_F16, PoolCase, bf16, check, write_reference
-from tests.test_gpu_q8 import _device_pool, _same_pool, _state, _write
+from tests.test_gpu_q8 import _check_evict, _device_pool, _same_pool, _state, _write
 
 pytestmark = pytest.mark.gpu
 
@@ -204,3 +204,41 @@ def test_large_write_of_many_heads(hkv, n, order):
     pool = _device_pool(st)
     assert _write(cfg, pool, k, v, slot, j) == la.DSTATUS_BAD_SLOT
     _same_pool(pool, write_reference(cfg, st, k, v, slot, j))
+
+
+# -------------------------------------------------------------------------------------------- evict
+@pytest.mark.parametrize("reqs", [2048, 2049, 8193, 20000])
+def test_evict_of_thousands_of_requests(reqs):
+    """On both sides of the number from which a kernel of its own writes the row pointers, and of its CTAs' shares."""
+    rng = np.random.default_rng(reqs)
+    n = rng.integers(0, 7, reqs)
+    ind = np.concatenate([[3], 3 + np.cumsum(n)])
+    total = int(ind[-1]) + 2
+    assert _check_evict(rng.integers(0, 1 << 32, total, dtype=np.uint32), ind, 5, rng.random(total).astype(np.float32),
+                        rng.integers(-1, 8, reqs), 1, 1) == la.DSTATUS_BAD_TABLE
+
+
+def test_evict_of_the_most_requests():
+    """2^20 requests of no or one word: right, and not in time that grows with their square."""
+    reqs = 1 << 20
+    rng = np.random.default_rng(7)
+    n, keep = rng.integers(0, 2, reqs), rng.integers(0, 2, reqs)
+    t = lambda a, dt: torch.from_numpy(np.ascontiguousarray(np.asarray(a, dt))).cuda()      # noqa: E731
+    ind = np.concatenate([[0], np.cumsum(n)])
+    total = int(ind[-1])
+    table, mass = t(np.arange(total), np.int32), t(rng.random(total), np.float32)
+    out, gone, mo = torch.full_like(table, -1), torch.full_like(table, -1), torch.zeros_like(mass)
+    io, first = torch.full((reqs + 1,), -1, dtype=torch.int32, device="cuda"), t(ind, np.int32)
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    kd = t(keep, np.int32)
+    a.record()
+    la.evict_blocks(table, first, 1, mass, kd, 0, 0, out, io, mo, gone)
+    b.record()
+    torch.cuda.synchronize()
+    stays = (n * keep)[n > 0] > 0                                  # of each word
+    assert np.array_equal(io.cpu().numpy(), np.concatenate([[0], np.cumsum(n * keep)]))
+    k = int(stays.sum())
+    assert np.array_equal(out[:k].cpu().numpy(), np.nonzero(stays)[0]) and (out[k:] == -1).all()
+    assert np.array_equal(gone[:total - k].cpu().numpy(), np.nonzero(~stays)[0]) and (gone[total - k:] == -1).all()
+    assert torch.equal(mo[:k], mass[torch.from_numpy(stays).cuda()])
+    assert a.elapsed_time(b) < 1000.0
