@@ -224,5 +224,8 @@ __device__ __forceinline__ uint32_t word_block(uint32_t w) { return w & (LAZY_MA
 __device__ __forceinline__ int word_offset(uint32_t w) { return static_cast<int>(w >> LAZY_BLOCK_BITS); }
 __device__ __forceinline__ int meta_j0(uint32_t m) { return static_cast<int>(m >> 8) * kBlockTokens; }
 __device__ __forceinline__ int meta_valid(uint32_t m) { return static_cast<int>(m & 0xFFu); }
+// Slots of a block that a query at position q sees: those of its `valid` ones, the first at position pos >= 0, that
+// are not behind it.  For every q (q - pos + 1 overflows at both ends of int).
+__device__ __forceinline__ int seen_slots(int valid, int q, int pos) { return q < pos ? 0 : min(valid - 1, q - pos) + 1; }
 
 }  // namespace lazy

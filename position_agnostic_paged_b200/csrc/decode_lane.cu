@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32, kOcc)
         const int off = word_offset(w);
         const int pos0 = off + meta_j0(meta);
         // keys of this word that the query sees: slots 0 .. lim - 1
-        const int lim = i_req < a.max_words ? min(meta_valid(meta), qpos - pos0 + 1) : 0;
+        const int lim = i_req < a.max_words ? seen_slots(meta_valid(meta), qpos, pos0) : 0;
         float *lse = p.ws_lse + (static_cast<size_t>(r) * a.max_words + i_req) * a.hq + kvh * G;
         if (lim <= 0) {
             if (i_req < a.max_words && lane < 8 && g0 + lane < G) lse[g0 + lane] = -INFINITY;

@@ -344,7 +344,7 @@ __global__ void __launch_bounds__((Cfg<NG, QP>::kThreads), (Cfg<NG, QP>::kOcc)) 
             const int i = k - b0, x = b0 + lane;             // lane `lane` holds word x
             const int pos = word_offset(wl) + meta_j0(ml);
             const bool mine = x >= k && x < cnt && lo + x < r_end;
-            const int lim = mine && lo + x - r_beg < a.max_words ? min(meta_valid(ml), last - pos + 1) : 0;
+            const int lim = mine && lo + x - r_beg < a.max_words ? seen_slots(meta_valid(ml), last, pos) : 0;
             const uint32_t seen = __ballot_sync(0xffffffffu, lim > 0);
             const int here = __popc(__ballot_sync(0xffffffffu, mine));      // words of the request from k on, in this batch
             if (!((seen >> i) & 1u)) {

@@ -493,7 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const uint32_t m = ti.meta[k0 + k];
-                        const int lim = min(meta_valid(m), prow - ti.off - meta_j0(m) + 1);
+                        // (a tile's keys are not all behind the last query, so the difference does not overflow)
+                        const int lim = min(meta_valid(m) - 1, prow - ti.off - meta_j0(m)) + 1;
 #pragma unroll
                         for (int c = 16 * k; c < 16 * k + 16; ++c) sv[c] = (c & 15) < lim ? sv[c] : 0xFF800000u;
                     }
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
             uint32_t keep = 0u;   // bit k: some row may see slot rb of block k
 #pragma unroll
             for (int k = 0; k < kTileBlocks; ++k)
-                keep |= (rb < min(meta_valid(ti.meta[k]), Plast - ti.off - meta_j0(ti.meta[k]) + 1) ? 1u : 0u) << k;
+                keep |= (rb <= min(meta_valid(ti.meta[k]) - 1, Plast - ti.off - meta_j0(ti.meta[k])) ? 1u : 0u) << k;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[B_IEMPTY + is]);
             if (!warp_wait(&bars[B_AFULL + st], (j / kStages) & 1, abort_flag, p.d_status)) break;

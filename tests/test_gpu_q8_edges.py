@@ -242,3 +242,24 @@ def test_evict_of_the_most_requests():
     assert np.array_equal(gone[:total - k].cpu().numpy(), np.nonzero(~stays)[0]) and (gone[total - k:] == -1).all()
     assert torch.equal(mo[:k], mass[torch.from_numpy(stays).cuda()])
     assert a.elapsed_time(b) < 1000.0
+
+
+# ---------------------------------------------------------------------------------------- positions
+@pytest.mark.parametrize("kind", ["rope", "alibi"])
+@pytest.mark.parametrize("hq,q8", [(8, True), (40, True), (8, False)])
+def test_positions_at_the_ends_of_int(hq, q8, kind):
+    """The largest int sees every key, the smallest and -1 (a padded row) none."""
+    top, low = 2 ** 31 - 1, -2 ** 31
+    cfg = la.Cfg(hq, 2) if kind == "rope" else la.Cfg(hq, 2, alibi_slopes=(0.0,) * hq)
+    reqs = [([(0, 0), (1, 100)], p, 1) for p in (top, low, -1, top - 20)] + [([(1, 32767)], p, 1) for p in (low, top, -1)]
+    c = PoolCase(cfg, [100, 37], reqs, seed=hq, q8=q8).to()
+    u = {} if q8 else dict(u_qk=2.0 ** -22, u_p=U_BF16)
+    ref, bound, mref, mbound = c.reference(**u)
+    assert (np.abs(ref).max((1, 2)) > 0).tolist() == [True, False, False, True, False, True, False]
+    m = torch.zeros(c.words.size, device="cuda")
+    check(c.decode(m), ref, bound, f"decode at the last position, {hq} heads {kind} q8={q8}")
+    check(m, mref, mbound, f"mass at the last position, {hq} heads {kind} q8={q8}")
+    if q8:
+        check(c.decode(), ref, bound, f"decode at the last position, {hq} heads {kind}")
+        check(c.prefill(), *c.reference(**PREFILL_U)[:2], f"prefill at the last position, {hq} heads {kind}")
+    assert c.dev["status"].item() == 0
