@@ -73,6 +73,8 @@ class Cfg:
             st._alibi_keepalive = sl
             st.alibi_slopes = ctypes.cast(sl, ctypes.POINTER(ctypes.c_double))
         if self.rope_theta is not None:
+            if len(self.rope_theta) < 64 and self.head_dim == 128:   # (other head sizes are refused before it is read)
+                raise ValueError("rope_theta needs head_dim / 2 = 64 frequencies")
             arr = (ctypes.c_double * len(self.rope_theta))(*[float(x) for x in self.rope_theta])
             st._theta_keepalive = arr
             st.rope_theta = ctypes.cast(arr, ctypes.POINTER(ctypes.c_double))

@@ -49,6 +49,16 @@ def test_workspace_and_status_are_what_they_seem(call):
             _calls(good, st)[call]()
 
 
+def test_a_short_frequency_table_is_refused():
+    """The library reads 64 of them."""
+    for n in (0, 1, 63):
+        cfg = la.Cfg(8, 2, rope_theta=(0.1,) * n)
+        for call in (cfg.c, lambda: la.decode_q8_workspace_bytes(cfg, 1, 1), lambda: la.decode_workspace_bytes(cfg, 1, 1)):
+            with pytest.raises(ValueError):
+                call()
+    assert la.decode_q8_workspace_bytes(la.Cfg(8, 2, rope_theta=(0.1,) * 64), 1, 1) > 0
+
+
 def test_codec_tables_and_cache_need_no_torch():
     """A host program without torch: table words, position tables, workspace sizes, the block cache and its simulation."""
     code = """
