@@ -24,14 +24,16 @@
 //   V^T (rows = head dims as the A operand): lane (rr, c) takes piece rr of key rows 2c, 2c+1,
 //     2c+8, 2c+9 and pairs keys with byte permutes.
 // The query is scaled by a power of two to [1, 2) and split into three bf16 parts, so that the
-// accumulated fp32 weights are good to a few 2^-22; the weights of the V product are rounded to bf16.
-// Scores, sums, maxima and outputs are fp32.
+// accumulated fp32 weights are good to a few 2^-22; the weights of the V product are two bf16 parts (2^-16: with one
+// the output is off by 0.0023 of itself in the 2-norm, with two by 0.0017, its bf16 rounding alone; 64 requests of 4161
+// tokens take the same time, with 32 heads on one KV head 83 us instead of 78).  Scores, sums, maxima and
+// outputs are fp32.
 //
 // What bounds it: HBM.  64 requests of 4161 tokens, 32 heads on 8, read 1.09 GB in 179 us (5.6 TB/s with
 // the requests' shared documents in L2), 192 us with the joining kernel; the two stages that fit a warp (12
 // warps per SM, 196 KB in flight) leave it waiting for loads most of the time.  A KV head's wider group of
 // query heads is taken by neighbouring warps, eight heads each: one warp with up to 32 heads spilled registers and held one
-// CTA per SM (64 requests, 32 heads on one KV head: 177 us against 79).
+// CTA per SM (64 requests, 32 heads on one KV head: 177 us against 79 at the time).
 #include <climits>
 
 #include "common.cuh"
@@ -403,9 +405,14 @@ __global__ void __launch_bounds__(kWarps * 32, kOcc)
             pr[j] = p0;
             pr[j + 2] = p1;
         }
-        // P^T (keys x heads) to the B fragment
-        const uint32_t pb0 = movmatrix_t(pack_bf16(pr[0], pr[1]));
-        const uint32_t pb1 = movmatrix_t(pack_bf16(pr[2], pr[3]));
+        // P^T (keys x heads) to the B fragment, as bf16 and what that leaves
+        uint32_t pb[2][2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const uint32_t w = pack_bf16(pr[2 * y], pr[2 * y + 1]);
+            pb[0][y] = movmatrix_t(w);
+            pb[1][y] = movmatrix_t(pack_bf16(pr[2 * y] - bf16_lo(w), pr[2 * y + 1] - bf16_hi(w)));
+        }
         // ---- O^T [128][8 heads] += V^T P^T
         const uint32_t sv = st + kTileBytes + 2 * c * 128;
         const uint32_t x0 = (rr ^ (2 * c)) << 4, x1 = (rr ^ (2 * c + 1)) << 4;
@@ -427,7 +434,8 @@ __global__ void __launch_bounds__(kWarps * 32, kOcc)
             for (int x = 0; x < 4; ++x) {
                 const uint32_t a0 = __byte_perm(w0[x], w1[x], 0x5410), a1 = __byte_perm(w0[x], w1[x], 0x7632);
                 const uint32_t a2 = __byte_perm(w2[x], w3[x], 0x5410), a3 = __byte_perm(w2[x], w3[x], 0x7632);
-                mma_bf16(oacc[4 * m + x], a0, a1, a2, a3, pb0, pb1);
+                mma_bf16(oacc[4 * m + x], a0, a1, a2, a3, pb[0][0], pb[0][1]);
+                mma_bf16(oacc[4 * m + x], a0, a1, a2, a3, pb[1][0], pb[1][1]);
             }
         }
     }

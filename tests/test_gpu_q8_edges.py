@@ -263,3 +263,17 @@ def test_positions_at_the_ends_of_int(hq, q8, kind):
         check(c.decode(), ref, bound, f"decode at the last position, {hq} heads {kind}")
         check(c.prefill(), *c.reference(**PREFILL_U)[:2], f"prefill at the last position, {hq} heads {kind}")
     assert c.dev["status"].item() == 0
+
+
+# ---------------------------------------------------------------------------------------- precision
+@pytest.mark.parametrize("hq,hkv", [(8, 8), (32, 8), (32, 1), (25, 1)])
+def test_block_mass_decode_keeps_its_weights(hq, hkv):
+    """The bf16 pool's decode with block mass: weights as two bf16 parts (2^-16), so that the output's rounding is what
+    is left also where large values cancel."""
+    docs = [100, 333, 48, 5]
+    reqs = [([(0, 0), (1, 100), (2, 433)], 480, 1), ([(3, 0)], 4, 1), ([(1, 0), (1, 333)], 500, 1), ([(2, 7)], 30, 1)]
+    c = PoolCase(la.Cfg(hq, hkv), docs, reqs, seed=hq, q8=False).to()
+    ref, bound, mref, mbound = c.reference(u_qk=2.0 ** -22, u_p=2.0 ** -16)
+    m = torch.zeros(c.words.size, device="cuda")
+    check(c.decode(m), ref, bound, f"decode with mass, weights in two parts, {hq}/{hkv}")
+    check(m, mref, mbound, f"mass {hq}/{hkv}")
