@@ -572,10 +572,9 @@ int lazy_prefill_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const 
                      d_status);
     if (rc) return rc;
     if (!q_raw || !cu_q || !q_pos0 || !aligned(q_raw, 8) || !aligned(out, 16)) return LAZY_EINVAL;
-    if (max_words == 0 || !blocks)
-        // nothing can be visible: every output row is zero
-        return launch_rc(cudaMemsetAsync(out, 0, static_cast<size_t>(total_q) * p.a.hq * 128 * 2,
-                                         static_cast<cudaStream_t>(stream)));
+    p.a.cu_q = cu_q;
+    if (max_words == 0 || !blocks)   // nothing can be visible: every request's rows are zero
+        return launch_rc(launch_zero_prefill(p.a, static_cast<cudaStream_t>(stream)));
     const int64_t units = prefill_units(cfg, num_req, max_q);
     // rows of all units, and the query kernel's grid
     if (static_cast<int64_t>(max_q) * p.a.group > (int64_t(1) << 30) || units > (int64_t(1) << 22) || num_req > 65535)
@@ -588,7 +587,6 @@ int lazy_prefill_attn_q8(const lazy_attn_cfg *cfg, const uint16_t *q_raw, const 
     if (!workspace || ws_bytes < need) return LAZY_EWORKSPACE;
     if (!aligned(workspace, 16)) return LAZY_EINVAL;
     p.a.q_raw = q_raw;
-    p.a.cu_q = cu_q;
     p.a.q_pos0 = q_pos0;
     p.a.max_q = max_q;
     if (few) {

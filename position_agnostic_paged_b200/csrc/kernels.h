@@ -178,6 +178,8 @@ struct Q8PrefillPlan {
     int nsplit, parts;
 };
 size_t q8_prefill_ws_bytes(int64_t units, int max_words, int sms);
+// Zeros for the requests' rows, where no key can be visible.
+cudaError_t launch_zero_prefill(const AttnParams &p, cudaStream_t s);
 cudaError_t launch_prefill_q8(Q8PrefillParams &p, void *workspace, int64_t units, int sms, cudaStream_t s);
 
 struct EvictParams {

@@ -819,6 +819,14 @@ __global__ void __launch_bounds__(256) prefill_q8_query_kernel(const __grid_cons
     }
 }
 
+// Zeros for the rows of all requests (one after the other from the first one's), and for no others.
+constexpr int kZeroCtas = 148;
+__global__ void __launch_bounds__(256) zero_prefill_kernel(const __grid_constant__ AttnParams p) {
+    const int64_t per = static_cast<int64_t>(p.hq) * (kHeadDim / 8), end = p.cu_q[p.num_req] * per;
+    uint4 *out = reinterpret_cast<uint4 *>(p.out);
+    for (int64_t i = p.cu_q[0] * per + blockIdx.x * 256 + threadIdx.x; i < end; i += kZeroCtas * 256) out[i] = make_uint4(0, 0, 0, 0);
+}
+
 constexpr int kQuerySplit = 512;   // CTAs of the query kernel up to which it takes a CTA per KV head
 
 template <bool ALIBI, int TILES>
@@ -858,6 +866,11 @@ size_t q8_prefill_ws_bytes(int64_t units, int max_words, int sms) {
     const Q8PrefillPlan pl = q8_prefill_plan(units, max_words, sms);
     return static_cast<size_t>(units) * kRows * (kHeadDim * 2 + 4) +
            static_cast<size_t>(pl.nsplit) * pl.parts * (pl.nsplit ? kRows * (kHeadDim + 2) * 4 : 0);
+}
+
+cudaError_t launch_zero_prefill(const AttnParams &p, cudaStream_t s) {
+    zero_prefill_kernel<<<kZeroCtas, 256, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_prefill_q8(Q8PrefillParams &p, void *workspace, int64_t units, int sms, cudaStream_t s) {

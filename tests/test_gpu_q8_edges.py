@@ -277,3 +277,16 @@ def test_block_mass_decode_keeps_its_weights(hq, hkv):
     m = torch.zeros(c.words.size, device="cuda")
     check(c.decode(m), ref, bound, f"decode with mass, weights in two parts, {hq}/{hkv}")
     check(m, mref, mbound, f"mass {hq}/{hkv}")
+
+
+# ----------------------------------------------------------------------------- what a call leaves alone
+@pytest.mark.parametrize("blocks,max_words", [(0, 3), (2, 0)])
+@pytest.mark.parametrize("most", [1, 40])
+def test_prefill_without_keys_leaves_other_rows(blocks, max_words, most):
+    """No blocks, or no words: zeros for the requests' rows, and nothing for the rows before and behind them."""
+    i = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")                      # noqa: E731
+    q = torch.randn(100, 8, D, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 5.0)
+    la.prefill_attn_q8(la.Cfg(8, 2), q, i(3, 4, 4, 4 + most), i(0, 0, 0), most, i(0, 0, 0), i(0, 0, 0, 0), max_words,
+                       la.Q8Pool.empty(blocks, 2), out, None)
+    assert (out[3:4 + most] == 0).all() and (out[:3] == 5).all() and (out[4 + most:] == 5).all()
