@@ -167,7 +167,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_q8_kernel(const __grid_co
     const int q0 = p.cu_q[r];
     const int T = p.cu_q[r + 1] - q0;
     const int R0 = mt * kRows;
-    if (R0 >= T * G) return;   // uniform: no rows
+    if (R0 >= T * G) {   // uniform: no rows
+        pdl_wait();      // (what follows on the stream waits for this kernel, and so for the query kernel, in every case)
+        return;
+    }
     const int wbase = p.table_indptr[r];
     const int n_all = p.table_indptr[r + 1] - wbase, n_words = min(n_all, p.max_words);
     int wbeg = 0, wend = n_words;

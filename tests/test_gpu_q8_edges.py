@@ -290,3 +290,68 @@ def test_prefill_without_keys_leaves_other_rows(blocks, max_words, most):
     la.prefill_attn_q8(la.Cfg(8, 2), q, i(3, 4, 4, 4 + most), i(0, 0, 0), most, i(0, 0, 0), i(0, 0, 0, 0), max_words,
                        la.Q8Pool.empty(blocks, 2), out, None)
     assert (out[3:4 + most] == 0).all() and (out[:3] == 5).all() and (out[4 + most:] == 5).all()
+
+
+@pytest.mark.parametrize("most", [3, 12, 200])
+def test_prefill_of_requests_without_tokens(most):
+    """Row pointers that give no request a token, for every size of max_q, and inputs overwritten right behind the call."""
+    docs = [100]
+    c = PoolCase(la.Cfg(8, 2), docs, [([(0, 0)], 90, 2), ([(0, 5)], 90, 2)], seed=1).to()
+    d = c.dev
+    out = torch.full_like(d["q"], 5.0)
+    ws = c.ws(la.prefill_q8_workspace_bytes(c.cfg, 2, 4, most, c.max_words, c.words.size))
+    for _ in range(50):
+        cu = torch.full((3,), 2, dtype=torch.int32, device="cuda")
+        la.prefill_attn_q8(c.cfg, d["q"], cu, d["pos0"], most, d["table"], d["indptr"], c.max_words, c.pool, out, ws, d["status"])
+        cu.copy_(torch.tensor([0, 2, 4], dtype=torch.int32), non_blocking=True)
+    assert (out == 5).all() and d["status"].item() == 0
+
+
+def _guarded(n):
+    """A workspace of exactly n bytes, and the bytes behind it (1 MiB, so that nothing can land outside)."""
+    buf = torch.full((n + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    return buf[:n], buf[n:]
+
+
+@pytest.mark.parametrize("reqs,doc,tokens", [(1, 2000, 1), (1, 2000, 4), (1, 2000, 300), (3, 700, 5), (40, 90, 12), (300, 20, 1), (5, 3, 2)])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (32, 1), (5, 5)])
+def test_workspaces_are_not_left(hq, hkv, reqs, doc, tokens):
+    """Calls with exactly the workspace that they ask for write nothing behind it."""
+    c = PoolCase(la.Cfg(hq, hkv), [doc, 37], [([(0, 0), (1, doc)], doc + 30, tokens)] * reqs, seed=doc).to()
+    n, mw, d = reqs, c.max_words, c.dev
+    guards = []
+    if tokens == 1:
+        for mass in (None, torch.zeros(c.words.size, device="cuda")):
+            ws, g = _guarded(la.decode_q8_workspace_bytes(c.cfg, n, mw, mass is not None))
+            c.decode(mass, ws=ws)
+            guards.append(g)
+        k = torch.randn(c.num_blocks, hkv, BLK, D, device="cuda").to(torch.bfloat16)
+        ws, g = _guarded(la.decode_mass_workspace_bytes(c.cfg, n, mw))
+        la.decode_attn_mass(c.cfg, d["q"], d["pos0"], d["table"], d["indptr"], mw, d["meta"], k, k, torch.empty_like(d["q"]),
+                            mass, ws, d["status"])
+        guards.append(g)
+    ws, g = _guarded(la.prefill_q8_workspace_bytes(c.cfg, n, d["q"].shape[0], tokens, mw, c.words.size))
+    c.prefill(ws=ws)
+    guards.append(g)
+    m = 1025 + doc
+    ws, g = _guarded(la.kv_write_q8_workspace_bytes(c.cfg, m, m // BLK + 1))
+    kv, at = torch.randn(m, hkv, D, device="cuda").to(torch.bfloat16), torch.arange(m, dtype=torch.int32, device="cuda")
+    la.kv_write_q8(c.cfg, kv, kv, at, at, la.Q8Pool.empty(m // BLK + 1, hkv), ws, d["status"])
+    guards.append(g)
+    assert d["status"].item() == 0
+    assert all((g == 0xA5).all() for g in guards)
+
+
+@pytest.mark.parametrize("tokens", [2, 9, 70])
+def test_prefill_of_requests_longer_than_max_words(tokens):
+    """Words past max_words are ignored and reported, with few rows, one and two row tiles."""
+    segs = [(0, 0), (1, 200)]
+    c = PoolCase(la.Cfg(8, 2), [200, 150], [(segs, 349 - r, tokens) for r in range(3)], seed=tokens).to()
+    d, mw = c.dev, 15                                              # of 13 + 10 words
+    out = torch.full_like(d["q"], 7.0)
+    ws = c.ws(la.prefill_q8_workspace_bytes(c.cfg, 3, out.shape[0], tokens, mw, c.words.size))
+    la.prefill_attn_q8(c.cfg, d["q"], d["cu"], d["pos0"], tokens, d["table"], d["indptr"], mw, c.pool, out, ws, d["status"])
+    assert d["status"].item() == la.DSTATUS_BAD_TABLE
+    keep = np.concatenate([np.arange(i, i + mw) for i in c.indptr[:-1]])
+    c.words, c.indptr = c.words[keep], [mw * r for r in range(4)]
+    check(out, *c.reference(**PREFILL_U)[:2], f"prefill of {tokens} tokens, words past max_words")
