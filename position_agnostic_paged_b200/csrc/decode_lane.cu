@@ -29,8 +29,8 @@
 // tokens take the same time, with 32 heads on one KV head 83 us instead of 78).  Scores, sums, maxima and
 // outputs are fp32.
 //
-// What bounds it: HBM.  64 requests of 4161 tokens, 32 heads on 8, read 1.09 GB in 179 us (5.6 TB/s with
-// the requests' shared documents in L2), 192 us with the joining kernel; the two stages that fit a warp (12
+// What bounds it: HBM.  64 requests of 4161 tokens, 32 heads on 8, read 1.09 GB in 182 us from cold
+// caches (6.0 TB/s), 193 us a call with the joining kernel; the two stages that fit a warp (12
 // warps per SM, 196 KB in flight) leave it waiting for loads most of the time.  A KV head's wider group of
 // query heads is taken by neighbouring warps, eight heads each: one warp with up to 32 heads spilled registers and held one
 // CTA per SM (64 requests, 32 heads on one KV head: 177 us against 79 at the time).

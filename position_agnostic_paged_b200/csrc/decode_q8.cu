@@ -9,10 +9,11 @@
 // rotated query or a weight x <= 448, becomes a sum of e4m3 parts with steps of 2^-4 (e4m3 rounds to 2^-4 of
 // a value, so 2^4 times the rest is at most 256):
 //   x = x_0 + 2^-4 x_1 + 2^-8 x_2,   x_0 = e4m3(x), x_1 = e4m3(2^4 (x - x_0)), x_2 = e4m3(2^4 (...)):
-// three parts (the query) are off by 2^-5 at most, 2^-12 of 128 (f16 would keep 2^-11); four (the weights)
-// reach down to 2^-21.  Each
+// three parts (the query, its largest element at least 128) are off by 2^-6 at most, 2^-13 of 128 (f16 would keep
+// 2^-11); four (the weights) by 2^-11, and reach down to 2^-21.  Each
 // part is a row group of the B operand with accumulator columns of its own; the sum is taken in fp32
-// when they are read.  With block mass the query has five parts (2^-13).
+// when they are read.  With block mass, whose fp32 sums are the result, the query has five parts (2^-16, fp32's own
+// rounding of such numbers).
 //
 //   S^T [128 keys][parts x heads] = K [128 keys][128] Q^T      A: the K codes of 8 words as they lie in the pool
 //   O^T [128 dims][parts x heads] += V^T [128 dims][keys] P^T  A: the V codes, keys as rows (MN-major)
@@ -26,20 +27,20 @@
 // on to the next piece or the next request.  A second kernel joins a request's partials in order.
 //
 // A CTA takes up to 16 query rows of a KV head; a wider group of heads is taken by neighbouring CTAs, two per
-// SM, whose barriers and waits overlap (32 heads on one KV head with block mass: one CTA of 32 rows 136 us, two
-// of 16 131).  A prefill of a few tokens runs here too, its rows (token, head) pairs: 128 keys cost a CTA of the
+// SM, whose barriers and waits overlap (32 heads on one KV head with block mass, with the operand's rows as they were
+// before kKeyRows: one CTA of 32 rows 136 us, two of 16 131).  A prefill of a few tokens runs here too, its rows (token, head) pairs: 128 keys cost a CTA of the
 // prefill's kernel about 3 us however few its rows, here under 2.
 //
 // Warps: four per group of 8 query rows (or 4) for the softmax (thread t of a group: key t of the tile, later
 // head dim t), one for the table walk and the TMA loads, one for MMA issue.  A tile is up to 8 words of one
 // request with one offset; K and V of a tile (32 KiB) share a stage.  Scores are double-buffered; QK of tile
 // i + 1 runs under the weights of tile i.  (Making tile i + 1's query before the scores of tile i, to run QK
-// under all of it: 107 -> 111 us, 131 -> 137.)
+// under all of it: 107 -> 111 us; with block mass and 32 heads, before kKeyRows, 131 -> 137.)
 //
 // What bounds it: HBM for long tables with few rows (64 requests of 4161 tokens, 32 heads on 8: 548 MB in 106 us
 // with the joining kernel, 5.2 TB/s, 79 % of the copy rate), the chain of a tile (scores, references, weights'
 // parts, about 1900 cycles with 4 rows) and its instructions where rows are many (32 heads with block mass:
-// 120 us, 57 % of issue slots).
+// 118 us, 56 % of issue slots).
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -87,7 +88,8 @@ struct Cfg {
     static constexpr int kQRows = QP * NG, kQN = (kQRows + 15) / 16 * 16;    // rows of the Q operand, N of the S product
     static constexpr int kPRows = kPP * NG, kPN = (kPRows + 15) / 16 * 16;
     // The P operand: keys as rows of kPN bytes (MN-major), which a thread writes eight heads at a time; with 4
-    // heads too narrow for that, rows of 128 keys (K-major), a byte per store (which cost 16 heads 131 us for 117)
+    // heads too narrow for that, rows of 128 keys (K-major), a byte per store (32 heads on one KV head with block mass: 131 us
+    // with it, 117 without)
     static constexpr bool kKeyRows = NG >= 8;
     static constexpr int kQBytes = (kQN + 7) / 8 * 1024, kPBytes = (kPN + 7) / 8 * 1024;
     static constexpr int kFixed = 2 * kQBytes + 2 * kPBytes + 4096 + 1024;   // buffers, small state, alignment

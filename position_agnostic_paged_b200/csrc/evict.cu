@@ -11,7 +11,7 @@
 // words move 2.5 MB (0.4 us at the copy rate) in 15 us, most of it the four passes' barriers and the atomics
 // of the histograms; one CTA per request took 48 us for them.  About 16 clusters of such CTAs run at once, so
 // that many requests are better off with a CTA each (64 of 8192 words: 15 us, in clusters
-// 48; but 32 of 32768: 48 us, in clusters 39).
+// 48; but 32 of 32768: 48 us, in clusters 39 to 45).
 #include <cooperative_groups.h>
 
 #include "common.cuh"

@@ -31,8 +31,8 @@
 // halves), then O0, O1 of 128 columns.
 //
 // What bounds it: shared memory's data pipe, which the tensor cores' operands take half of and the conversions
-// with their stores about a third: 16 requests of 256 tokens over 4161, 32 heads on 8, 352 GFLOP in 383 us alone
-// (0.92 PFLOP/s), 452 us in a row of calls.
+// with their stores about a third: 16 requests of 256 tokens over 4161, 32 heads on 8, 352 GFLOP in 385 us alone
+// (0.91 PFLOP/s), 407 us in a graph, 445 to 458 us in a row of calls.
 #include <cuda_fp16.h>
 
 #include <algorithm>

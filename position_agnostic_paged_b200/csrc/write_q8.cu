@@ -16,8 +16,11 @@
 // pair, times a table of the 16 slots' (one per call), shared by the heads.  A warp takes every fourth
 // head; its rows come by bulk copies into shared memory, values while keys are worked on and the next
 // head's keys while values are.  Loops over rows stay rolled: unrolled, the code missed the instruction
-// cache (32768 tokens x 8 heads: 118 us, now 79; 202 MB, 2.5 TB/s).  Bound by instructions: 36.8 M of them,
-// half the issue slots, a third each for angles and rotation, scales, and codes with their error intervals.
+// cache (32768 tokens x 8 heads: 118 us, now 79; 202 MB, 2.5 TB/s).  37.2 M instructions take half the
+// issue slots, a third each for angles and rotation, scales, and codes with their error intervals; the rest are waits that
+// 28 % occupancy does not hide (loads, two barriers and 64 fp64 angles per block ahead of its rows).  Ownership by the
+// first token puts up to 16 blocks into one CTA where the call's tokens are not in slot order: 20000 tokens 64 us in
+// order, 215 permuted.
 // Half a warp per token row, 8 elements per lane.  Rotations run in fp32.  Where a code or a scale could
 // depend on the rotation's rounding (the error interval holds a rounding border: some elements in 10^5) it is
 // computed again in fp64.  A code is e4m3_rne(float_rne(x / s)): the quotient is rounded to fp32 first, here as there.
