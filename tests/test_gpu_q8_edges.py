@@ -355,3 +355,19 @@ def test_prefill_of_requests_longer_than_max_words(tokens):
     keep = np.concatenate([np.arange(i, i + mw) for i in c.indptr[:-1]])
     c.words, c.indptr = c.words[keep], [mw * r for r in range(4)]
     check(out, *c.reference(**PREFILL_U)[:2], f"prefill of {tokens} tokens, words past max_words")
+
+
+@pytest.mark.parametrize("n", [30, 1200])
+def test_write_of_a_call_that_contradicts_itself(n):
+    """Tokens of one block with local indices from different blocks: each key is turned by its own, the metadata word is
+    the largest."""
+    rng = np.random.default_rng(n)
+    nb = n // BLK + 2
+    st = _state(nb, 3, n, [7] * nb)
+    slot = rng.permutation(nb * BLK)[:n]
+    j = slot % BLK + BLK * rng.integers(0, 2000, n)
+    k, v = bf16(rng.standard_normal((n, 3, D))), bf16(rng.standard_normal((n, 3, D)))
+    cfg = la.Cfg(3, 3)
+    pool = _device_pool(st)
+    assert _write(cfg, pool, k, v, slot, j) == 0
+    _same_pool(pool, write_reference(cfg, st, k, v, slot, j))
